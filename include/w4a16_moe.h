@@ -18,6 +18,12 @@
  *   w4a16_moe_contiguous_forward / w4a16_moe_masked_forward
  *                       the layer on expert-grouped activation layouts
  *   w4a16_repack        once at weight load: canonical int4 + scales -> kernel layout
+ *   moe_permute / moe_unpermute and their _backward
+ *                       token rows into moe_align's order and back, with gradients
+ *   mxfp4_quantize / mxfp4_silu_mul_quantize / mxfp4_dequantize
+ *                       rows to 4-bit floating point with a scale per 32 values, and back
+ *   mxfp4_repack / mxfp4_moe_gemm
+ *                       the experts' product on such operands
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -412,6 +418,154 @@ size_t w4a16_moe_masked_workspace_bytes(const w4a16_moe_shape* shape, int32_t ma
 int w4a16_moe_masked_forward(const w4a16_moe_shape* shape, const uint16_t* x, int32_t max_m,
                              const int32_t* masked_m, int32_t block_m, const void* w13_packed, const void* w2_packed,
                              uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rows sorted by expert and back                                            */
+/* ------------------------------------------------------------------------ */
+
+/* Element type of a row buffer. */
+typedef enum { W4A16_BF16 = 0, W4A16_FP16 = 1, W4A16_FP32 = 2 } w4a16_dtype;
+
+/* Token rows into the aligned order of moe_align: the step in front of the
+ * grouped layouts (with block_m 128 and all experts' rows it makes the x of
+ * w4a16_moe_contiguous_forward) and of mxfp4_moe_gemm, which need each expert's
+ * rows side by side.
+ *   xp[p, :] = x[sorted_token_ids[p] / topk, :]   for real rows p,
+ *   xp[p, :] = 0                                  for padding rows p < num_tokens_post_padded,
+ * and the rows from num_tokens_post_padded on are left as they were.
+ *
+ *   x                 device [T, hidden] of `dtype`, contiguous; any hidden >= 1
+ *   sorted_token_ids, capacity, num_tokens_post_padded
+ *                     moe_align's outputs (also of moe_align_filtered), or the first
+ *                     `capacity` entries of them where the caller knows that no row
+ *                     lies behind; rows >= capacity are not touched
+ *   xp                device [capacity, hidden] of `dtype`
+ *   slot_rows         device int32 [T, topk], written: the row p of each slot, -1
+ *                     where the slot has no row (expert not resident)
+ * A row of 16-byte multiples in 16-byte aligned buffers moves 16 bytes at a
+ * time, any other element by element; the buffers need only their element
+ * type's alignment. Deterministic: the result does not depend on the order in
+ * which rows are written. */
+int moe_permute(const void* x, int32_t dtype, int32_t T, int32_t topk, int32_t hidden,
+                const int32_t* sorted_token_ids, int32_t capacity, const int32_t* num_tokens_post_padded, void* xp,
+                int32_t* slot_rows, void* stream);
+
+/* Gradient of moe_permute: dx[t, :] = sum_j dxp[slot_rows[t, j], :] over the
+ * slots that have a row, summed in fp32 in j order and rounded once to `dtype`;
+ * zero for a token without one.
+ *   dxp               device [rows, hidden] of `dtype`
+ *   slot_rows         device int32 [T, topk] as written by moe_permute; an entry
+ *                     outside [0, rows) counts as no row
+ *   dx                device [T, hidden] of `dtype`, every row written */
+int moe_permute_backward(const void* dxp, int32_t dtype, int32_t rows, int32_t T, int32_t topk, int32_t hidden,
+                         const int32_t* slot_rows, void* dx, void* stream);
+
+/* Rows in the aligned order back to their tokens, weighted:
+ *   out[t, :] = sum_j topk_weights[t, j] * y[slot_rows[t, j], :]
+ * over the slots that have a row, in fp32 in j order, rounded once; zero for a
+ * token without one. The weight of a slot without a row is not read.
+ *   y                 device [rows, hidden] of y_dtype
+ *   topk_weights      device fp32 [T, topk], or NULL for weights of 1
+ *   slot_rows         as for moe_permute_backward
+ *   out               device [T, hidden] of out_dtype, every row written; out_dtype is
+ *                     y_dtype, or any type where y_dtype is fp32 (else
+ *                     W4A16_ERR_UNSUPPORTED) */
+int moe_unpermute(const void* y, int32_t y_dtype, int32_t rows, int32_t T, int32_t topk, int32_t hidden,
+                  const int32_t* slot_rows, const float* topk_weights, void* out, int32_t out_dtype, void* stream);
+
+/* Gradients of moe_unpermute:
+ *   dy[p, :]  = topk_weights[s] * dout[s / topk, :]  for real rows p, s = sorted_token_ids[p],
+ *   dy[p, :]  = 0 for padding rows p < num_tokens_post_padded; later rows are left as they were,
+ *   dweights[t, j] = <dout[t, :], y[slot_rows[t, j], :]> in fp32, 0 for a slot without a row.
+ *   dout              device [T, hidden] of out_dtype (types as in moe_unpermute)
+ *   y                 device [rows, hidden] of y_dtype, as given to moe_unpermute; may be
+ *                     NULL where dweights is
+ *   slot_rows, sorted_token_ids, capacity, num_tokens_post_padded
+ *                     as for moe_permute, of one and the same routing
+ *   rows              rows of y and dy; >= capacity (else W4A16_ERR_CAPACITY)
+ *   topk_weights      as for moe_unpermute
+ *   dy                device [rows, hidden] of y_dtype, or NULL
+ *   dweights          device fp32 [T, topk], or NULL; one of the two is given
+ * dy must not overlap y or dout. The products' sums have a fixed order: runs
+ * on the same inputs give the same bits. */
+int moe_unpermute_backward(const void* dout, int32_t out_dtype, const void* y, int32_t y_dtype, int32_t rows,
+                           int32_t T, int32_t topk, int32_t hidden, const int32_t* slot_rows,
+                           const float* topk_weights, const int32_t* sorted_token_ids, int32_t capacity,
+                           const int32_t* num_tokens_post_padded, void* dy, float* dweights, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Microscaled 4-bit floating point (MXFP4)                                  */
+/* ------------------------------------------------------------------------ */
+
+/* The format: 32 consecutive values of a row share one scale byte s, which
+ * stands for 2^(s - 127) (255: NaN, and then all 32 values are NaN); a value is
+ * a 4-bit code (sign, two exponent bits, one mantissa bit) of magnitude 0, 0.5,
+ * 1, 1.5, 2, 3, 4 or 6 times that scale. Codes are two to a byte, the even
+ * element in the low half; code bytes are [rows, K / 2], scale bytes [rows, K / 32].
+ *
+ * Quantisation of a block with largest magnitude m: the scale is
+ * 2^(floor(log2 m) - 2), at least 2^-127, so that m lands in [4, 8); each value
+ * is divided by it (exactly) and rounded to the nearest magnitude, ties to the
+ * even code, those above 6 to 6. The sign of what rounds to zero is kept. A
+ * block of zeros gets s = 0; a block that holds an infinity or a NaN gets
+ * s = 255 with codes 0, so that no such value is lost in silence.
+ *
+ *   x                 device [rows, K] of `dtype`, contiguous
+ *   K                 a multiple of 32 (else W4A16_ERR_UNSUPPORTED)
+ *   num_rows          device int32 [1] or NULL: rows from *num_rows on are neither
+ *                     read nor written (num_tokens_post_padded of aligned rows)
+ *   q, s              device uint8 [rows, K / 2] and [rows, K / 32]
+ * x must be 16-byte aligned and q 4-byte aligned. */
+int mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const int32_t* num_rows, uint8_t* q,
+                   uint8_t* s, void* stream);
+
+/* The activation between the expert layer's two products, to 4 bits:
+ * a = silu(gu[r, c]) * gu[r, I + c] in fp32, c in [0, I), quantised as above
+ * (one rounding: a is not rounded to another type in between).
+ *   gu                device [rows, 2 I] of `dtype`; I a multiple of 32
+ *   q, s              device uint8 [rows, I / 2] and [rows, I / 32] */
+int mxfp4_silu_mul_quantize(const void* gu, int32_t dtype, int32_t rows, int32_t I, const int32_t* num_rows,
+                            uint8_t* q, uint8_t* s, void* stream);
+
+/* The values that codes and scales stand for, rounded once to `dtype` (exact
+ * in bf16 and fp32; fp16 overflows to infinity and rounds below 2^-24).
+ *   out               device [rows, K] of `dtype`, 16-byte aligned; q 4-byte aligned */
+int mxfp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K, const int32_t* num_rows, void* out,
+                     int32_t dtype, void* stream);
+
+/* Bytes of the packed weight buffer of num_experts matrices [N, K]: the codes
+ * and scale bytes with N rounded up to 64 and K to 128. N a multiple of 16, K a
+ * multiple of 32, both at most 2^20 (else W4A16_ERR_UNSUPPORTED). */
+int mxfp4_packed_bytes(int32_t num_experts, int32_t N, int32_t K, size_t* bytes);
+
+/* Canonical weights (w_q uint8 [E, N, K / 2], w_s uint8 [E, N, K / 32], as
+ * mxfp4_quantize writes them for [E * N, K] rows) into the layout that
+ * mxfp4_moe_gemm reads, once at load. The layout is private to the library. */
+int mxfp4_repack(int32_t num_experts, int32_t N, int32_t K, const uint8_t* w_q, const uint8_t* w_s, void* packed,
+                 void* stream);
+
+/* The experts' product: for every aligned row p < num_tokens_post_padded whose
+ * slot sorted_token_ids[p] is real, with e the expert of its block,
+ *   out[p, n] = sum_k A[r, k] * W[e, n, k],   r = sorted_token_ids[p] / topk with gather, else p,
+ * on the matrix cores' 4-bit operands: products exact, sums in fp32, one rounding to
+ * out_dtype. Padding rows p < num_tokens_post_padded (and rows of a block whose
+ * expert id lies outside [0, num_experts)) are written as zeros; later rows are
+ * left as they were. A scale byte of 255 makes NaN of the outputs it enters.
+ *
+ *   num_experts, N, K the packed weights' (see mxfp4_packed_bytes)
+ *   a_q, a_s          device uint8 [a_rows, K / 2] and [a_rows, K / 32]; with gather
+ *                     a_rows >= T (token rows, read through sorted_token_ids: gate_up),
+ *                     without a_rows >= capacity (aligned rows: down); else W4A16_ERR_INVALID_ARG
+ *   T, topk           tokens and slots per token of the alignment
+ *   sorted_token_ids, capacity, expert_ids, num_tokens_post_padded, block_m
+ *                     moe_align's outputs and block size
+ *   out               device [capacity, N] of out_dtype
+ * a_q, packed and out must be 16-byte aligned. No workspace; sums have a fixed
+ * order, so runs on the same inputs give the same bits. */
+int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q, const uint8_t* a_s, int32_t a_rows,
+                   int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids, int32_t capacity,
+                   const int32_t* expert_ids, const int32_t* num_tokens_post_padded, int32_t block_m,
+                   const void* packed, void* out, int32_t out_dtype, void* stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,9 @@ __all__ = [
     "w4a16_moe_stage_workspace_bytes", "w4a16_moe_prepare_x", "w4a16_moe_prepare_h",
     "w4a16_moe_workspace_bytes", "w4a16_moe_forward", "w4a16_moe_gate_up", "w4a16_moe_down",
     "w4a16_moe_combine", "align_buffers",
+    "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
+    "mxfp4_quantize", "mxfp4_silu_mul_quantize", "mxfp4_dequantize", "mxfp4_packed_bytes", "mxfp4_repack",
+    "mxfp4_moe_gemm",
 ]
 
 OK = 0
@@ -231,6 +234,230 @@ def w4a16_moe_combine(shape: Shape, topk_ids, topk_weights, y, out, stream=None)
     T, topk = topk_ids.shape
     _check(load().w4a16_moe_combine(ctypes.byref(shape), T, topk, _p(topk_ids), _p(topk_weights), _p(y), _p(out),
                                     _stream(stream)), "w4a16_moe_combine")
+
+
+# ---------------------------------------------------------------------------
+# Rows sorted by expert and back; 4-bit floating point. These take torch's own
+# bfloat16, float16 and float32 tensors (int16 and uint16 count as bf16 bits, as
+# everywhere in this package) and refuse, with the status the C ABI would give,
+# what a pointer alone cannot show: another device than the current one, strides
+# that are not the contiguous ones, a type or shape that does not fit.
+# ---------------------------------------------------------------------------
+
+INVALID_ARG, UNSUPPORTED, CAPACITY = 1, 2, 3
+_codes = {}  # torch dtype -> w4a16_dtype
+
+
+def _refuse(where: str, what: str, status: int = INVALID_ARG):
+    raise W4A16Error(status, f"{where}: {what}")
+
+
+def _dtype(t, where: str) -> int:
+    if not _codes:
+        import torch
+
+        _codes.update({torch.bfloat16: 0, torch.int16: 0, torch.uint16: 0, torch.float16: 1, torch.float32: 2,
+                       torch.int32: None, torch.uint8: None})
+    code = _codes.get(t.dtype)
+    if code is None:
+        _refuse(where, f"{t.dtype} rows", UNSUPPORTED)
+    return code
+
+
+def _launch(fn, where: str, args, tensors, stream):
+    """Check that every tensor is contiguous and on the current device, then call the C ABI on the stream."""
+    import torch
+
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None:
+            if t.get_device() != here:
+                _refuse(where, f"a tensor is on {t.device}, not on the current GPU")
+            if not t.is_contiguous():
+                _refuse(where, "a tensor is not contiguous")
+    raw = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    status = fn(*args, raw)
+    if status != OK:
+        raise W4A16Error(status, where)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _int32(where: str, *tensors):
+    import torch
+
+    for t in tensors:
+        if t is not None and t.dtype is not torch.int32:
+            _refuse(where, "indexes and counts are int32")
+
+
+def _fp32(where: str, *tensors):
+    import torch
+
+    for t in tensors:
+        if t is not None and t.dtype is not torch.float32:
+            _refuse(where, "weights are float32")
+
+
+def moe_permute(x, sorted_token_ids, num_tokens_post_padded, topk: int, xp, slot_rows, stream=None):
+    name = "moe_permute"
+    T, H = x.shape
+    capacity = sorted_token_ids.numel()
+    if slot_rows.shape != (T, topk):
+        _refuse(name, "slot_rows is not [T, topk]")
+    rows, width = xp.shape
+    if width != H or xp.dtype is not x.dtype:
+        _refuse(name, "xp is not [rows, hidden] of x's type")
+    if rows < capacity:
+        _refuse(name, "xp has fewer rows than sorted_token_ids", CAPACITY)
+    _int32(name, sorted_token_ids, num_tokens_post_padded, slot_rows)
+    _launch(load().moe_permute, name,
+            (x.data_ptr(), _dtype(x, name), T, topk, H, sorted_token_ids.data_ptr(), capacity,
+             num_tokens_post_padded.data_ptr(), xp.data_ptr(), slot_rows.data_ptr()),
+            (x, sorted_token_ids, num_tokens_post_padded, xp, slot_rows), stream)
+
+
+def moe_permute_backward(dxp, slot_rows, dx, stream=None):
+    name = "moe_permute_backward"
+    rows, H = dxp.shape
+    T, topk = slot_rows.shape
+    if dx.shape != (T, H) or dx.dtype is not dxp.dtype:
+        _refuse(name, "dx is not [T, hidden] of dxp's type")
+    _int32(name, slot_rows)
+    _launch(load().moe_permute_backward, name,
+            (dxp.data_ptr(), _dtype(dxp, name), rows, T, topk, H, slot_rows.data_ptr(), dx.data_ptr()),
+            (dxp, slot_rows, dx), stream)
+
+
+def moe_unpermute(y, slot_rows, out, topk_weights=None, stream=None):
+    name = "moe_unpermute"
+    rows, H = y.shape
+    T, topk = slot_rows.shape
+    if out.shape != (T, H):
+        _refuse(name, "out is not [T, hidden]")
+    if topk_weights is not None and topk_weights.shape != (T, topk):
+        _refuse(name, "topk_weights is not [T, topk]")
+    _int32(name, slot_rows)
+    _fp32(name, topk_weights)
+    _launch(load().moe_unpermute, name,
+            (y.data_ptr(), _dtype(y, name), rows, T, topk, H, slot_rows.data_ptr(), _ptr(topk_weights),
+             out.data_ptr(), _dtype(out, name)),
+            (y, slot_rows, topk_weights, out), stream)
+
+
+def moe_unpermute_backward(dout, y, slot_rows, topk_weights, sorted_token_ids, num_tokens_post_padded, dy, dweights,
+                           stream=None):
+    """dy or dweights may be None (not wanted), and y where dweights is; topk_weights None means weights of 1."""
+    name = "moe_unpermute_backward"
+    given = y if y is not None else dy
+    if given is None:
+        _refuse(name, "neither y nor dy")
+    rows, H = given.shape
+    T, topk = slot_rows.shape
+    if dout.shape != (T, H):
+        _refuse(name, "dout is not [T, hidden]")
+    if dy is not None and (dy.shape != given.shape or dy.dtype is not given.dtype):
+        _refuse(name, "dy is not like y")
+    if dy is not None and (sorted_token_ids is None or num_tokens_post_padded is None):
+        _refuse(name, "dy needs sorted_token_ids and num_tokens_post_padded")
+    if dweights is not None and (y is None or dweights.shape != (T, topk)):
+        _refuse(name, "dweights is not [T, topk], or y is missing")
+    if topk_weights is not None and topk_weights.shape != (T, topk):
+        _refuse(name, "topk_weights is not [T, topk]")
+    _int32(name, slot_rows, sorted_token_ids, num_tokens_post_padded)
+    _fp32(name, topk_weights, dweights)
+    capacity = 0 if sorted_token_ids is None else sorted_token_ids.numel()
+    _launch(load().moe_unpermute_backward, name,
+            (dout.data_ptr(), _dtype(dout, name), _ptr(y), _dtype(given, name), rows, T, topk, H,
+             slot_rows.data_ptr(), _ptr(topk_weights), _ptr(sorted_token_ids), capacity,
+             _ptr(num_tokens_post_padded), _ptr(dy), _ptr(dweights)),
+            (dout, y, slot_rows, topk_weights, sorted_token_ids, num_tokens_post_padded, dy, dweights), stream)
+
+
+def _fp4_buffers(name: str, rows: int, K: int, q, s, num_rows):
+    import torch
+
+    if K % 32:
+        _refuse(name, "rows are not a multiple of 32 long", UNSUPPORTED)
+    if q.shape != (rows, K // 2) or s.shape != (rows, K // 32):
+        _refuse(name, "codes and scales are not [rows, K / 2] and [rows, K / 32]")
+    if q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
+        _refuse(name, "codes and scales are uint8")
+    _int32(name, num_rows)
+
+
+def mxfp4_quantize(x, q, s, num_rows=None, stream=None):
+    name = "mxfp4_quantize"
+    rows, K = x.shape
+    _fp4_buffers(name, rows, K, q, s, num_rows)
+    _launch(load().mxfp4_quantize, name,
+            (x.data_ptr(), _dtype(x, name), rows, K, _ptr(num_rows), q.data_ptr(), s.data_ptr()),
+            (x, q, s, num_rows), stream)
+
+
+def mxfp4_silu_mul_quantize(gu, q, s, num_rows=None, stream=None):
+    name = "mxfp4_silu_mul_quantize"
+    rows, two_i = gu.shape
+    if two_i % 2:
+        _refuse(name, "gu is not [rows, 2 I]")
+    _fp4_buffers(name, rows, two_i // 2, q, s, num_rows)
+    _launch(load().mxfp4_silu_mul_quantize, name,
+            (gu.data_ptr(), _dtype(gu, name), rows, two_i // 2, _ptr(num_rows), q.data_ptr(), s.data_ptr()),
+            (gu, q, s, num_rows), stream)
+
+
+def mxfp4_dequantize(q, s, out, num_rows=None, stream=None):
+    name = "mxfp4_dequantize"
+    rows, K = out.shape
+    _fp4_buffers(name, rows, K, q, s, num_rows)
+    _launch(load().mxfp4_dequantize, name,
+            (q.data_ptr(), s.data_ptr(), rows, K, _ptr(num_rows), out.data_ptr(), _dtype(out, name)),
+            (q, s, out, num_rows), stream)
+
+
+def mxfp4_packed_bytes(num_experts: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().mxfp4_packed_bytes(num_experts, N, K, ctypes.byref(n)), "mxfp4_packed_bytes")
+    return n.value
+
+
+def mxfp4_repack(w_q, w_s, packed, stream=None):
+    import torch
+
+    name = "mxfp4_repack"
+    E, N, half = w_q.shape
+    need = mxfp4_packed_bytes(E, N, 2 * half)
+    if w_s.shape != (E, N, half // 16) or w_q.dtype is not torch.uint8 or w_s.dtype is not torch.uint8:
+        _refuse(name, "w_q and w_s are not uint8 [E, N, K / 2] and [E, N, K / 32]")
+    if _nbytes(packed) < need:
+        _refuse(name, "packed is smaller than mxfp4_packed_bytes")
+    _launch(load().mxfp4_repack, name, (E, N, 2 * half, w_q.data_ptr(), w_s.data_ptr(), packed.data_ptr()),
+            (w_q, w_s, packed), stream)
+
+
+def mxfp4_moe_gemm(a_q, a_s, T: int, topk: int, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m: int,
+                   num_experts: int, packed, out, gather: bool = False, stream=None):
+    """gather: A holds token rows [T, K] (gate_up), read through sorted_token_ids; else aligned rows (down)."""
+    name = "mxfp4_moe_gemm"
+    rows, half = a_q.shape
+    out_rows, N = out.shape
+    K = 2 * half
+    capacity = sorted_token_ids.numel()
+    _fp4_buffers(name, rows, K, a_q, a_s, None)
+    if out_rows < capacity:
+        _refuse(name, "out has fewer rows than sorted_token_ids", CAPACITY)
+    if block_m > 0 and expert_ids.numel() < capacity // block_m:
+        _refuse(name, "expert_ids has too few blocks")
+    if _nbytes(packed) < mxfp4_packed_bytes(num_experts, N, K):
+        _refuse(name, "packed is smaller than mxfp4_packed_bytes")
+    _int32(name, sorted_token_ids, expert_ids, num_tokens_post_padded)
+    _launch(load().mxfp4_moe_gemm, name,
+            (num_experts, N, K, a_q.data_ptr(), a_s.data_ptr(), rows, 1 if gather else 0, T, topk,
+             sorted_token_ids.data_ptr(), capacity, expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), block_m,
+             packed.data_ptr(), out.data_ptr(), _dtype(out, name)),
+            (a_q, a_s, sorted_token_ids, expert_ids, num_tokens_post_padded, packed, out), stream)
 
 
 def align_buffers(T: int, topk: int, num_experts: int, block_m: int, device="cuda"):

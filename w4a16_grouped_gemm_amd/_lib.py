@@ -46,6 +46,16 @@ SIGNATURES = {
     "w4a16_moe_prepare_h": (ctypes.c_int, [P, I32, I32, P, P, I32, P, I32, P, SZ, P]),
     "w4a16_moe_down": (ctypes.c_int, [P, I32, I32, P, P, I32, P, P, I32, P, P, P, SZ, P]),
     "w4a16_moe_combine": (ctypes.c_int, [P, I32, I32, P, P, P, P, P]),
+    "moe_permute": (ctypes.c_int, [P, I32, I32, I32, I32, P, I32, P, P, P, P]),
+    "moe_permute_backward": (ctypes.c_int, [P, I32, I32, I32, I32, I32, P, P, P]),
+    "moe_unpermute": (ctypes.c_int, [P, I32, I32, I32, I32, I32, P, P, P, I32, P]),
+    "moe_unpermute_backward": (ctypes.c_int, [P, I32, P, I32, I32, I32, I32, I32, P, P, P, I32, P, P, P, P]),
+    "mxfp4_quantize": (ctypes.c_int, [P, I32, I32, I32, P, P, P, P]),
+    "mxfp4_silu_mul_quantize": (ctypes.c_int, [P, I32, I32, I32, P, P, P, P]),
+    "mxfp4_dequantize": (ctypes.c_int, [P, P, I32, I32, P, P, I32, P]),
+    "mxfp4_packed_bytes": (ctypes.c_int, [I32, I32, I32, ctypes.POINTER(SZ)]),
+    "mxfp4_repack": (ctypes.c_int, [I32, I32, I32, P, P, P, P]),
+    "mxfp4_moe_gemm": (ctypes.c_int, [I32, I32, I32, P, P, I32, I32, I32, I32, P, I32, P, P, I32, P, P, I32, P]),
 }
 
 

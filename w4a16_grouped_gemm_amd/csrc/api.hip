@@ -682,3 +682,174 @@ int w4a16_moe_routed_forward(const w4a16_moe_shape* shape, const uint16_t* x, in
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Rows sorted by expert and back; 4-bit floating point
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int32_t kMaxRow = 1 << 20;  // elements of a row
+
+bool dtype_ok(int32_t dtype) { return dtype == W4A16_BF16 || dtype == W4A16_FP16 || dtype == W4A16_FP32; }
+size_t dtype_size(int32_t dtype) { return dtype == W4A16_FP32 ? 4 : 2; }
+bool aligned_to(const void* p, size_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
+
+// T tokens of topk slots each, rows of `hidden` elements.
+int check_rows(int32_t T, int32_t topk, int32_t hidden, int32_t rows) {
+  if (T < 0 || topk < 1 || hidden < 1 || rows < 0) return W4A16_ERR_INVALID_ARG;
+  if (topk > W4A16_MAX_TOPK || hidden > kMaxRow) return W4A16_ERR_UNSUPPORTED;
+  if ((int64_t)T * topk > INT_MAX / 2 || rows > INT_MAX / 2) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+int check_unpermute_types(int32_t y_dtype, int32_t out_dtype) {
+  if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return W4A16_ERR_INVALID_ARG;
+  return y_dtype == out_dtype || y_dtype == W4A16_FP32 ? W4A16_OK : W4A16_ERR_UNSUPPORTED;
+}
+
+int check_fp4_rows(int32_t rows, int32_t K) {
+  if (rows < 0 || K < 1) return W4A16_ERR_INVALID_ARG;
+  if (K % 32 != 0 || K > kMaxRow) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+int check_fp4_weights(int32_t E, int32_t N, int32_t K) {
+  if (E < 1 || N < 1 || K < 1) return W4A16_ERR_INVALID_ARG;
+  if (E > W4A16_MAX_EXPERTS || N % 16 != 0 || K % 32 != 0 || N > kMaxRow || K > kMaxRow) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_permute(const void* x, int32_t dtype, int32_t T, int32_t topk, int32_t hidden,
+                const int32_t* sorted_token_ids, int32_t capacity, const int32_t* num_tokens_post_padded, void* xp,
+                int32_t* slot_rows, void* stream) {
+  if (!dtype_ok(dtype)) return W4A16_ERR_INVALID_ARG;
+  const int st = check_rows(T, topk, hidden, capacity);
+  if (st != W4A16_OK) return st;
+  if (T > 0 && (!x || !slot_rows || !num_tokens_post_padded)) return W4A16_ERR_INVALID_ARG;
+  if (T > 0 && capacity > 0 && (!sorted_token_ids || !xp)) return W4A16_ERR_INVALID_ARG;
+  if (!aligned_to(x, dtype_size(dtype)) || !aligned_to(xp, dtype_size(dtype))) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_permute(x, dtype, T, topk, hidden, sorted_token_ids, capacity, num_tokens_post_padded, xp,
+                                   slot_rows, static_cast<hipStream_t>(stream)));
+}
+
+int moe_permute_backward(const void* dxp, int32_t dtype, int32_t rows, int32_t T, int32_t topk, int32_t hidden,
+                         const int32_t* slot_rows, void* dx, void* stream) {
+  return moe_unpermute(dxp, dtype, rows, T, topk, hidden, slot_rows, nullptr, dx, dtype, stream);
+}
+
+int moe_unpermute(const void* y, int32_t y_dtype, int32_t rows, int32_t T, int32_t topk, int32_t hidden,
+                  const int32_t* slot_rows, const float* topk_weights, void* out, int32_t out_dtype, void* stream) {
+  int st = check_unpermute_types(y_dtype, out_dtype);
+  if (st != W4A16_OK) return st;
+  st = check_rows(T, topk, hidden, rows);
+  if (st != W4A16_OK) return st;
+  if (T > 0 && (!slot_rows || !out || (rows > 0 && !y))) return W4A16_ERR_INVALID_ARG;
+  if (!aligned_to(y, dtype_size(y_dtype)) || !aligned_to(out, dtype_size(out_dtype))) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_unpermute(y, y_dtype, rows, T, topk, hidden, slot_rows, topk_weights, out, out_dtype,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+int moe_unpermute_backward(const void* dout, int32_t out_dtype, const void* y, int32_t y_dtype, int32_t rows,
+                           int32_t T, int32_t topk, int32_t hidden, const int32_t* slot_rows,
+                           const float* topk_weights, const int32_t* sorted_token_ids, int32_t capacity,
+                           const int32_t* num_tokens_post_padded, void* dy, float* dweights, void* stream) {
+  int st = check_unpermute_types(y_dtype, out_dtype);
+  if (st != W4A16_OK) return st;
+  st = check_rows(T, topk, hidden, rows);
+  if (st != W4A16_OK) return st;
+  if (capacity < 0 || (!dy && !dweights)) return W4A16_ERR_INVALID_ARG;
+  if (T > 0 && (!dout || !slot_rows || (dweights && rows > 0 && !y))) return W4A16_ERR_INVALID_ARG;
+  if (dy && capacity > 0 && (!sorted_token_ids || !num_tokens_post_padded)) return W4A16_ERR_INVALID_ARG;
+  if (!aligned_to(y, dtype_size(y_dtype)) || !aligned_to(dy, dtype_size(y_dtype)) ||
+      !aligned_to(dout, dtype_size(out_dtype)))
+    return W4A16_ERR_INVALID_ARG;
+  if (rows < capacity) return W4A16_ERR_CAPACITY;
+  return hip_status(launch_unpermute_backward(dout, out_dtype, y, y_dtype, rows, T, topk, hidden, slot_rows,
+                                              topk_weights, sorted_token_ids, capacity, num_tokens_post_padded, dy,
+                                              dweights, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const int32_t* num_rows, uint8_t* q,
+                   uint8_t* s, void* stream) {
+  if (!dtype_ok(dtype)) return W4A16_ERR_INVALID_ARG;
+  const int st = check_fp4_rows(rows, K);
+  if (st != W4A16_OK) return st;
+  if (rows > 0 && (!x || !q || !s)) return W4A16_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned_to(q, 4)) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_fp4_quantize(x, dtype, rows, K, num_rows, q, s, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_silu_mul_quantize(const void* gu, int32_t dtype, int32_t rows, int32_t I, const int32_t* num_rows,
+                            uint8_t* q, uint8_t* s, void* stream) {
+  if (!dtype_ok(dtype)) return W4A16_ERR_INVALID_ARG;
+  const int st = check_fp4_rows(rows, I);
+  if (st != W4A16_OK) return st;
+  if (rows > 0 && (!gu || !q || !s)) return W4A16_ERR_INVALID_ARG;
+  if (!aligned16(gu) || !aligned_to(q, 4)) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_fp4_silu_mul_quantize(gu, dtype, rows, I, num_rows, q, s, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K, const int32_t* num_rows, void* out,
+                     int32_t dtype, void* stream) {
+  if (!dtype_ok(dtype)) return W4A16_ERR_INVALID_ARG;
+  const int st = check_fp4_rows(rows, K);
+  if (st != W4A16_OK) return st;
+  if (rows > 0 && (!q || !s || !out)) return W4A16_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned_to(q, 4)) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_fp4_dequantize(q, s, rows, K, num_rows, out, dtype, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_packed_bytes(int32_t num_experts, int32_t N, int32_t K, size_t* bytes) {
+  const int st = check_fp4_weights(num_experts, N, K);
+  if (st != W4A16_OK) return st;
+  if (!bytes) return W4A16_ERR_INVALID_ARG;
+  *bytes = (size_t)num_experts * fp4_nblocks(N) * fp4_steps(K) * kFp4UnitBytes;
+  return W4A16_OK;
+}
+
+int mxfp4_repack(int32_t num_experts, int32_t N, int32_t K, const uint8_t* w_q, const uint8_t* w_s, void* packed,
+                 void* stream) {
+  const int st = check_fp4_weights(num_experts, N, K);
+  if (st != W4A16_OK) return st;
+  if (!w_q || !w_s || !packed || !all_aligned16(w_q, packed)) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_fp4_repack(w_q, w_s, num_experts, N, K, static_cast<uint8_t*>(packed),
+                                      static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q, const uint8_t* a_s, int32_t a_rows,
+                   int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids, int32_t capacity,
+                   const int32_t* expert_ids, const int32_t* num_tokens_post_padded, int32_t block_m,
+                   const void* packed, void* out, int32_t out_dtype, void* stream) {
+  if (!dtype_ok(out_dtype)) return W4A16_ERR_INVALID_ARG;
+  int st = check_fp4_weights(num_experts, N, K);
+  if (st != W4A16_OK) return st;
+  st = check_tokens(T, topk, num_experts, block_m);
+  if (st != W4A16_OK) return st;
+  if (capacity < 0 || a_rows < (gather ? T : capacity)) return W4A16_ERR_INVALID_ARG;
+  if (T == 0 || capacity == 0) return W4A16_OK;  // no slot, no row
+  if (!a_q || !a_s || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !packed || !out)
+    return W4A16_ERR_INVALID_ARG;
+  if (!all_aligned16(a_q, packed, out)) return W4A16_ERR_INVALID_ARG;
+  Fp4GemmParams p{};
+  p.a_q = a_q;
+  p.a_s = a_s;
+  p.packed = static_cast<const uint8_t*>(packed);
+  p.sorted = sorted_token_ids;
+  p.expert_ids = expert_ids;
+  p.ntpp = num_tokens_post_padded;
+  p.out = out;
+  p.E = num_experts;
+  p.N = N;
+  p.K = K;
+  p.gather = gather != 0;
+  p.topk = topk;
+  p.n_slots = T * topk;
+  p.capacity = capacity;
+  return hip_status(launch_fp4_gemm(block_m, p, out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,197 @@
+// The experts' product on 4-bit floating point operands with a scale per 32.
+//
+// out[p, n] = sum_k A[r(p), k] W[e, n, k] on v_mfma_scale_f32_16x16x128_f8f6f4,
+// which multiplies 4-bit operands, applies both operands' block scales and
+// adds in fp32. The weights are the instruction's first operand and the
+// activation rows its second, so a lane's four results are four
+// neighbouring output columns of one row.
+#include "internal.h"
+#include "rows.h"
+
+#include <algorithm>
+
+namespace w4a16 {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+// J: which byte of `ws` holds the weights' scale; the rows' is in byte 0.
+template <int J>
+__device__ __forceinline__ floatx4 mfma_fp4(i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
+  const i32x8 w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, J, ws, 0, as);
+}
+
+__device__ __forceinline__ floatx4 mfma_fp4(int j, i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
+  switch (j) {
+    case 0: return mfma_fp4<0>(w, a, c, ws, as);
+    case 1: return mfma_fp4<1>(w, a, c, ws, as);
+    case 2: return mfma_fp4<2>(w, a, c, ws, as);
+    default: return mfma_fp4<3>(w, a, c, ws, as);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, floatx4 v) {
+  struct Four {
+    T v[4];
+  } r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = (T)v[i];
+  *reinterpret_cast<__attribute__((aligned(4 * sizeof(T)))) Four*>(p) = r;
+}
+
+// Weight streaming: a workgroup of four waves takes 4 / SPLIT units, a unit
+// being one row block (16 RB rows) times 64 columns; SPLIT waves share a unit's
+// steps of K = 128 and add up through LDS in wave order. Weights and rows go
+// from memory straight to the registers that the MFMAs read, D steps ahead.
+// TAIL: K may end inside a step, and what lies past it is zeroed, or the scales
+// are not aligned to 4 bytes: scales are then read one by one instead of the four
+// of a row and step at once.
+template <typename T, int RB, int SPLIT, int D, bool TAIL>
+__global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
+  constexpr int kUnits = 4 / SPLIT;
+  __shared__ floatx4 part[SPLIT > 1 ? (SPLIT - 1) * kUnits : 1][RB * 4][SPLIT > 1 ? 64 : 1];
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int split = wave % SPLIT, local = wave / SPLIT;
+  const int nblocks = fp4_nblocks(p.N), steps = fp4_steps(p.K);
+  const int used = min(p.capacity, *p.ntpp) / (16 * RB);
+  const int64_t units = (int64_t)used * nblocks;
+  for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < units; u0 += (int64_t)gridDim.x * kUnits) {
+    const int64_t u = u0 + local;
+    const bool active = u < units;
+    const int b = (int)(u / nblocks), nb = (int)(u - (int64_t)b * nblocks);
+    const int e = active ? p.expert_ids[b] : -1;
+    const bool known = (uint32_t)e < (uint32_t)p.E;
+    floatx4 acc[RB][4] = {};
+    bool real[RB] = {};
+    if (known) {
+      const uint8_t* aq[RB];
+      const uint8_t* as[RB];
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        const int row = b * 16 * RB + 16 * r + (lane & 15);
+        const uint32_t slot = (uint32_t)p.sorted[row];
+        real[r] = slot < (uint32_t)p.n_slots;
+        const int64_t src = !real[r] ? 0 : p.gather ? (int64_t)(slot / (uint32_t)p.topk) : row;
+        aq[r] = p.a_q + src * (p.K / 2);
+        as[r] = p.a_s + src * (p.K / 32);
+      }
+      const uint8_t* wu = p.packed + ((int64_t)e * nblocks + nb) * steps * kFp4UnitBytes;
+      i32x4 w[D][4], a[D][RB];
+      int ws[D], sc[D][RB];
+      // a step past the last repeats it, so that the loop has no branch but its own
+      auto fetch = [&](int d, int step) {
+        step = min(step, steps - 1);
+        const uint8_t* at = wu + (int64_t)step * kFp4UnitBytes;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[d][j] = *reinterpret_cast<const i32x4*>(at + 1024 * j + 16 * lane);
+        ws[d] = *reinterpret_cast<const int*>(at + 4096 + 4 * lane);
+        const int block = step * 4 + (lane >> 4);  // of 32 values
+        const bool in = !TAIL || block < p.K / 32;
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          a[d][r] = *reinterpret_cast<const i32x4*>(aq[r] + (in ? 16 * block : 0));
+          sc[d][r] = TAIL ? as[r][in ? block : 0] : *reinterpret_cast<const int*>(as[r] + 4 * step);
+          if (TAIL && !in) a[d][r] = i32x4{0, 0, 0, 0}, sc[d][r] = 0;
+        }
+      };
+      auto compute = [&](int d) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const int scale = TAIL ? sc[d][r] : (int)((uint32_t)sc[d][r] >> (8 * (lane >> 4)));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[r][j] = mfma_fp4(j, w[d][j], a[d][r], acc[r][j], ws[d], scale);
+        }
+      };
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        fetch(d, split + d * SPLIT);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      int step = split;
+      for (; step + (D - 1) * SPLIT < steps; step += D * SPLIT) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          compute(d);
+          fetch(d, step + (D + d) * SPLIT);
+          __builtin_amdgcn_sched_barrier(0);  // keeps the fetches in step order, so that a wait is for the oldest
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < D - 1; ++d)
+        if (step + d * SPLIT < steps) compute(d);
+    }
+    if (SPLIT > 1) {
+      if (split > 0) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) part[local * (SPLIT - 1) + split - 1][4 * r + j][lane] = acc[r][j];
+      }
+      __syncthreads();
+      if (split == 0) {
+        for (int k = 0; k < SPLIT - 1; ++k)
+#pragma unroll
+          for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[r][j] += part[local * (SPLIT - 1) + k][4 * r + j][lane];
+      }
+      __syncthreads();
+    }
+    if (split == 0 && active) {
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        T* out = static_cast<T*>(p.out) + (int64_t)(b * 16 * RB + 16 * r + (lane & 15)) * p.N;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = nb * kNBlock + 16 * j + 4 * (lane >> 4);
+          const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+          if (n < p.N) store4(out + n, real[r] ? acc[r][j] : zero);
+        }
+      }
+    }
+  }
+}
+
+// K is whole steps of 128 and a row's scale bytes of a step are an aligned dword.
+bool whole_steps(const Fp4GemmParams& p) {
+  return p.K % kFp4StepK == 0 && (reinterpret_cast<uintptr_t>(p.a_s) & 3) == 0;
+}
+
+template <typename T, int RB, int SPLIT, int D>
+hipError_t launch_stream(const Fp4GemmParams& p, hipStream_t stream) {
+  const int64_t units = (int64_t)(p.capacity / (16 * RB)) * fp4_nblocks(p.N);
+  const int64_t groups = (units * SPLIT + 3) / 4;
+  if (groups == 0) return hipSuccess;
+  const int grid = (int)std::min<int64_t>(groups, (int64_t)device_cu_count() * 8);
+  if (!whole_steps(p))
+    hipLaunchKernelGGL((fp4_stream_kernel<T, RB, SPLIT, D, true>), dim3(grid), dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL((fp4_stream_kernel<T, RB, SPLIT, D, false>), dim3(grid), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch(int32_t block_m, const Fp4GemmParams& p, hipStream_t stream) {
+  switch (block_m) {
+    case 16: return launch_stream<T, 1, 4, 4>(p, stream);
+    case 32: return launch_stream<T, 2, 4, 3>(p, stream);
+    case 64: return launch_stream<T, 4, 1, 2>(p, stream);
+    case 128: return launch_stream<T, 8, 1, 1>(p, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_fp4_gemm(int32_t block_m, const Fp4GemmParams& p, int32_t out_dtype, hipStream_t stream) {
+  if (out_dtype == kBF16) return launch<bf16_t>(block_m, p, stream);
+  if (out_dtype == kFP16) return launch<f16_t>(block_m, p, stream);
+  return launch<float>(block_m, p, stream);
+}
+
+}  // namespace w4a16

@@ -1,0 +1,404 @@
+// Token rows into the aligned order of moe_align and back, with gradients.
+//
+//   permute            xp[p] = x[sorted[p] / topk], zero for padding rows
+//   unpermute          out[t] = sum_j w[t, j] * y[slot_rows[t, j]]   (fp32, j order)
+//   its gradients      dy[p] = w[s] * dout[s / topk], dw[t, j] = <dout[t], y[slot_rows[t, j]]>
+//   permute's gradient is unpermute with weights of 1.
+//
+// All of it is bound by memory: one token row against its (at most topk) expert
+// rows. slot_rows, the inverse of the aligned order, lets every kernel go token by token.
+#include "internal.h"
+#include "rows.h"
+
+#include <algorithm>
+
+namespace w4a16 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// slot_rows[i] = -1 for the n slots, then slot_rows[sorted[p]] = p for the real rows.
+__global__ __launch_bounds__(kThreads) void slot_fill_kernel(int32_t* slot_rows, int32_t n) {
+  const int32_t i = (int32_t)(blockIdx.x * kThreads + threadIdx.x);
+  if (i < n) slot_rows[i] = -1;
+}
+
+__global__ __launch_bounds__(kThreads) void slot_scatter_kernel(const int32_t* sorted, int32_t capacity,
+                                                                const int32_t* ntpp, int32_t n, int32_t* slot_rows) {
+  const int32_t p = (int32_t)(blockIdx.x * kThreads + threadIdx.x);
+  if (p >= min(capacity, *ntpp)) return;
+  const uint32_t s = (uint32_t)sorted[p];
+  if (s < (uint32_t)n) slot_rows[s] = p;
+}
+
+template <typename T>
+__device__ __forceinline__ void zero_row(T* row, int32_t H, int32_t first, int32_t step) {
+  Eight<T> z;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z.v[i] = (T)0.f;
+  for (int32_t c = first; c < H; c += step) {
+    if (c + 8 <= H) {
+      store8(row + c, z);
+    } else {
+      for (int32_t k = c; k < H; ++k) row[k] = (T)0.f;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void copy_row(T* dst, const T* src, int32_t H, int32_t first, int32_t step) {
+  for (int32_t c = first; c < H; c += step) {
+    if (c + 8 <= H) {
+      store8(dst + c, load8(src + c));
+    } else {
+      for (int32_t k = c; k < H; ++k) dst[k] = src[k];
+    }
+  }
+}
+
+// The padding rows among the 256 aligned rows from `first` on, zeroed by a wave each.
+template <typename T>
+__device__ __forceinline__ void zero_padding(T* rows, const int32_t* sorted, int32_t first, int32_t capacity,
+                                             const int32_t* ntpp, int32_t n, int32_t H) {
+  const int lane = (int)threadIdx.x & 63;
+  const int32_t p = first + (int32_t)threadIdx.x;
+  const bool pad = p < min(capacity, *ntpp) && (uint32_t)sorted[p] >= (uint32_t)n;
+  for (uint64_t m = __ballot(pad); m; m &= m - 1)
+    zero_row(rows + (int64_t)(p - lane + __builtin_ctzll(m)) * H, H, 8 * lane, 8 * 64);
+}
+
+// Few slots, one launch: block 0 writes slot_rows, the others one aligned row each.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void permute_by_row_kernel(const T* x, T* xp, const int32_t* sorted,
+                                                                  int32_t capacity, const int32_t* ntpp, int32_t n,
+                                                                  int32_t topk, int32_t H, int32_t* slot_rows) {
+  const int32_t live = min(capacity, *ntpp);
+  if (blockIdx.x == 0) {
+    for (int32_t i = (int32_t)threadIdx.x; i < n; i += kThreads) slot_rows[i] = -1;
+    __syncthreads();
+    for (int32_t p = (int32_t)threadIdx.x; p < live; p += 8 * kThreads) {
+      uint32_t slot[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) slot[k] = p + k * kThreads < live ? (uint32_t)sorted[p + k * kThreads] : ~0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (slot[k] < (uint32_t)n) slot_rows[slot[k]] = p + k * kThreads;
+    }
+    return;
+  }
+  const int32_t p = (int32_t)blockIdx.x - 1;
+  if (p >= live) return;
+  const uint32_t s = (uint32_t)sorted[p];
+  T* dst = xp + (int64_t)p * H;
+  const int32_t first = 8 * (int32_t)threadIdx.x;
+  if (s >= (uint32_t)n) return zero_row(dst, H, first, 8 * kThreads);
+  copy_row(dst, x + (int64_t)(s / (uint32_t)topk) * H, H, first, 8 * kThreads);
+}
+
+// Many slots, slot_rows known: blocks [0, T) read a token's row once and write it to
+// all of its rows; later blocks zero the padding rows among 256 aligned rows each.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void permute_by_token_kernel(const T* x, T* xp, const int32_t* sorted,
+                                                                    int32_t capacity, const int32_t* ntpp, int32_t n,
+                                                                    int32_t tokens, int32_t topk, int32_t H,
+                                                                    const int32_t* slot_rows) {
+  if ((int32_t)blockIdx.x >= tokens)
+    return zero_padding(xp, sorted, ((int32_t)blockIdx.x - tokens) * kThreads, capacity, ntpp, n, H);
+  const int lane = (int)threadIdx.x & 63;
+  const int32_t t = (int32_t)blockIdx.x;
+  const int32_t row = lane < topk ? slot_rows[(int64_t)t * topk + lane] : -1;
+  const uint64_t has = __ballot(row >= 0);
+  if (!has) return;
+  const T* src = x + (int64_t)t * H;
+  for (int32_t c = 8 * (int32_t)threadIdx.x; c < H; c += 8 * kThreads) {
+    const int count = min(8, H - c);
+    Eight<T> v;
+    if (count == 8) {
+      v = load8(src + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v.v[i] = i < count ? src[c + i] : (T)0.f;
+    }
+    for (uint64_t m = has; m; m &= m - 1) {
+      T* dst = xp + (int64_t)__builtin_amdgcn_readlane(row, __builtin_ctzll(m)) * H + c;
+      if (count == 8) {
+        store8(dst, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < count) dst[i] = v.v[i];
+      }
+    }
+  }
+}
+
+// The next K slots of `has` in ascending order, removed from it.
+template <int K>
+__device__ __forceinline__ void take(uint64_t& has, int (&j)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    j[k] = __builtin_ctzll(has);
+    has &= has - 1;
+  }
+}
+
+// f(std::integral_constant-like width) over the slots of `has`, eight at a time and
+// the rest by halves: the rows of one group are loaded side by side, and no row twice.
+template <int K>
+struct Width {
+  static constexpr int value = K;
+};
+template <typename F>
+__device__ __forceinline__ void in_groups(uint64_t has, F f) {
+  int left = __builtin_popcountll(has);
+  for (; left >= 8; left -= 8) f(Width<8>{}, has);
+  if (left & 4) f(Width<4>{}, has);
+  if (left & 2) f(Width<2>{}, has);
+  if (left & 1) f(Width<1>{}, has);
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// One block per token and `cols` columns. topk <= 32: lane j of every wave
+// holds the row of slot j.
+template <typename TY, typename TO>
+__global__ __launch_bounds__(kThreads) void unpermute_kernel(const TY* y, int32_t rows, const int32_t* slot_rows,
+                                                             const float* weights, TO* out, int32_t topk, int32_t H,
+                                                             int32_t cols) {
+  const int32_t chunks = (H + cols - 1) / cols;
+  const int32_t t = (int32_t)blockIdx.x / chunks;
+  const int32_t c0 = ((int32_t)blockIdx.x - t * chunks) * cols;
+  const int32_t c1 = min(H, c0 + cols);
+  const int lane = (int)threadIdx.x & 63;
+  const int32_t row = lane < topk ? slot_rows[(int64_t)t * topk + lane] : -1;
+  const bool live = (uint32_t)row < (uint32_t)rows;
+  const uint64_t has = __ballot(live);
+  const float weight = weights && live ? weights[(int64_t)t * topk + lane] : 1.f;
+  for (int32_t c = c0 + 8 * (int32_t)threadIdx.x; c < c1; c += 8 * kThreads) {
+    float sum[8] = {};
+    const int count = min(8, H - c);
+    in_groups(has, [&](auto width, uint64_t& left) {
+      constexpr int K = decltype(width)::value;
+      int j[K];
+      take<K>(left, j);
+      Eight<TY> v[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const TY* src = y + (int64_t)__builtin_amdgcn_readlane(row, j[k]) * H + c;
+        if (count == 8) {
+          v[k] = load8(src);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[k].v[i] = i < count ? src[i] : (TY)0.f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float wt = lane_value(weight, j[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += wt * (float)v[k].v[i];
+      }
+    });
+    TO* dst = out + (int64_t)t * H + c;
+    Eight<TO> r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i] = (TO)sum[i];
+    if (count == 8) {
+      store8(dst, r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < count) dst[i] = r.v[i];
+    }
+  }
+}
+
+// The sum over a wave, in lane 63: within rows of 16 lanes by shifts, then over the rows.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, true));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0x111, 0xF>(v);  // row_shr:1
+  v = dpp_add<0x112, 0xF>(v);  // row_shr:2
+  v = dpp_add<0x114, 0xF>(v);  // row_shr:4
+  v = dpp_add<0x118, 0xF>(v);  // row_shr:8
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+}
+
+// Blocks [0, T): one token each, its dy rows and weight gradients, up to eight
+// slots at a time. Later blocks: 256 aligned rows each, whose padding rows of dy are zeroed.
+template <typename TO, typename TY>
+__global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
+    const TO* dout, const TY* y, int32_t rows, int32_t T, const int32_t* slot_rows, const float* weights,
+    const int32_t* sorted, int32_t capacity, const int32_t* ntpp, int32_t n, TY* dy, float* dweights, int32_t topk,
+    int32_t H) {
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  if ((int32_t)blockIdx.x >= T)
+    return zero_padding(dy, sorted, ((int32_t)blockIdx.x - T) * kThreads, capacity, ntpp, n, H);
+  __shared__ float part[kThreads / 64][8];
+  const int32_t t = (int32_t)blockIdx.x;
+  const int32_t row = lane < topk ? slot_rows[(int64_t)t * topk + lane] : -1;
+  const bool live = (uint32_t)row < (uint32_t)rows;
+  const uint64_t has = __ballot(live);
+  const float weight = weights && live ? weights[(int64_t)t * topk + lane] : 1.f;
+  if (dweights && wave == 0 && lane < topk && !live) dweights[(int64_t)t * topk + lane] = 0.f;
+  const TO* d = dout + (int64_t)t * H;
+  in_groups(has, [&](auto width, uint64_t& left) {
+    constexpr int K = decltype(width)::value;
+    int j[K];
+    take<K>(left, j);
+    float dot[K] = {};
+    for (int32_t c = 8 * (int32_t)threadIdx.x; c < H; c += 8 * kThreads) {
+      const int count = min(8, H - c);
+      Eight<TO> dv;
+      Eight<TY> yv[K];
+      int64_t at[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) at[k] = (int64_t)__builtin_amdgcn_readlane(row, j[k]) * H + c;
+      if (count == 8) {
+        dv = load8(d + c);
+        if (dweights) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) yv[k] = load8(y + at[k]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dv.v[i] = i < count ? d[c + i] : (TO)0.f;
+#pragma unroll
+          for (int k = 0; k < K; ++k) yv[k].v[i] = dweights && i < count ? y[at[k] + i] : (TY)0.f;
+        }
+      }
+      if (dy) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const float wt = lane_value(weight, j[k]);
+          Eight<TY> r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r.v[i] = (TY)(wt * (float)dv.v[i]);
+          if (count == 8) {
+            store8(dy + at[k], r);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < count) dy[at[k] + i] = r.v[i];
+          }
+        }
+      }
+      if (dweights) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[k] += (float)dv.v[i] * (float)yv[k].v[i];
+      }
+    }
+    if (!dweights) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float sum = wave_sum(dot[k]);
+      if (lane == 63) part[wave][k] = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if ((int)threadIdx.x == k)
+        dweights[(int64_t)t * topk + j[k]] = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
+    __syncthreads();
+  });
+}
+
+// Up to this many slots and aligned rows one block writes slot_rows while the others move rows.
+constexpr int32_t kByRowSlots = 4096, kByRowCapacity = 16384;
+
+int blocks_for(int64_t items) { return (int)((items + kThreads - 1) / kThreads); }
+
+template <typename T>
+hipError_t permute(const void* x, int32_t tokens, int32_t topk, int32_t H, const int32_t* sorted, int32_t capacity,
+                   const int32_t* ntpp, void* xp, int32_t* slot_rows, hipStream_t stream) {
+  const int32_t n = tokens * topk;
+  const T* src = static_cast<const T*>(x);
+  T* dst = static_cast<T*>(xp);
+  if (n <= kByRowSlots && capacity <= kByRowCapacity) {
+    hipLaunchKernelGGL((permute_by_row_kernel<T>), dim3(1 + capacity), dim3(kThreads), 0, stream, src, dst, sorted,
+                       capacity, ntpp, n, topk, H, slot_rows);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(slot_fill_kernel, dim3(blocks_for(n)), dim3(kThreads), 0, stream, slot_rows, n);
+  if (capacity > 0) {
+    hipLaunchKernelGGL(slot_scatter_kernel, dim3(blocks_for(capacity)), dim3(kThreads), 0, stream, sorted, capacity,
+                       ntpp, n, slot_rows);
+    hipLaunchKernelGGL((permute_by_token_kernel<T>), dim3(tokens + blocks_for(capacity)), dim3(kThreads), 0, stream,
+                       src, dst, sorted, capacity, ntpp, n, tokens, topk, H, slot_rows);
+  }
+  return hipGetLastError();
+}
+
+template <typename TY, typename TO>
+hipError_t unpermute(const void* y, int32_t rows, int32_t T, int32_t topk, int32_t H, const int32_t* slot_rows,
+                     const float* weights, void* out, hipStream_t stream) {
+  // few tokens: split rows over blocks for parallelism; many tokens: a block per row
+  const int32_t cols = T >= 1024 ? H : 8 * kThreads;
+  const int64_t blocks = (int64_t)T * (((int64_t)H + cols - 1) / cols);
+  hipLaunchKernelGGL((unpermute_kernel<TY, TO>), dim3((unsigned)blocks), dim3(kThreads), 0, stream,
+                     static_cast<const TY*>(y), rows, slot_rows, weights, static_cast<TO*>(out), topk, H, cols);
+  return hipGetLastError();
+}
+
+template <typename TO, typename TY>
+hipError_t unpermute_backward(const void* dout, const void* y, int32_t rows, int32_t T, int32_t topk, int32_t H,
+                              const int32_t* slot_rows, const float* weights, const int32_t* sorted, int32_t capacity,
+                              const int32_t* ntpp, void* dy, float* dweights, hipStream_t stream) {
+  const int32_t pads = dy ? blocks_for(capacity) : 0;
+  if (T + pads == 0) return hipSuccess;
+  hipLaunchKernelGGL((unpermute_backward_kernel<TO, TY>), dim3((unsigned)(T + pads)), dim3(kThreads), 0, stream,
+                     static_cast<const TO*>(dout), static_cast<const TY*>(y), rows, T, slot_rows, weights, sorted,
+                     capacity, ntpp, T * topk, static_cast<TY*>(dy), dweights, topk, H);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_permute(const void* x, int32_t dtype, int32_t T, int32_t topk, int32_t H, const int32_t* sorted,
+                          int32_t capacity, const int32_t* ntpp, void* xp, int32_t* slot_rows, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  // rows are only moved: two- and four-byte elements
+  if (dtype == kFP32) return permute<float>(x, T, topk, H, sorted, capacity, ntpp, xp, slot_rows, stream);
+  return permute<bf16_t>(x, T, topk, H, sorted, capacity, ntpp, xp, slot_rows, stream);
+}
+
+hipError_t launch_unpermute(const void* y, int32_t y_dtype, int32_t rows, int32_t T, int32_t topk, int32_t H,
+                            const int32_t* slot_rows, const float* weights, void* out, int32_t out_dtype,
+                            hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  if (y_dtype == kBF16) return unpermute<bf16_t, bf16_t>(y, rows, T, topk, H, slot_rows, weights, out, stream);
+  if (y_dtype == kFP16) return unpermute<f16_t, f16_t>(y, rows, T, topk, H, slot_rows, weights, out, stream);
+  if (out_dtype == kBF16) return unpermute<float, bf16_t>(y, rows, T, topk, H, slot_rows, weights, out, stream);
+  if (out_dtype == kFP16) return unpermute<float, f16_t>(y, rows, T, topk, H, slot_rows, weights, out, stream);
+  return unpermute<float, float>(y, rows, T, topk, H, slot_rows, weights, out, stream);
+}
+
+hipError_t launch_unpermute_backward(const void* dout, int32_t out_dtype, const void* y, int32_t y_dtype, int32_t rows,
+                                     int32_t T, int32_t topk, int32_t H, const int32_t* slot_rows,
+                                     const float* weights, const int32_t* sorted, int32_t capacity,
+                                     const int32_t* ntpp, void* dy, float* dweights, hipStream_t stream) {
+  if (y_dtype == kBF16)
+    return unpermute_backward<bf16_t, bf16_t>(dout, y, rows, T, topk, H, slot_rows, weights, sorted, capacity, ntpp,
+                                              dy, dweights, stream);
+  if (y_dtype == kFP16)
+    return unpermute_backward<f16_t, f16_t>(dout, y, rows, T, topk, H, slot_rows, weights, sorted, capacity, ntpp, dy,
+                                            dweights, stream);
+  if (out_dtype == kBF16)
+    return unpermute_backward<bf16_t, float>(dout, y, rows, T, topk, H, slot_rows, weights, sorted, capacity, ntpp,
+                                             dy, dweights, stream);
+  if (out_dtype == kFP16)
+    return unpermute_backward<f16_t, float>(dout, y, rows, T, topk, H, slot_rows, weights, sorted, capacity, ntpp, dy,
+                                            dweights, stream);
+  return unpermute_backward<float, float>(dout, y, rows, T, topk, H, slot_rows, weights, sorted, capacity, ntpp, dy,
+                                          dweights, stream);
+}
+
+}  // namespace w4a16
