@@ -246,6 +246,18 @@ def w4a16_moe_combine(shape: Shape, topk_ids, topk_weights, y, out, stream=None)
 
 INVALID_ARG, UNSUPPORTED, CAPACITY = 1, 2, 3
 _codes = {}  # torch dtype -> w4a16_dtype
+_torch = None
+
+
+def _t():
+    """torch, imported at the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _codes.update({torch.bfloat16: 0, torch.int16: 0, torch.uint16: 0, torch.float16: 1, torch.float32: 2})
+        _torch = torch
+    return _torch
 
 
 def _refuse(where: str, what: str, status: int = INVALID_ARG):
@@ -253,11 +265,7 @@ def _refuse(where: str, what: str, status: int = INVALID_ARG):
 
 
 def _dtype(t, where: str) -> int:
-    if not _codes:
-        import torch
-
-        _codes.update({torch.bfloat16: 0, torch.int16: 0, torch.uint16: 0, torch.float16: 1, torch.float32: 2,
-                       torch.int32: None, torch.uint8: None})
+    _t()
     code = _codes.get(t.dtype)
     if code is None:
         _refuse(where, f"{t.dtype} rows", UNSUPPORTED)
@@ -266,16 +274,15 @@ def _dtype(t, where: str) -> int:
 
 def _launch(fn, where: str, args, tensors, stream):
     """Check that every tensor is contiguous and on the current device, then call the C ABI on the stream."""
-    import torch
-
-    here = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else None
+    cuda = _t().cuda
+    here = cuda.current_device() if cuda.is_available() else None
     for t in tensors:
         if t is not None:
             if t.get_device() != here:
                 _refuse(where, f"a tensor is on {t.device}, not on the current GPU")
             if not t.is_contiguous():
                 _refuse(where, "a tensor is not contiguous")
-    raw = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    raw = (cuda.current_stream() if stream is None else stream).cuda_stream
     status = fn(*args, raw)
     if status != OK:
         raise W4A16Error(status, where)
@@ -286,18 +293,16 @@ def _ptr(t):
 
 
 def _int32(where: str, *tensors):
-    import torch
-
+    int32 = _t().int32
     for t in tensors:
-        if t is not None and t.dtype is not torch.int32:
+        if t is not None and t.dtype is not int32:
             _refuse(where, "indexes and counts are int32")
 
 
 def _fp32(where: str, *tensors):
-    import torch
-
+    float32 = _t().float32
     for t in tensors:
-        if t is not None and t.dtype is not torch.float32:
+        if t is not None and t.dtype is not float32:
             _refuse(where, "weights are float32")
 
 
@@ -377,13 +382,12 @@ def moe_unpermute_backward(dout, y, slot_rows, topk_weights, sorted_token_ids, n
 
 
 def _fp4_buffers(name: str, rows: int, K: int, q, s, num_rows):
-    import torch
-
+    uint8 = _t().uint8
     if K % 32:
         _refuse(name, "rows are not a multiple of 32 long", UNSUPPORTED)
     if q.shape != (rows, K // 2) or s.shape != (rows, K // 32):
         _refuse(name, "codes and scales are not [rows, K / 2] and [rows, K / 32]")
-    if q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
+    if q.dtype is not uint8 or s.dtype is not uint8:
         _refuse(name, "codes and scales are uint8")
     _int32(name, num_rows)
 
@@ -424,12 +428,11 @@ def mxfp4_packed_bytes(num_experts: int, N: int, K: int) -> int:
 
 
 def mxfp4_repack(w_q, w_s, packed, stream=None):
-    import torch
-
     name = "mxfp4_repack"
+    uint8 = _t().uint8
     E, N, half = w_q.shape
     need = mxfp4_packed_bytes(E, N, 2 * half)
-    if w_s.shape != (E, N, half // 16) or w_q.dtype is not torch.uint8 or w_s.dtype is not torch.uint8:
+    if w_s.shape != (E, N, half // 16) or w_q.dtype is not uint8 or w_s.dtype is not uint8:
         _refuse(name, "w_q and w_s are not uint8 [E, N, K / 2] and [E, N, K / 32]")
     if _nbytes(packed) < need:
         _refuse(name, "packed is smaller than mxfp4_packed_bytes")

@@ -157,6 +157,135 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
   }
 }
 
+// A barrier that orders LDS only: global loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The tile (row block b, 256-column tile nt) of this workgroup, from the row
+// blocks in use. Workgroups go round-robin to the 8 XCDs, each with an L2 of
+// its own: XCD x takes a contiguous eighth of the tiles, in groups of kGroupRows
+// row blocks with all their columns, row blocks innermost.
+constexpr int kXcds = 8;
+constexpr int kGroupRows = 8;
+__device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
+  const int64_t total = (int64_t)used * ntiles;
+  const int64_t chunk = (total + kXcds - 1) / kXcds;
+  const int64_t at = (int64_t)blockIdx.x / kXcds;
+  const int64_t tile = ((int64_t)blockIdx.x % kXcds) * chunk + at;
+  if (at >= chunk || tile >= total) return false;
+  const int64_t per_group = (int64_t)kGroupRows * ntiles;
+  const int first = (int)(tile / per_group) * kGroupRows;
+  const int rows = min(kGroupRows, used - first);
+  const int rest = (int)(tile % per_group);
+  nt = rest / rows;
+  b = first + rest - nt * rows;
+  return true;
+}
+
+// Many rows per expert: a workgroup of four waves computes 16 RB rows times 256
+// columns, a wave all of its rows times 64 columns. A wave's weights are its own
+// and go from memory to registers; the rows are shared, so each wave fetches its
+// part of them and all read them from LDS, in the order the MFMA takes. Both are
+// fetched D steps of K = 128 ahead; one barrier per step.
+template <typename T, int RB, int D>
+__global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int ntiles) {
+  constexpr int BM = 16 * RB;
+  constexpr int kMine = RB / 4;  // row blocks that a wave fetches
+  __shared__ i32x4 rows_lds[D][RB][64];
+  __shared__ uint32_t scales_lds[D][BM];
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nblocks = fp4_nblocks(p.N), steps = p.K / kFp4StepK;
+  int b, nt;
+  if (!tile_of(min(p.capacity, *p.ntpp) / BM, ntiles, b, nt)) return;
+  const int nb = nt * 4 + wave;
+  const int e = p.expert_ids[b];
+  const bool known = (uint32_t)e < (uint32_t)p.E;
+  floatx4 acc[RB][4] = {};
+
+  if (known) {
+    // rows without a slot read row 0 and are zeroed at the store
+    auto source = [&](int row) -> int64_t {
+      const uint32_t slot = (uint32_t)p.sorted[row];
+      if (slot >= (uint32_t)p.n_slots) return 0;
+      return p.gather ? (int64_t)(slot / (uint32_t)p.topk) : row;
+    };
+    const uint8_t* aq[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      aq[i] = p.a_q + source(b * BM + 16 * (wave * kMine + i) + (lane & 15)) * (p.K / 2) + 16 * (lane >> 4);
+    const uint8_t* as = p.a_s + source(b * BM + (tid & (BM - 1))) * (p.K / 32);
+    // a wave past the last column block repeats it and stores nothing
+    const uint8_t* wp = p.packed + ((int64_t)e * nblocks + min(nb, nblocks - 1)) * steps * kFp4UnitBytes;
+
+    i32x4 w[D][4], a[D][kMine];
+    int ws[D];
+    uint32_t sc[D];
+    // a step past the last repeats it, so that the loop has no branch but its own
+    auto fetch_rows = [&](int slot, int step) {
+      step = min(step, steps - 1);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) a[slot][i] = *reinterpret_cast<const i32x4*>(aq[i] + 64 * step);
+      sc[slot] = *reinterpret_cast<const uint32_t*>(as + 4 * step);
+    };
+    auto fetch_weights = [&](int slot, int step) {
+      const uint8_t* u = wp + (int64_t)min(step, steps - 1) * kFp4UnitBytes;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[slot][j] = *reinterpret_cast<const i32x4*>(u + 1024 * j + 16 * lane);
+      ws[slot] = *reinterpret_cast<const int*>(u + 4096 + 4 * lane);
+    };
+    auto publish = [&](int slot) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) rows_lds[slot][wave * kMine + i][lane] = a[slot][i];
+      scales_lds[slot][tid & (BM - 1)] = sc[slot];  // the same value from every thread that has it
+    };
+    // step s, in ring slot d: the slot written here was last read a barrier ago
+    auto compute = [&](int d, int s) {
+      const int next = (d + 1) % D;
+      publish(next);
+      fetch_rows(next, s + 1 + D);
+      const uint8_t* sb = reinterpret_cast<const uint8_t*>(scales_lds[d]) + 4 * (lane & 15) + (lane >> 4);
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        const i32x4 av = rows_lds[d][r][lane];
+        const int av_s = sb[64 * r];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[r][j] = mfma_fp4(j, w[d][j], av, acc[r][j], ws[d], av_s);
+      }
+      fetch_weights(d, s + D);
+      lds_barrier();
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      fetch_rows(d, d);
+      fetch_weights(d, d);
+    }
+    publish(0);
+    fetch_rows(0, D);
+    lds_barrier();
+    int s = 0;
+    for (; s + D <= steps; s += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) compute(d, s + d);
+    }
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+      if (s + d < steps) compute(d, s + d);
+  }
+  if (nb >= nblocks) return;
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    const int row = b * BM + 16 * r + (lane & 15);
+    const bool real = known && (uint32_t)p.sorted[row] < (uint32_t)p.n_slots;
+    T* out = static_cast<T*>(p.out) + (int64_t)row * p.N;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = nb * kNBlock + 16 * j + 4 * (lane >> 4);
+      const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+      if (n < p.N) store4(out + n, real ? acc[r][j] : zero);
+    }
+  }
+}
+
 // K is whole steps of 128 and a row's scale bytes of a step are an aligned dword.
 bool whole_steps(const Fp4GemmParams& p) {
   return p.K % kFp4StepK == 0 && (reinterpret_cast<uintptr_t>(p.a_s) & 3) == 0;
@@ -175,8 +304,21 @@ hipError_t launch_stream(const Fp4GemmParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <typename T, int RB, int D>
+hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
+  const int ntiles = (fp4_nblocks(p.N) + 3) / 4;
+  const int64_t tiles = (int64_t)(p.capacity / (16 * RB)) * ntiles;
+  const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
+  if (grid == 0) return hipSuccess;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((fp4_tile_kernel<T, RB, D>), dim3((unsigned)grid), dim3(256), 0, stream, p, ntiles);
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t launch(int32_t block_m, const Fp4GemmParams& p, hipStream_t stream) {
+  if (whole_steps(p) && block_m == 128) return launch_tile<T, 8, 2>(p, stream);
+  if (whole_steps(p) && block_m == 64) return launch_tile<T, 4, 2>(p, stream);
   switch (block_m) {
     case 16: return launch_stream<T, 1, 4, 4>(p, stream);
     case 32: return launch_stream<T, 2, 4, 3>(p, stream);
