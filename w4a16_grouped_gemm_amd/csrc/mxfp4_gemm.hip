@@ -17,19 +17,30 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-// J: which byte of `ws` holds the weights' scale; the rows' is in byte 0.
-template <int J>
+// J, R: which byte of `ws` and `as` holds the weights' and the rows' scale.
+template <int J, int R>
 __device__ __forceinline__ floatx4 mfma_fp4(i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
   const i32x8 w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, J, ws, 0, as);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, J, ws, R, as);
 }
 
+template <int R>
 __device__ __forceinline__ floatx4 mfma_fp4(int j, i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
   switch (j) {
-    case 0: return mfma_fp4<0>(w, a, c, ws, as);
-    case 1: return mfma_fp4<1>(w, a, c, ws, as);
-    case 2: return mfma_fp4<2>(w, a, c, ws, as);
-    default: return mfma_fp4<3>(w, a, c, ws, as);
+    case 0: return mfma_fp4<0, R>(w, a, c, ws, as);
+    case 1: return mfma_fp4<1, R>(w, a, c, ws, as);
+    case 2: return mfma_fp4<2, R>(w, a, c, ws, as);
+    default: return mfma_fp4<3, R>(w, a, c, ws, as);
+  }
+}
+
+// j and r are constants wherever this is used, so one call remains.
+__device__ __forceinline__ floatx4 mfma_fp4(int j, int r, i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
+  switch (r) {
+    case 0: return mfma_fp4<0>(j, w, a, c, ws, as);
+    case 1: return mfma_fp4<1>(j, w, a, c, ws, as);
+    case 2: return mfma_fp4<2>(j, w, a, c, ws, as);
+    default: return mfma_fp4<3>(j, w, a, c, ws, as);
   }
 }
 
@@ -104,7 +115,7 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
         for (int r = 0; r < RB; ++r) {
           const int scale = TAIL ? sc[d][r] : (int)((uint32_t)sc[d][r] >> (8 * (lane >> 4)));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[r][j] = mfma_fp4(j, w[d][j], a[d][r], acc[r][j], ws[d], scale);
+          for (int j = 0; j < 4; ++j) acc[r][j] = mfma_fp4(j, 0, w[d][j], a[d][r], acc[r][j], ws[d], scale);
         }
       };
 #pragma unroll
@@ -185,13 +196,16 @@ __device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
 // columns, a wave all of its rows times 64 columns. A wave's weights are its own
 // and go from memory to registers; the rows are shared, so each wave fetches its
 // part of them and all read them from LDS, in the order the MFMA takes. Both are
-// fetched D steps of K = 128 ahead; one barrier per step.
+// fetched D steps of K = 128 ahead; one barrier per step. Row scales lie in LDS
+// so that a lane reads those of its row in all RB row blocks at once, and the
+// MFMA picks the byte.
 template <typename T, int RB, int D>
 __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int ntiles) {
   constexpr int BM = 16 * RB;
   constexpr int kMine = RB / 4;  // row blocks that a wave fetches
+  constexpr int kAhead = 2;      // row blocks read from LDS before their use
   __shared__ i32x4 rows_lds[D][RB][64];
-  __shared__ uint32_t scales_lds[D][BM];
+  __shared__ uint8_t scales_lds[D][4][16][RB];  // k block of 32, row of 16, row block
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nblocks = fp4_nblocks(p.N), steps = p.K / kFp4StepK;
@@ -213,14 +227,15 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
       aq[i] = p.a_q + source(b * BM + 16 * (wave * kMine + i) + (lane & 15)) * (p.K / 2) + 16 * (lane >> 4);
-    const uint8_t* as = p.a_s + source(b * BM + (tid & (BM - 1))) * (p.K / 32);
+    const int mine = tid & (BM - 1);  // the row whose scales this thread fetches, as others may
+    const uint8_t* as = p.a_s + source(b * BM + mine) * (p.K / 32);
     // a wave past the last column block repeats it and stores nothing
     const uint8_t* wp = p.packed + ((int64_t)e * nblocks + min(nb, nblocks - 1)) * steps * kFp4UnitBytes;
 
     i32x4 w[D][4], a[D][kMine];
     int ws[D];
     uint32_t sc[D];
-    // a step past the last repeats it, so that the loop has no branch but its own
+    // a step past the last repeats it, so that no load is behind a branch
     auto fetch_rows = [&](int slot, int step) {
       step = min(step, steps - 1);
 #pragma unroll
@@ -236,28 +251,37 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
     auto publish = [&](int slot) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) rows_lds[slot][wave * kMine + i][lane] = a[slot][i];
-      scales_lds[slot][tid & (BM - 1)] = sc[slot];  // the same value from every thread that has it
+#pragma unroll
+      for (int k = 0; k < 4; ++k) scales_lds[slot][k][mine & 15][mine >> 4] = (uint8_t)(sc[slot] >> (8 * k));
     };
     // step s, in ring slot d: the slot written here was last read a barrier ago
     auto compute = [&](int d, int s) {
       const int next = (d + 1) % D;
       publish(next);
       fetch_rows(next, s + 1 + D);
-      const uint8_t* sb = reinterpret_cast<const uint8_t*>(scales_lds[d]) + 4 * (lane & 15) + (lane >> 4);
+      uint32_t rs[RB / 4];
+      __builtin_memcpy(rs, scales_lds[d][lane >> 4][lane & 15], sizeof(rs));
+      i32x4 av[kAhead + 1];
+#pragma unroll
+      for (int r = 0; r < kAhead; ++r) av[r] = rows_lds[d][r][lane];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int r = 0; r < RB; ++r) {
-        const i32x4 av = rows_lds[d][r][lane];
-        const int av_s = sb[64 * r];
+        if (r + kAhead < RB) av[(r + kAhead) % (kAhead + 1)] = rows_lds[d][r + kAhead][lane];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[r][j] = mfma_fp4(j, w[d][j], av, acc[r][j], ws[d], av_s);
+        for (int j = 0; j < 4; ++j)
+          acc[r][j] = mfma_fp4(j, r & 3, w[d][j], av[r % (kAhead + 1)], acc[r][j], ws[d], (int)rs[r / 4]);
+        __builtin_amdgcn_sched_barrier(0);
       }
       fetch_weights(d, s + D);
       lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       fetch_rows(d, d);
       fetch_weights(d, d);
+      __builtin_amdgcn_sched_barrier(0);
     }
     publish(0);
     fetch_rows(0, D);
@@ -271,17 +295,30 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
     for (int d = 0; d < D - 1; ++d)
       if (s + d < steps) compute(d, s + d);
   }
-  if (nb >= nblocks) return;
+
+  // A row block at a time through LDS, so that a store covers whole 128-byte
+  // lines: 16 rows of 64 columns, rows 16 bytes apart from a bank conflict.
+  constexpr int kPitch = 64 * (int)sizeof(T) + 16;
+  constexpr int kChunks = 64 * (int)sizeof(T) / 16;  // of a row
+  constexpr int kRowsAtOnce = 64 / kChunks;
+  __shared__ __attribute__((aligned(16))) uint8_t tile_lds[4][16 * kPitch];
+  uint8_t* tile = tile_lds[wave];
+  uint64_t real[(BM + 63) / 64];  // which rows have a slot
+#pragma unroll
+  for (int i = 0; i < BM / 64; ++i) real[i] = __ballot(known && (uint32_t)p.sorted[b * BM + 64 * i + lane] < (uint32_t)p.n_slots);
+  const int col = nb * kNBlock + lane % kChunks * (16 / (int)sizeof(T));
 #pragma unroll
   for (int r = 0; r < RB; ++r) {
-    const int row = b * BM + 16 * r + (lane & 15);
-    const bool real = known && (uint32_t)p.sorted[row] < (uint32_t)p.n_slots;
-    T* out = static_cast<T*>(p.out) + (int64_t)row * p.N;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = nb * kNBlock + 16 * j + 4 * (lane >> 4);
-      const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-      if (n < p.N) store4(out + n, real ? acc[r][j] : zero);
+    for (int j = 0; j < 4; ++j)
+      store4(reinterpret_cast<T*>(tile + (lane & 15) * kPitch) + 16 * j + 4 * (lane >> 4), acc[r][j]);
+#pragma unroll
+    for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
+      const int row = 16 * r + i * kRowsAtOnce + lane / kChunks;
+      i32x4 v = *reinterpret_cast<const i32x4*>(tile + (row & 15) * kPitch + 16 * (lane % kChunks));
+      if (!((real[16 * r / 64] >> (row & 63)) & 1)) v = i32x4{0, 0, 0, 0};
+      T* out = static_cast<T*>(p.out) + (int64_t)(b * BM + row) * p.N + col;
+      if (col < p.N) __builtin_nontemporal_store(v, reinterpret_cast<i32x4*>(out));
     }
   }
 }

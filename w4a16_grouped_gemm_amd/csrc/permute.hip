@@ -6,7 +6,10 @@
 //   permute's gradient is unpermute with weights of 1.
 //
 // All of it is bound by memory: one token row against its (at most topk) expert
-// rows. slot_rows, the inverse of the aligned order, lets every kernel go token by token.
+// rows. slot_rows, the inverse of the aligned order, lets every kernel go token by
+// token, so that a token's row is read or written once. Rows are moved eight
+// elements a thread; the last hidden % 8 columns go one a thread, so that the
+// loop over whole groups has no branches.
 #include "internal.h"
 #include "rows.h"
 
@@ -31,40 +34,23 @@ __global__ __launch_bounds__(kThreads) void slot_scatter_kernel(const int32_t* s
   if (s < (uint32_t)n) slot_rows[s] = p;
 }
 
-template <typename T>
-__device__ __forceinline__ void zero_row(T* row, int32_t H, int32_t first, int32_t step) {
-  Eight<T> z;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) z.v[i] = (T)0.f;
-  for (int32_t c = first; c < H; c += step) {
-    if (c + 8 <= H) {
-      store8(row + c, z);
-    } else {
-      for (int32_t k = c; k < H; ++k) row[k] = (T)0.f;
-    }
-  }
+template <Policy P = kCached, typename T>
+__device__ __forceinline__ void zero_row(T* row, int32_t H, int32_t thread, int32_t threads) {
+  const int32_t whole = H & ~7;
+  for (int32_t c = 8 * thread; c < whole; c += 8 * threads) store8<P>(row + c, Eight<T>{});
+  if (thread < H - whole) row[whole + thread] = (T)0.f;
 }
 
-template <typename T>
-__device__ __forceinline__ void copy_row(T* dst, const T* src, int32_t H, int32_t first, int32_t step) {
-  for (int32_t c = first; c < H; c += step) {
-    if (c + 8 <= H) {
-      store8(dst + c, load8(src + c));
-    } else {
-      for (int32_t k = c; k < H; ++k) dst[k] = src[k];
-    }
-  }
-}
-
-// The padding rows among the 256 aligned rows from `first` on, zeroed by a wave each.
+// The padding rows among the 32 aligned rows from `first` on, eight rows a wave.
+constexpr int kPadRows = 32;
 template <typename T>
 __device__ __forceinline__ void zero_padding(T* rows, const int32_t* sorted, int32_t first, int32_t capacity,
                                              const int32_t* ntpp, int32_t n, int32_t H) {
+  constexpr int kWaveRows = kPadRows / (kThreads / 64);
   const int lane = (int)threadIdx.x & 63;
-  const int32_t p = first + (int32_t)threadIdx.x;
-  const bool pad = p < min(capacity, *ntpp) && (uint32_t)sorted[p] >= (uint32_t)n;
-  for (uint64_t m = __ballot(pad); m; m &= m - 1)
-    zero_row(rows + (int64_t)(p - lane + __builtin_ctzll(m)) * H, H, 8 * lane, 8 * 64);
+  const int32_t p0 = first + kWaveRows * ((int32_t)threadIdx.x >> 6);
+  const bool pad = lane < kWaveRows && p0 + lane < min(capacity, *ntpp) && (uint32_t)sorted[p0 + lane] >= (uint32_t)n;
+  for (uint64_t m = __ballot(pad); m; m &= m - 1) zero_row<kStreamed>(rows + (int64_t)(p0 + __builtin_ctzll(m)) * H, H, lane, 64);
 }
 
 // Few slots, one launch: block 0 writes slot_rows, the others one aligned row each.
@@ -90,45 +76,51 @@ __global__ __launch_bounds__(kThreads) void permute_by_row_kernel(const T* x, T*
   if (p >= live) return;
   const uint32_t s = (uint32_t)sorted[p];
   T* dst = xp + (int64_t)p * H;
-  const int32_t first = 8 * (int32_t)threadIdx.x;
-  if (s >= (uint32_t)n) return zero_row(dst, H, first, 8 * kThreads);
-  copy_row(dst, x + (int64_t)(s / (uint32_t)topk) * H, H, first, 8 * kThreads);
+  if (s >= (uint32_t)n) return zero_row(dst, H, (int32_t)threadIdx.x, kThreads);
+  const T* src = x + (int64_t)(s / (uint32_t)topk) * H;
+  const int32_t whole = H & ~7;
+  for (int32_t c = 8 * (int32_t)threadIdx.x; c < whole; c += 8 * kThreads) store8(dst + c, load8(src + c));
+  if ((int32_t)threadIdx.x < H - whole) dst[whole + threadIdx.x] = src[whole + threadIdx.x];
 }
 
-// Many slots, slot_rows known: blocks [0, T) read a token's row once and write it to
-// all of its rows; later blocks zero the padding rows among 256 aligned rows each.
+// Lane j of every wave holds the row of token t's slot j, topk <= 32; which of them are rows.
+__device__ __forceinline__ uint64_t token_rows(const int32_t* slot_rows, int64_t t, int32_t topk, int32_t rows,
+                                               int32_t& row) {
+  const int lane = (int)threadIdx.x & 63;
+  row = lane < topk ? slot_rows[t * topk + lane] : -1;
+  return __ballot((uint32_t)row < (uint32_t)rows);
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// Many slots, slot_rows known: a token's row is read once and written to all of its
+// rows. The first `pads` blocks zero the padding rows. The rows written are
+// streamed: 32768 rows of 7168 bf16 take 109 us so and 187 us with cached stores,
+// 149 us row by row (4.9, 2.8 and 3.6 TB/s).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void permute_by_token_kernel(const T* x, T* xp, const int32_t* sorted,
                                                                     int32_t capacity, const int32_t* ntpp, int32_t n,
-                                                                    int32_t tokens, int32_t topk, int32_t H,
+                                                                    int32_t pads, int32_t topk, int32_t H,
                                                                     const int32_t* slot_rows) {
-  if ((int32_t)blockIdx.x >= tokens)
-    return zero_padding(xp, sorted, ((int32_t)blockIdx.x - tokens) * kThreads, capacity, ntpp, n, H);
-  const int lane = (int)threadIdx.x & 63;
-  const int32_t t = (int32_t)blockIdx.x;
-  const int32_t row = lane < topk ? slot_rows[(int64_t)t * topk + lane] : -1;
-  const uint64_t has = __ballot(row >= 0);
+  if ((int32_t)blockIdx.x < pads)
+    return zero_padding(xp, sorted, (int32_t)blockIdx.x * kPadRows, capacity, ntpp, n, H);
+  const int64_t t = (int32_t)blockIdx.x - pads;
+  int32_t row;
+  const uint64_t has = token_rows(slot_rows, t, topk, capacity, row);
   if (!has) return;
-  const T* src = x + (int64_t)t * H;
-  for (int32_t c = 8 * (int32_t)threadIdx.x; c < H; c += 8 * kThreads) {
-    const int count = min(8, H - c);
-    Eight<T> v;
-    if (count == 8) {
-      v = load8(src + c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v.v[i] = i < count ? src[c + i] : (T)0.f;
-    }
-    for (uint64_t m = has; m; m &= m - 1) {
-      T* dst = xp + (int64_t)__builtin_amdgcn_readlane(row, __builtin_ctzll(m)) * H + c;
-      if (count == 8) {
-        store8(dst, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < count) dst[i] = v.v[i];
-      }
-    }
+  const T* src = x + t * H;
+  const int32_t whole = H & ~7;
+  for (int32_t c = 8 * (int32_t)threadIdx.x; c < whole; c += 8 * kThreads) {
+    const Eight<T> v = load8(src + c);
+    for (uint64_t m = has; m; m &= m - 1)
+      store8<kStreamed>(xp + (int64_t)__builtin_amdgcn_readlane(row, __builtin_ctzll(m)) * H + c, v);
+  }
+  const int32_t c = whole + (int32_t)threadIdx.x;
+  if (c < H) {
+    const T v = src[c];
+    for (uint64_t m = has; m; m &= m - 1) xp[(int64_t)__builtin_amdgcn_readlane(row, __builtin_ctzll(m)) * H + c] = v;
   }
 }
 
@@ -142,8 +134,8 @@ __device__ __forceinline__ void take(uint64_t& has, int (&j)[K]) {
   }
 }
 
-// f(std::integral_constant-like width) over the slots of `has`, eight at a time and
-// the rest by halves: the rows of one group are loaded side by side, and no row twice.
+// f(width, left) over the slots of `has`, eight at a time and the rest by
+// halves: the rows of one group are loaded side by side, and no row twice.
 template <int K>
 struct Width {
   static constexpr int value = K;
@@ -157,43 +149,30 @@ __device__ __forceinline__ void in_groups(uint64_t has, F f) {
   if (left & 1) f(Width<1>{}, has);
 }
 
-__device__ __forceinline__ float lane_value(float v, int lane) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
-}
-
-// One block per token and `cols` columns. topk <= 32: lane j of every wave
-// holds the row of slot j.
+// One block per token and `cols` columns, a multiple of 8.
 template <typename TY, typename TO>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(const TY* y, int32_t rows, const int32_t* slot_rows,
                                                              const float* weights, TO* out, int32_t topk, int32_t H,
                                                              int32_t cols) {
   const int32_t chunks = (H + cols - 1) / cols;
-  const int32_t t = (int32_t)blockIdx.x / chunks;
-  const int32_t c0 = ((int32_t)blockIdx.x - t * chunks) * cols;
+  const int64_t t = (int32_t)blockIdx.x / chunks;
+  const int32_t c0 = ((int32_t)blockIdx.x - (int32_t)t * chunks) * cols;
   const int32_t c1 = min(H, c0 + cols);
   const int lane = (int)threadIdx.x & 63;
-  const int32_t row = lane < topk ? slot_rows[(int64_t)t * topk + lane] : -1;
-  const bool live = (uint32_t)row < (uint32_t)rows;
-  const uint64_t has = __ballot(live);
-  const float weight = weights && live ? weights[(int64_t)t * topk + lane] : 1.f;
-  for (int32_t c = c0 + 8 * (int32_t)threadIdx.x; c < c1; c += 8 * kThreads) {
+  int32_t row;
+  const uint64_t has = token_rows(slot_rows, t, topk, rows, row);
+  const float weight = weights && ((has >> lane) & 1) ? weights[t * topk + lane] : 1.f;
+  TO* dst = out + t * H;
+  const int32_t whole = c1 & ~7;
+  for (int32_t c = c0 + 8 * (int32_t)threadIdx.x; c < whole; c += 8 * kThreads) {
     float sum[8] = {};
-    const int count = min(8, H - c);
     in_groups(has, [&](auto width, uint64_t& left) {
       constexpr int K = decltype(width)::value;
       int j[K];
       take<K>(left, j);
       Eight<TY> v[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const TY* src = y + (int64_t)__builtin_amdgcn_readlane(row, j[k]) * H + c;
-        if (count == 8) {
-          v[k] = load8(src);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[k].v[i] = i < count ? src[i] : (TY)0.f;
-        }
-      }
+      for (int k = 0; k < K; ++k) v[k] = load8<kStreamed>(y + (int64_t)__builtin_amdgcn_readlane(row, j[k]) * H + c);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const float wt = lane_value(weight, j[k]);
@@ -201,17 +180,19 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(const TY* y, int32_
         for (int i = 0; i < 8; ++i) sum[i] += wt * (float)v[k].v[i];
       }
     });
-    TO* dst = out + (int64_t)t * H + c;
     Eight<TO> r;
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.v[i] = (TO)sum[i];
-    if (count == 8) {
-      store8(dst, r);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < count) dst[i] = r.v[i];
+    store8(dst + c, r);
+  }
+  const int32_t c = whole + (int32_t)threadIdx.x;
+  if (c < c1) {
+    float sum = 0.f;
+    for (uint64_t m = has; m; m &= m - 1) {
+      const int j = __builtin_ctzll(m);
+      sum += lane_value(weight, j) * (float)y[(int64_t)__builtin_amdgcn_readlane(row, j) * H + c];
     }
+    dst[c] = (TO)sum;
   }
 }
 
@@ -229,64 +210,50 @@ __device__ __forceinline__ float wave_sum(float v) {
   return dpp_add<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
 }
 
-// Blocks [0, T): one token each, its dy rows and weight gradients, up to eight
-// slots at a time. Later blocks: 256 aligned rows each, whose padding rows of dy are zeroed.
+// The first `pads` blocks zero the padding rows of dy; then one block per token: its
+// dy rows and weight gradients, up to eight slots at a time.
 template <typename TO, typename TY>
 __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
-    const TO* dout, const TY* y, int32_t rows, int32_t T, const int32_t* slot_rows, const float* weights,
+    const TO* dout, const TY* y, int32_t rows, int32_t pads, const int32_t* slot_rows, const float* weights,
     const int32_t* sorted, int32_t capacity, const int32_t* ntpp, int32_t n, TY* dy, float* dweights, int32_t topk,
     int32_t H) {
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-  if ((int32_t)blockIdx.x >= T)
-    return zero_padding(dy, sorted, ((int32_t)blockIdx.x - T) * kThreads, capacity, ntpp, n, H);
+  if ((int32_t)blockIdx.x < pads)
+    return zero_padding(dy, sorted, (int32_t)blockIdx.x * kPadRows, capacity, ntpp, n, H);
   __shared__ float part[kThreads / 64][8];
-  const int32_t t = (int32_t)blockIdx.x;
-  const int32_t row = lane < topk ? slot_rows[(int64_t)t * topk + lane] : -1;
-  const bool live = (uint32_t)row < (uint32_t)rows;
-  const uint64_t has = __ballot(live);
-  const float weight = weights && live ? weights[(int64_t)t * topk + lane] : 1.f;
-  if (dweights && wave == 0 && lane < topk && !live) dweights[(int64_t)t * topk + lane] = 0.f;
-  const TO* d = dout + (int64_t)t * H;
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int64_t t = (int32_t)blockIdx.x - pads;
+  int32_t row;
+  const uint64_t has = token_rows(slot_rows, t, topk, rows, row);
+  const bool live = (has >> lane) & 1;
+  const float weight = weights && live ? weights[t * topk + lane] : 1.f;
+  if (dweights && wave == 0 && lane < topk && !live) dweights[t * topk + lane] = 0.f;
+  const TO* d = dout + t * H;
+  const int32_t whole = H & ~7;
   in_groups(has, [&](auto width, uint64_t& left) {
     constexpr int K = decltype(width)::value;
     int j[K];
     take<K>(left, j);
-    float dot[K] = {};
-    for (int32_t c = 8 * (int32_t)threadIdx.x; c < H; c += 8 * kThreads) {
-      const int count = min(8, H - c);
-      Eight<TO> dv;
+    int64_t at[K];
+    float wt[K], dot[K] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      at[k] = (int64_t)__builtin_amdgcn_readlane(row, j[k]) * H;
+      wt[k] = lane_value(weight, j[k]);
+    }
+    for (int32_t c = 8 * (int32_t)threadIdx.x; c < whole; c += 8 * kThreads) {
+      const Eight<TO> dv = load8(d + c);
       Eight<TY> yv[K];
-      int64_t at[K];
+      if (dweights) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) at[k] = (int64_t)__builtin_amdgcn_readlane(row, j[k]) * H + c;
-      if (count == 8) {
-        dv = load8(d + c);
-        if (dweights) {
-#pragma unroll
-          for (int k = 0; k < K; ++k) yv[k] = load8(y + at[k]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dv.v[i] = i < count ? d[c + i] : (TO)0.f;
-#pragma unroll
-          for (int k = 0; k < K; ++k) yv[k].v[i] = dweights && i < count ? y[at[k] + i] : (TY)0.f;
-        }
+        for (int k = 0; k < K; ++k) yv[k] = load8<kStreamed>(y + at[k] + c);
       }
       if (dy) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          const float wt = lane_value(weight, j[k]);
           Eight<TY> r;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r.v[i] = (TY)(wt * (float)dv.v[i]);
-          if (count == 8) {
-            store8(dy + at[k], r);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < count) dy[at[k] + i] = r.v[i];
-          }
+          for (int i = 0; i < 8; ++i) r.v[i] = (TY)(wt[k] * (float)dv.v[i]);
+          store8<kStreamed>(dy + at[k] + c, r);
         }
       }
       if (dweights) {
@@ -294,6 +261,15 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int i = 0; i < 8; ++i) dot[k] += (float)dv.v[i] * (float)yv[k].v[i];
+      }
+    }
+    const int32_t c = whole + (int32_t)threadIdx.x;
+    if (c < H) {
+      const float dv = (float)d[c];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (dweights) dot[k] += dv * (float)y[at[k] + c];
+        if (dy) dy[at[k] + c] = (TY)(wt[k] * dv);
       }
     }
     if (!dweights) return;
@@ -306,7 +282,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if ((int)threadIdx.x == k)
-        dweights[(int64_t)t * topk + j[k]] = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
+        dweights[t * topk + j[k]] = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
     __syncthreads();
   });
 }
@@ -314,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
 // Up to this many slots and aligned rows one block writes slot_rows while the others move rows.
 constexpr int32_t kByRowSlots = 4096, kByRowCapacity = 16384;
 
-int blocks_for(int64_t items) { return (int)((items + kThreads - 1) / kThreads); }
+int blocks_for(int64_t items, int each) { return (int)((items + each - 1) / each); }
 
 template <typename T>
 hipError_t permute(const void* x, int32_t tokens, int32_t topk, int32_t H, const int32_t* sorted, int32_t capacity,
@@ -327,12 +303,13 @@ hipError_t permute(const void* x, int32_t tokens, int32_t topk, int32_t H, const
                        capacity, ntpp, n, topk, H, slot_rows);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(slot_fill_kernel, dim3(blocks_for(n)), dim3(kThreads), 0, stream, slot_rows, n);
+  hipLaunchKernelGGL(slot_fill_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, stream, slot_rows, n);
   if (capacity > 0) {
-    hipLaunchKernelGGL(slot_scatter_kernel, dim3(blocks_for(capacity)), dim3(kThreads), 0, stream, sorted, capacity,
-                       ntpp, n, slot_rows);
-    hipLaunchKernelGGL((permute_by_token_kernel<T>), dim3(tokens + blocks_for(capacity)), dim3(kThreads), 0, stream,
-                       src, dst, sorted, capacity, ntpp, n, tokens, topk, H, slot_rows);
+    const int32_t pads = blocks_for(capacity, kPadRows);
+    hipLaunchKernelGGL(slot_scatter_kernel, dim3(blocks_for(capacity, kThreads)), dim3(kThreads), 0, stream, sorted,
+                       capacity, ntpp, n, slot_rows);
+    hipLaunchKernelGGL((permute_by_token_kernel<T>), dim3((unsigned)pads + (unsigned)tokens), dim3(kThreads), 0,
+                       stream, src, dst, sorted, capacity, ntpp, n, pads, topk, H, slot_rows);
   }
   return hipGetLastError();
 }
@@ -341,8 +318,8 @@ template <typename TY, typename TO>
 hipError_t unpermute(const void* y, int32_t rows, int32_t T, int32_t topk, int32_t H, const int32_t* slot_rows,
                      const float* weights, void* out, hipStream_t stream) {
   // few tokens: split rows over blocks for parallelism; many tokens: a block per row
-  const int32_t cols = T >= 1024 ? H : 8 * kThreads;
-  const int64_t blocks = (int64_t)T * (((int64_t)H + cols - 1) / cols);
+  const int32_t cols = T >= 1024 ? (H + 7) & ~7 : 8 * kThreads;
+  const int64_t blocks = (int64_t)T * ((H + cols - 1) / cols);
   hipLaunchKernelGGL((unpermute_kernel<TY, TO>), dim3((unsigned)blocks), dim3(kThreads), 0, stream,
                      static_cast<const TY*>(y), rows, slot_rows, weights, static_cast<TO*>(out), topk, H, cols);
   return hipGetLastError();
@@ -352,11 +329,11 @@ template <typename TO, typename TY>
 hipError_t unpermute_backward(const void* dout, const void* y, int32_t rows, int32_t T, int32_t topk, int32_t H,
                               const int32_t* slot_rows, const float* weights, const int32_t* sorted, int32_t capacity,
                               const int32_t* ntpp, void* dy, float* dweights, hipStream_t stream) {
-  const int32_t pads = dy ? blocks_for(capacity) : 0;
+  const int32_t pads = dy ? blocks_for(capacity, kPadRows) : 0;
   if (T + pads == 0) return hipSuccess;
-  hipLaunchKernelGGL((unpermute_backward_kernel<TO, TY>), dim3((unsigned)(T + pads)), dim3(kThreads), 0, stream,
-                     static_cast<const TO*>(dout), static_cast<const TY*>(y), rows, T, slot_rows, weights, sorted,
-                     capacity, ntpp, T * topk, static_cast<TY*>(dy), dweights, topk, H);
+  hipLaunchKernelGGL((unpermute_backward_kernel<TO, TY>), dim3((unsigned)T + (unsigned)pads), dim3(kThreads), 0,
+                     stream, static_cast<const TO*>(dout), static_cast<const TY*>(y), rows, pads, slot_rows, weights,
+                     sorted, capacity, ntpp, T * topk, static_cast<TY*>(dy), dweights, topk, H);
   return hipGetLastError();
 }
 
