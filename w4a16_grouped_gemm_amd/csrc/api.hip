@@ -845,6 +845,7 @@ int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q
   p.E = num_experts;
   p.N = N;
   p.K = K;
+  p.a_rows = a_rows;
   p.gather = gather != 0;
   p.topk = topk;
   p.n_slots = T * topk;

@@ -16,33 +16,51 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-// J, R: which byte of `ws` and `as` holds the weights' and the rows' scale.
-template <int J, int R>
-__device__ __forceinline__ floatx4 mfma_fp4(i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
-  const i32x8 w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, J, ws, R, as);
-}
+__device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
-template <int R>
+// 16 x 16 x 128. j: which byte of `ws` holds the weights' scales; the rows' are in byte 0.
+// j (below also r) is a constant wherever this is used, so one of the calls remains.
 __device__ __forceinline__ floatx4 mfma_fp4(int j, i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
+#define MFMA(J) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w), widen(a), c, 4, 4, J, ws, 0, as)
   switch (j) {
-    case 0: return mfma_fp4<0, R>(w, a, c, ws, as);
-    case 1: return mfma_fp4<1, R>(w, a, c, ws, as);
-    case 2: return mfma_fp4<2, R>(w, a, c, ws, as);
-    default: return mfma_fp4<3, R>(w, a, c, ws, as);
+    case 0: MFMA(0);
+    case 1: MFMA(1);
+    case 2: MFMA(2);
+    default: MFMA(3);
   }
+#undef MFMA
 }
 
-// j and r are constants wherever this is used, so one call remains.
-__device__ __forceinline__ floatx4 mfma_fp4(int j, int r, i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
+// 32 x 32 x 64. The weights' scales are in byte 2 c of `ws`, the rows' in byte r of `as`.
+template <int C>
+__device__ __forceinline__ floatx16 mfma_fp4_32(int r, i32x4 w, i32x4 a, floatx16 acc, int ws, int as) {
+#define MFMA(R) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(w), widen(a), acc, 4, 4, 2 * C, ws, R, as)
   switch (r) {
-    case 0: return mfma_fp4<0>(j, w, a, c, ws, as);
-    case 1: return mfma_fp4<1>(j, w, a, c, ws, as);
-    case 2: return mfma_fp4<2>(j, w, a, c, ws, as);
-    default: return mfma_fp4<3>(j, w, a, c, ws, as);
+    case 0: MFMA(0);
+    case 1: MFMA(1);
+    case 2: MFMA(2);
+    default: MFMA(3);
   }
+#undef MFMA
 }
+__device__ __forceinline__ floatx16 mfma_fp4_32(int c, int r, i32x4 w, i32x4 a, floatx16 acc, int ws, int as) {
+  return c == 0 ? mfma_fp4_32<0>(r, w, a, acc, ws, as) : mfma_fp4_32<1>(r, w, a, acc, ws, as);
+}
+
+// A buffer of less than 4 GiB, read at a byte offset per lane plus one that all share.
+struct Buffer {
+  __amdgpu_buffer_rsrc_t rsrc;
+  __device__ __forceinline__ Buffer(const uint8_t* base, int64_t bytes)
+      : rsrc(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (int)(uint32_t)bytes, 0x00020000)) {}
+  __device__ __forceinline__ i32x4 load4(uint32_t lane_offset, int offset) const {
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)lane_offset, offset, 0));
+  }
+  __device__ __forceinline__ uint32_t load(uint32_t lane_offset, int offset) const {
+    return __builtin_amdgcn_raw_buffer_load_b32(rsrc, (int)lane_offset, offset, 0);
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(T* p, floatx4 v) {
@@ -68,7 +86,7 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int split = wave % SPLIT, local = wave / SPLIT;
-  const int nblocks = fp4_nblocks(p.N), steps = fp4_steps(p.K);
+  const int nblocks = fp4_nblocks(p.N), steps = (p.K + kFp4StepK - 1) / kFp4StepK;
   const int used = min(p.capacity, *p.ntpp) / (16 * RB);
   const int64_t units = (int64_t)used * nblocks;
   for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < units; u0 += (int64_t)gridDim.x * kUnits) {
@@ -91,7 +109,7 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
         aq[r] = p.a_q + src * (p.K / 2);
         as[r] = p.a_s + src * (p.K / 32);
       }
-      const uint8_t* wu = p.packed + ((int64_t)e * nblocks + nb) * steps * kFp4UnitBytes;
+      const uint8_t* wu = p.packed + ((int64_t)e * nblocks + nb) * fp4_steps(p.K) * kFp4UnitBytes;
       i32x4 w[D][4], a[D][RB];
       int ws[D], sc[D][RB];
       // a step past the last repeats it, so that the loop has no branch but its own
@@ -99,7 +117,7 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
         step = min(step, steps - 1);
         const uint8_t* at = wu + (int64_t)step * kFp4UnitBytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[d][j] = *reinterpret_cast<const i32x4*>(at + 1024 * j + 16 * lane);
+        for (int j = 0; j < 4; ++j) w[d][j] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(at + 1024 * j + 16 * lane));
         ws[d] = *reinterpret_cast<const int*>(at + 4096 + 4 * lane);
         const int block = step * 4 + (lane >> 4);  // of 32 values
         const bool in = !TAIL || block < p.K / 32;
@@ -115,7 +133,7 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
         for (int r = 0; r < RB; ++r) {
           const int scale = TAIL ? sc[d][r] : (int)((uint32_t)sc[d][r] >> (8 * (lane >> 4)));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[r][j] = mfma_fp4(j, 0, w[d][j], a[d][r], acc[r][j], ws[d], scale);
+          for (int j = 0; j < 4; ++j) acc[r][j] = mfma_fp4(j, w[d][j], a[d][r], acc[r][j], ws[d], scale);
         }
       };
 #pragma unroll
@@ -192,131 +210,180 @@ __device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
   return true;
 }
 
-// Many rows per expert: a workgroup of four waves computes 16 RB rows times 256
-// columns, a wave all of its rows times 64 columns. A wave's weights are its own
-// and go from memory to registers; the rows are shared, so each wave fetches its
-// part of them and all read them from LDS, in the order the MFMA takes. Both are
-// fetched D steps of K = 128 ahead; one barrier per step. Row scales lie in LDS
-// so that a lane reads those of its row in all RB row blocks at once, and the
-// MFMA picks the byte.
-template <typename T, int RB, int D>
+// Many rows per expert: a workgroup of four waves computes BM rows times 256
+// columns, a wave all of its rows times 64 columns, on 32 x 32 x 64 MFMAs. A
+// wave's weights are its own and go from memory to registers; the rows are shared,
+// so each wave fetches its part of them and all read them from LDS. Both are
+// fetched two steps of K = 128 ahead; one barrier per step. A step past the last
+// of K has zero weights (see internal.h) and repeats the rows of the last.
+//
+// Rows are fetched with four neighbouring lanes on a row's 64 bytes, since the
+// vector cache takes one line of four lanes at a time, and lie in LDS as they
+// come, row by row, the 16-byte chunk c of row r in place c ^ (r / 2 % 4): eight
+// rows' chunks c then fall on all 32 banks. Row scales are fetched for G steps at
+// once and lie so that a lane reads those of its row in all row blocks together,
+// the MFMA picking the byte.
+template <typename T, int BM, int G>
 __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int ntiles) {
-  constexpr int BM = 16 * RB;
-  constexpr int kMine = RB / 4;  // row blocks that a wave fetches
-  constexpr int kAhead = 2;      // row blocks read from LDS before their use
-  __shared__ i32x4 rows_lds[D][RB][64];
-  __shared__ uint8_t scales_lds[D][4][16][RB];  // k block of 32, row of 16, row block
+  constexpr int D = 2;
+  constexpr int kBlocks = BM / 32;  // row blocks
+  constexpr int kMine = BM / 64;    // 16-row parts that a wave fetches
+  constexpr int kAhead = 2;         // row fragments read from LDS before their use
+  __shared__ i32x4 rows_lds[D][BM][4];
+  __shared__ uint8_t scales_lds[2][G][4][32][4];  // group, step, k block of 32, row of 32, row block
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nblocks = fp4_nblocks(p.N), steps = p.K / kFp4StepK;
+  const int nblocks = fp4_nblocks(p.N), steps = fp4_steps(p.K), last = p.K / kFp4StepK - 1;
   int b, nt;
   if (!tile_of(min(p.capacity, *p.ntpp) / BM, ntiles, b, nt)) return;
   const int nb = nt * 4 + wave;
   const int e = p.expert_ids[b];
   const bool known = (uint32_t)e < (uint32_t)p.E;
-  floatx4 acc[RB][4] = {};
+  floatx16 acc[kBlocks][2] = {};
 
   if (known) {
     // rows without a slot read row 0 and are zeroed at the store
-    auto source = [&](int row) -> int64_t {
-      const uint32_t slot = (uint32_t)p.sorted[row];
+    auto source = [&](int row) -> uint32_t {
+      const uint32_t slot = (uint32_t)p.sorted[b * BM + row];
       if (slot >= (uint32_t)p.n_slots) return 0;
-      return p.gather ? (int64_t)(slot / (uint32_t)p.topk) : row;
+      return p.gather ? slot / (uint32_t)p.topk : (uint32_t)(b * BM + row);
     };
-    const uint8_t* aq[kMine];
+    const Buffer a_q(p.a_q, (int64_t)p.a_rows * (p.K / 2)), a_s(p.a_s, (int64_t)p.a_rows * (p.K / 32));
+    uint32_t aq[kMine];
+    i32x4* put[kMine];  // in ring slot 0
 #pragma unroll
-    for (int i = 0; i < kMine; ++i)
-      aq[i] = p.a_q + source(b * BM + 16 * (wave * kMine + i) + (lane & 15)) * (p.K / 2) + 16 * (lane >> 4);
-    const int mine = tid & (BM - 1);  // the row whose scales this thread fetches, as others may
-    const uint8_t* as = p.a_s + source(b * BM + mine) * (p.K / 32);
+    for (int i = 0; i < kMine; ++i) {
+      const int row = 16 * (wave * kMine + i) + (lane >> 2);
+      aq[i] = source(row) * (uint32_t)(p.K / 2) + 16 * (lane & 3);
+      put[i] = &rows_lds[0][row][(lane & 3) ^ (row >> 1 & 3)];
+    }
+    const bool scaler = wave < BM / 64;  // this wave fetches scales, a row a thread
+    const uint32_t as = scaler ? source(tid) * (uint32_t)(p.K / 32) : 0;
     // a wave past the last column block repeats it and stores nothing
-    const uint8_t* wp = p.packed + ((int64_t)e * nblocks + min(nb, nblocks - 1)) * steps * kFp4UnitBytes;
+    const Buffer wp(p.packed + ((int64_t)e * nblocks + min(nb, nblocks - 1)) * steps * kFp4UnitBytes,
+                    (int64_t)steps * kFp4UnitBytes);
+    // of a 16 x 128 part: this lane's column and k block in the first half of K
+    const uint32_t part = (lane & 15) + 16 * (lane >> 5), odd = lane >> 4 & 1;
+    const uint32_t wcodes = 1024 * odd + 16 * part, wscales = 4096 + 4 * part;
 
-    i32x4 w[D][4], a[D][kMine];
-    int ws[D];
-    uint32_t sc[D];
-    // a step past the last repeats it, so that no load is behind a branch
+    i32x4 w[D][2][2], a[D][kMine];
+    uint32_t ws[D][2], sc[G];
+    // what lies past the end repeats the last, so that no load is behind a branch
     auto fetch_rows = [&](int slot, int step) {
-      step = min(step, steps - 1);
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) a[slot][i] = *reinterpret_cast<const i32x4*>(aq[i] + 64 * step);
-      sc[slot] = *reinterpret_cast<const uint32_t*>(as + 4 * step);
+      for (int i = 0; i < kMine; ++i) a[slot][i] = a_q.load4(aq[i], 64 * min(step, last));
+    };
+    auto publish_rows = [&](int slot) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) put[i][slot * BM * 4] = a[slot][i];
+    };
+    auto fetch_scales = [&](int group) {  // last + 1 is a multiple of G
+      const int at = 4 * G * min(group, last / G);
+      if (G == 4) {
+        const i32x4 got = a_s.load4(as, at);
+#pragma unroll
+        for (int g = 0; g < G; ++g) sc[g] = (uint32_t)got[g];
+      } else {
+        sc[0] = a_s.load(as, at);
+      }
+    };
+    auto publish_scales = [&](int group) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) scales_lds[group & 1][g][k][tid & 31][tid >> 5] = (uint8_t)(sc[g] >> (8 * k));
     };
     auto fetch_weights = [&](int slot, int step) {
-      const uint8_t* u = wp + (int64_t)min(step, steps - 1) * kFp4UnitBytes;
+      const int at = min(step, steps - 1) * kFp4UnitBytes;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[slot][j] = *reinterpret_cast<const i32x4*>(u + 1024 * j + 16 * lane);
-      ws[slot] = *reinterpret_cast<const int*>(u + 4096 + 4 * lane);
-    };
-    auto publish = [&](int slot) {
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) rows_lds[slot][wave * kMine + i][lane] = a[slot][i];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) scales_lds[slot][k][mine & 15][mine >> 4] = (uint8_t)(sc[slot] >> (8 * k));
+        for (int c = 0; c < 2; ++c) w[slot][h][c] = wp.load4(wcodes + 2048 * c + 512 * h, at);
+        ws[slot][h] = wp.load(wscales + 128 * h, at);
+      }
     };
     // step s, in ring slot d: the slot written here was last read a barrier ago
     auto compute = [&](int d, int s) {
       const int next = (d + 1) % D;
-      publish(next);
+      publish_rows(next);
       fetch_rows(next, s + 1 + D);
-      uint32_t rs[RB / 4];
-      __builtin_memcpy(rs, scales_lds[d][lane >> 4][lane & 15], sizeof(rs));
-      i32x4 av[kAhead + 1];
+      if (scaler && s % G == 0) {
+        publish_scales(s / G + 1);
+        fetch_scales(s / G + 2);
+      }
+      uint32_t rs[2], cs[2];
 #pragma unroll
-      for (int r = 0; r < kAhead; ++r) av[r] = rows_lds[d][r][lane];
+      for (int h = 0; h < 2; ++h) {
+        rs[h] = *reinterpret_cast<const uint32_t*>(scales_lds[s / G & 1][s % G][2 * h + (lane >> 5)][lane & 31]);
+        cs[h] = ws[d][h] >> (8 * odd);  // bytes 0 and 2: the scales of this lane's two columns
+      }
+      constexpr int kFragments = 2 * kBlocks;  // (half of K, row block)
+      i32x4 av[kAhead + 1];
+      auto fragment = [&](int f) {
+        const int row = 32 * (f % kBlocks) + (lane & 31), chunk = 2 * (f / kBlocks) + (lane >> 5);
+        av[f % (kAhead + 1)] = rows_lds[d][row][chunk ^ (row >> 1 & 3)];
+      };
+#pragma unroll
+      for (int f = 0; f < kAhead; ++f) fragment(f);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int r = 0; r < RB; ++r) {
-        if (r + kAhead < RB) av[(r + kAhead) % (kAhead + 1)] = rows_lds[d][r + kAhead][lane];
+      for (int f = 0; f < kFragments; ++f) {
+        if (f + kAhead < kFragments) fragment(f + kAhead);
+        const int h = f / kBlocks, r = f % kBlocks;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[r][j] = mfma_fp4(j, r & 3, w[d][j], av[r % (kAhead + 1)], acc[r][j], ws[d], (int)rs[r / 4]);
+        for (int c = 0; c < 2; ++c)
+          acc[r][c] = mfma_fp4_32(c, r, w[d][h][c], av[f % (kAhead + 1)], acc[r][c], (int)cs[h], (int)rs[h]);
         __builtin_amdgcn_sched_barrier(0);
       }
       fetch_weights(d, s + D);
       lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
     };
+    if (scaler) fetch_scales(0);
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       fetch_rows(d, d);
       fetch_weights(d, d);
       __builtin_amdgcn_sched_barrier(0);
     }
-    publish(0);
+    if (scaler) {
+      publish_scales(0);
+      fetch_scales(1);
+    }
+    publish_rows(0);
     fetch_rows(0, D);
     lds_barrier();
-    int s = 0;
-    for (; s + D <= steps; s += D) {
+    for (int s = 0; s < steps; s += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) compute(d, s + d);
     }
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d)
-      if (s + d < steps) compute(d, s + d);
   }
 
   // A row block at a time through LDS, so that a store covers whole 128-byte
-  // lines: 16 rows of 64 columns, rows 16 bytes apart from a bank conflict.
+  // lines: 32 rows of 64 columns, rows 16 bytes apart from a bank conflict.
   constexpr int kPitch = 64 * (int)sizeof(T) + 16;
   constexpr int kChunks = 64 * (int)sizeof(T) / 16;  // of a row
   constexpr int kRowsAtOnce = 64 / kChunks;
-  __shared__ __attribute__((aligned(16))) uint8_t tile_lds[4][16 * kPitch];
+  __shared__ __attribute__((aligned(16))) uint8_t tile_lds[4][32 * kPitch];
   uint8_t* tile = tile_lds[wave];
-  uint64_t real[(BM + 63) / 64];  // which rows have a slot
+  uint64_t real[BM / 64];  // which rows have a slot
 #pragma unroll
-  for (int i = 0; i < BM / 64; ++i) real[i] = __ballot(known && (uint32_t)p.sorted[b * BM + 64 * i + lane] < (uint32_t)p.n_slots);
+  for (int i = 0; i < BM / 64; ++i)
+    real[i] = __ballot(known && (uint32_t)p.sorted[b * BM + 64 * i + lane] < (uint32_t)p.n_slots);
   const int col = nb * kNBlock + lane % kChunks * (16 / (int)sizeof(T));
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
+  for (int r = 0; r < kBlocks; ++r) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      store4(reinterpret_cast<T*>(tile + (lane & 15) * kPitch) + 16 * j + 4 * (lane >> 4), acc[r][j]);
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
-      const int row = 16 * r + i * kRowsAtOnce + lane / kChunks;
-      i32x4 v = *reinterpret_cast<const i32x4*>(tile + (row & 15) * kPitch + 16 * (lane % kChunks));
-      if (!((real[16 * r / 64] >> (row & 63)) & 1)) v = i32x4{0, 0, 0, 0};
+      for (int g = 0; g < 4; ++g)  // a lane's values are columns 8 g + 4 (lane / 32) + 0..3 of row lane % 32
+        store4(reinterpret_cast<T*>(tile + (lane & 31) * kPitch) + 32 * c + 8 * g + 4 * (lane >> 5),
+               floatx4{acc[r][c][4 * g], acc[r][c][4 * g + 1], acc[r][c][4 * g + 2], acc[r][c][4 * g + 3]});
+#pragma unroll
+    for (int i = 0; i < 32 / kRowsAtOnce; ++i) {
+      const int row = 32 * r + i * kRowsAtOnce + lane / kChunks;
+      i32x4 v = *reinterpret_cast<const i32x4*>(tile + (row & 31) * kPitch + 16 * (lane % kChunks));
+      if (!((real[32 * r / 64] >> (row & 63)) & 1)) v = i32x4{0, 0, 0, 0};
       T* out = static_cast<T*>(p.out) + (int64_t)(b * BM + row) * p.N + col;
       if (col < p.N) __builtin_nontemporal_store(v, reinterpret_cast<i32x4*>(out));
     }
@@ -341,21 +408,27 @@ hipError_t launch_stream(const Fp4GemmParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename T, int RB, int D>
+template <typename T, int BM>
 hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
   const int ntiles = (fp4_nblocks(p.N) + 3) / 4;
-  const int64_t tiles = (int64_t)(p.capacity / (16 * RB)) * ntiles;
+  const int64_t tiles = (int64_t)(p.capacity / BM) * ntiles;
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
   if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp4_tile_kernel<T, RB, D>), dim3((unsigned)grid), dim3(256), 0, stream, p, ntiles);
+  const dim3 g((unsigned)grid), t(256);
+  if (p.K / kFp4StepK % 4 == 0)
+    hipLaunchKernelGGL((fp4_tile_kernel<T, BM, 4>), g, t, 0, stream, p, ntiles);
+  else
+    hipLaunchKernelGGL((fp4_tile_kernel<T, BM, 1>), g, t, 0, stream, p, ntiles);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch(int32_t block_m, const Fp4GemmParams& p, hipStream_t stream) {
-  if (whole_steps(p) && block_m == 128) return launch_tile<T, 8, 2>(p, stream);
-  if (whole_steps(p) && block_m == 64) return launch_tile<T, 4, 2>(p, stream);
+  // the tile kernel's offsets into the rows are 32 bits
+  const bool tiles = whole_steps(p) && (int64_t)p.a_rows * (p.K / 2) < (int64_t)1 << 32;
+  if (tiles && block_m == 128) return launch_tile<T, 128>(p, stream);
+  if (tiles && block_m == 64) return launch_tile<T, 64>(p, stream);
   switch (block_m) {
     case 16: return launch_stream<T, 1, 4, 4>(p, stream);
     case 32: return launch_stream<T, 2, 4, 3>(p, stream);
