@@ -534,7 +534,7 @@ int mxfp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K
                      int32_t dtype, void* stream);
 
 /* Bytes of the packed weight buffer of num_experts matrices [N, K]: the codes
- * and scale bytes with N rounded up to 64 and K to 256. N a multiple of 16, K a
+ * and scale bytes with N rounded up to 64 and K to 128. N a multiple of 16, K a
  * multiple of 32, both at most 2^20 (else W4A16_ERR_UNSUPPORTED). */
 int mxfp4_packed_bytes(int32_t num_experts, int32_t N, int32_t K, size_t* bytes);
 

@@ -117,8 +117,8 @@ def test_gemm_refusals(lib, change, status):
 
 
 def test_packed_bytes_and_repack_refusals(lib):
-    # 64 columns by K = 128 are 4096 bytes of codes and 256 of scales; N rounds up to 64, K to 256
-    assert w.mxfp4_packed_bytes(3, 64, 256) == 3 * 2 * 4352
+    # 64 columns by K = 128 are 4096 bytes of codes and 256 of scales; N rounds up to 64, K to 128
+    assert w.mxfp4_packed_bytes(3, 64, 128) == 3 * 4352
     assert w.mxfp4_packed_bytes(3, 80, 160) == 3 * 2 * 2 * 4352
     for E, N, K, status in [(0, 64, 64, INVALID), (1, 8, 64, UNSUPPORTED), (1, 64, 16, UNSUPPORTED), (513, 64, 64, UNSUPPORTED)]:
         with pytest.raises(w.W4A16Error) as e:

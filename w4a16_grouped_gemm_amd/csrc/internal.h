@@ -179,14 +179,11 @@ hipError_t launch_unpermute_backward(const void* dout, int32_t out_dtype, const 
 // 64 nb + 16 j + (l & 15) from k = 128 step + 32 (l >> 4) on, in the canonical
 // order, which is the operand of v_mfma_scale_f32_16x16x128_f8f6f4; and the
 // dword at 4096 + 4 l, whose byte j is that block's scale. Columns past N and
-// values past K are zero codes with scale byte 0, and the steps are an even
-// number, so that the tile kernel's loop over pairs of steps has no rest.
+// values past K are zero codes with scale byte 0.
 constexpr int kFp4StepK = 128;
 constexpr int kFp4UnitBytes = 4352;
 __host__ __device__ inline int32_t fp4_nblocks(int32_t N) { return (N + kNBlock - 1) / kNBlock; }
-__host__ __device__ inline int32_t fp4_steps(int32_t K) {
-  return (K + 2 * kFp4StepK - 1) / (2 * kFp4StepK) * 2;
-}
+__host__ __device__ inline int32_t fp4_steps(int32_t K) { return (K + kFp4StepK - 1) / kFp4StepK; }
 
 hipError_t launch_fp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const int32_t* num_rows,
                                uint8_t* q, uint8_t* s, hipStream_t stream);

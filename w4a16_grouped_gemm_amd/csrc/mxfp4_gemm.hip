@@ -21,7 +21,7 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 // 16 x 16 x 128. j: which byte of `ws` holds the weights' scales; the rows' are in byte 0.
-// j (below also r) is a constant wherever this is used, so one of the calls remains.
+// j (c and h below) is a constant wherever this is used, so one of the calls remains.
 __device__ __forceinline__ floatx4 mfma_fp4(int j, i32x4 w, i32x4 a, floatx4 c, int ws, int as) {
 #define MFMA(J) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w), widen(a), c, 4, 4, J, ws, 0, as)
   switch (j) {
@@ -33,20 +33,15 @@ __device__ __forceinline__ floatx4 mfma_fp4(int j, i32x4 w, i32x4 a, floatx4 c, 
 #undef MFMA
 }
 
-// 32 x 32 x 64. The weights' scales are in byte 2 c of `ws`, the rows' in byte r of `as`.
-template <int C>
-__device__ __forceinline__ floatx16 mfma_fp4_32(int r, i32x4 w, i32x4 a, floatx16 acc, int ws, int as) {
-#define MFMA(R) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(w), widen(a), acc, 4, 4, 2 * C, ws, R, as)
-  switch (r) {
-    case 0: MFMA(0);
-    case 1: MFMA(1);
-    case 2: MFMA(2);
-    default: MFMA(3);
-  }
+// 32 x 32 x 64. The weights' scales are in byte 2 c of `ws`, the rows' in byte 2 h of `as`.
+__device__ __forceinline__ floatx16 mfma_fp4_32(int c, int h, i32x4 w, i32x4 a, floatx16 acc, int ws, int as) {
+#define MFMA(C, H) \
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(w), widen(a), acc, 4, 4, 2 * C, ws, 2 * H, as)
+  if (c == 0 && h == 0) MFMA(0, 0);
+  if (c == 0) MFMA(0, 1);
+  if (h == 0) MFMA(1, 0);
+  MFMA(1, 1);
 #undef MFMA
-}
-__device__ __forceinline__ floatx16 mfma_fp4_32(int c, int r, i32x4 w, i32x4 a, floatx16 acc, int ws, int as) {
-  return c == 0 ? mfma_fp4_32<0>(r, w, a, acc, ws, as) : mfma_fp4_32<1>(r, w, a, acc, ws, as);
 }
 
 // A buffer of less than 4 GiB, read at a byte offset per lane plus one that all share.
@@ -54,8 +49,10 @@ struct Buffer {
   __amdgpu_buffer_rsrc_t rsrc;
   __device__ __forceinline__ Buffer(const uint8_t* base, int64_t bytes)
       : rsrc(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (int)(uint32_t)bytes, 0x00020000)) {}
+  template <Policy P = kCached>
   __device__ __forceinline__ i32x4 load4(uint32_t lane_offset, int offset) const {
-    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)lane_offset, offset, 0));
+    constexpr int kAux = P == kStreamed ? 2 : 0;  // the non-temporal bit
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)lane_offset, offset, kAux));
   }
   __device__ __forceinline__ uint32_t load(uint32_t lane_offset, int offset) const {
     return __builtin_amdgcn_raw_buffer_load_b32(rsrc, (int)lane_offset, offset, 0);
@@ -86,7 +83,7 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int split = wave % SPLIT, local = wave / SPLIT;
-  const int nblocks = fp4_nblocks(p.N), steps = (p.K + kFp4StepK - 1) / kFp4StepK;
+  const int nblocks = fp4_nblocks(p.N), steps = fp4_steps(p.K);
   const int used = min(p.capacity, *p.ntpp) / (16 * RB);
   const int64_t units = (int64_t)used * nblocks;
   for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < units; u0 += (int64_t)gridDim.x * kUnits) {
@@ -109,7 +106,7 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
         aq[r] = p.a_q + src * (p.K / 2);
         as[r] = p.a_s + src * (p.K / 32);
       }
-      const uint8_t* wu = p.packed + ((int64_t)e * nblocks + nb) * fp4_steps(p.K) * kFp4UnitBytes;
+      const uint8_t* wu = p.packed + ((int64_t)e * nblocks + nb) * steps * kFp4UnitBytes;
       i32x4 w[D][4], a[D][RB];
       int ws[D], sc[D][RB];
       // a step past the last repeats it, so that the loop has no branch but its own
@@ -214,26 +211,26 @@ __device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
 // columns, a wave all of its rows times 64 columns, on 32 x 32 x 64 MFMAs. A
 // wave's weights are its own and go from memory to registers; the rows are shared,
 // so each wave fetches its part of them and all read them from LDS. Both are
-// fetched two steps of K = 128 ahead; one barrier per step. A step past the last
-// of K has zero weights (see internal.h) and repeats the rows of the last.
+// fetched two steps of K = 128 ahead; one barrier per step. The loop goes by two
+// steps; one past the last repeats the last one's weights with zero rows.
 //
 // Rows are fetched with four neighbouring lanes on a row's 64 bytes, since the
 // vector cache takes one line of four lanes at a time, and lie in LDS as they
 // come, row by row, the 16-byte chunk c of row r in place c ^ (r / 2 % 4): eight
-// rows' chunks c then fall on all 32 banks. Row scales are fetched for G steps at
-// once and lie so that a lane reads those of its row in all row blocks together,
-// the MFMA picking the byte.
-template <typename T, int BM, int G>
+// rows' chunks c then fall on all 32 banks. Row scales, a dword a step, are fetched
+// for G steps at once (4 where K allows it: a load of one row's scales per lane
+// takes the cache 64 lines).
+template <typename T, int BM, int G, Policy W>
 __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int ntiles) {
   constexpr int D = 2;
   constexpr int kBlocks = BM / 32;  // row blocks
   constexpr int kMine = BM / 64;    // 16-row parts that a wave fetches
   constexpr int kAhead = 2;         // row fragments read from LDS before their use
   __shared__ i32x4 rows_lds[D][BM][4];
-  __shared__ uint8_t scales_lds[2][G][4][32][4];  // group, step, k block of 32, row of 32, row block
+  __shared__ uint32_t scales_lds[2][G][BM];  // group, step, row: the scales of its four k blocks
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nblocks = fp4_nblocks(p.N), steps = fp4_steps(p.K), last = p.K / kFp4StepK - 1;
+  const int nblocks = fp4_nblocks(p.N), last = p.K / kFp4StepK - 1;
   int b, nt;
   if (!tile_of(min(p.capacity, *p.ntpp) / BM, ntiles, b, nt)) return;
   const int nb = nt * 4 + wave;
@@ -260,8 +257,8 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
     const bool scaler = wave < BM / 64;  // this wave fetches scales, a row a thread
     const uint32_t as = scaler ? source(tid) * (uint32_t)(p.K / 32) : 0;
     // a wave past the last column block repeats it and stores nothing
-    const Buffer wp(p.packed + ((int64_t)e * nblocks + min(nb, nblocks - 1)) * steps * kFp4UnitBytes,
-                    (int64_t)steps * kFp4UnitBytes);
+    const Buffer wp(p.packed + ((int64_t)e * nblocks + min(nb, nblocks - 1)) * (last + 1) * kFp4UnitBytes,
+                    (int64_t)(last + 1) * kFp4UnitBytes);
     // of a 16 x 128 part: this lane's column and k block in the first half of K
     const uint32_t part = (lane & 15) + 16 * (lane >> 5), odd = lane >> 4 & 1;
     const uint32_t wcodes = 1024 * odd + 16 * part, wscales = 4096 + 4 * part;
@@ -273,9 +270,10 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
 #pragma unroll
       for (int i = 0; i < kMine; ++i) a[slot][i] = a_q.load4(aq[i], 64 * min(step, last));
     };
-    auto publish_rows = [&](int slot) {
+    auto publish_rows = [&](int slot, int step) {
+      const int keep = step <= last ? -1 : 0;
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) put[i][slot * BM * 4] = a[slot][i];
+      for (int i = 0; i < kMine; ++i) put[i][slot * BM * 4] = a[slot][i] & keep;
     };
     auto fetch_scales = [&](int group) {  // last + 1 is a multiple of G
       const int at = 4 * G * min(group, last / G);
@@ -289,34 +287,33 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
     };
     auto publish_scales = [&](int group) {
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) scales_lds[group & 1][g][k][tid & 31][tid >> 5] = (uint8_t)(sc[g] >> (8 * k));
+      for (int g = 0; g < G; ++g) scales_lds[group & 1][g][tid] = sc[g];
     };
     auto fetch_weights = [&](int slot, int step) {
-      const int at = min(step, steps - 1) * kFp4UnitBytes;
+      const int at = min(step, last) * kFp4UnitBytes;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) w[slot][h][c] = wp.load4(wcodes + 2048 * c + 512 * h, at);
+        for (int c = 0; c < 2; ++c) w[slot][h][c] = wp.load4<W>(wcodes + 2048 * c + 512 * h, at);
         ws[slot][h] = wp.load(wscales + 128 * h, at);
       }
     };
     // step s, in ring slot d: the slot written here was last read a barrier ago
     auto compute = [&](int d, int s) {
       const int next = (d + 1) % D;
-      publish_rows(next);
+      publish_rows(next, s + 1);
       fetch_rows(next, s + 1 + D);
       if (scaler && s % G == 0) {
         publish_scales(s / G + 1);
         fetch_scales(s / G + 2);
       }
-      uint32_t rs[2], cs[2];
+      // bytes 0 and 2: of the rows' scales, this lane's k block in each half of K; of the
+      // columns', this lane's two columns
+      uint32_t rs[kBlocks], cs[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        rs[h] = *reinterpret_cast<const uint32_t*>(scales_lds[s / G & 1][s % G][2 * h + (lane >> 5)][lane & 31]);
-        cs[h] = ws[d][h] >> (8 * odd);  // bytes 0 and 2: the scales of this lane's two columns
-      }
+      for (int r = 0; r < kBlocks; ++r) rs[r] = scales_lds[s / G & 1][s % G][32 * r + (lane & 31)] >> (8 * (lane >> 5));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) cs[h] = ws[d][h] >> (8 * odd);
       constexpr int kFragments = 2 * kBlocks;  // (half of K, row block)
       i32x4 av[kAhead + 1];
       auto fragment = [&](int f) {
@@ -332,7 +329,7 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
         const int h = f / kBlocks, r = f % kBlocks;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          acc[r][c] = mfma_fp4_32(c, r, w[d][h][c], av[f % (kAhead + 1)], acc[r][c], (int)cs[h], (int)rs[h]);
+          acc[r][c] = mfma_fp4_32(c, h, w[d][h][c], av[f % (kAhead + 1)], acc[r][c], (int)cs[h], (int)rs[r]);
         __builtin_amdgcn_sched_barrier(0);
       }
       fetch_weights(d, s + D);
@@ -350,10 +347,10 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
       publish_scales(0);
       fetch_scales(1);
     }
-    publish_rows(0);
+    publish_rows(0, 0);
     fetch_rows(0, D);
     lds_barrier();
-    for (int s = 0; s < steps; s += D) {
+    for (int s = 0; s <= last; s += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) compute(d, s + d);
     }
@@ -408,7 +405,7 @@ hipError_t launch_stream(const Fp4GemmParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename T, int BM>
+template <typename T, int BM, int G>
 hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
   const int ntiles = (fp4_nblocks(p.N) + 3) / 4;
   const int64_t tiles = (int64_t)(p.capacity / BM) * ntiles;
@@ -416,11 +413,21 @@ hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
   if (grid == 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
   const dim3 g((unsigned)grid), t(256);
-  if (p.K / kFp4StepK % 4 == 0)
-    hipLaunchKernelGGL((fp4_tile_kernel<T, BM, 4>), g, t, 0, stream, p, ntiles);
+  // Weights that one row block of their expert reads are streamed, what several read is
+  // kept in the caches: 48 x 128 rows take 151 us so and 158 us cached, 16 x 2048 rows
+  // 377 us cached and 457 us streamed. The counts are on the device; n_slots over E is
+  // the most that is to be expected.
+  if (p.n_slots <= (int64_t)p.E * BM * 3 / 2)
+    hipLaunchKernelGGL((fp4_tile_kernel<T, BM, G, kStreamed>), g, t, 0, stream, p, ntiles);
   else
-    hipLaunchKernelGGL((fp4_tile_kernel<T, BM, 1>), g, t, 0, stream, p, ntiles);
+    hipLaunchKernelGGL((fp4_tile_kernel<T, BM, G, kCached>), g, t, 0, stream, p, ntiles);
   return hipGetLastError();
+}
+
+template <typename T, int BM>
+hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
+  if (p.K / kFp4StepK % 4 == 0) return launch_tile<T, BM, 4>(p, stream);
+  return launch_tile<T, BM, 1>(p, stream);
 }
 
 template <typename T>
