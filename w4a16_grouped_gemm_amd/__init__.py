@@ -247,13 +247,18 @@ def w4a16_moe_combine(shape: Shape, topk_ids, topk_weights, y, out, stream=None)
 INVALID_ARG, UNSUPPORTED, CAPACITY = 1, 2, 3
 _codes = {}  # torch dtype -> w4a16_dtype
 _torch = None
+_current = None  # device index -> handle of torch's current stream there
 
 
 def _t():
     """torch, imported at the first call that needs it."""
-    global _torch
+    global _torch, _current
     if _torch is None:
         import torch
+
+        # without the Stream object that torch.cuda.current_stream makes: 2.8 us less a call
+        _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
 
         _codes.update({torch.bfloat16: 0, torch.int16: 0, torch.uint16: 0, torch.float16: 1, torch.float32: 2})
         _torch = torch
@@ -275,15 +280,19 @@ def _dtype(t, where: str) -> int:
 def _launch(fn, where: str, args, tensors, stream):
     """Check that every tensor is contiguous and on the current device, then call the C ABI on the stream."""
     cuda = _t().cuda
-    here = cuda.current_device() if cuda.is_available() else None
+    try:
+        here = cuda.current_device()
+    except (RuntimeError, AssertionError):  # no GPU: no tensor is on it
+        here = None
     for t in tensors:
         if t is not None:
             if t.get_device() != here:
                 _refuse(where, f"a tensor is on {t.device}, not on the current GPU")
             if not t.is_contiguous():
                 _refuse(where, "a tensor is not contiguous")
-    raw = (cuda.current_stream() if stream is None else stream).cuda_stream
-    status = fn(*args, raw)
+    if stream is not None and stream.device_index != here:
+        _refuse(where, f"the stream is of GPU {stream.device_index}, not of the current one")
+    status = fn(*args, _current(here) if stream is None else stream.cuda_stream)
     if status != OK:
         raise W4A16Error(status, where)
 

@@ -850,7 +850,8 @@ int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q
   p.topk = topk;
   p.n_slots = T * topk;
   p.capacity = capacity;
-  return hip_status(launch_fp4_gemm(block_m, p, out_dtype, static_cast<hipStream_t>(stream)));
+  p.block_m = block_m;
+  return hip_status(launch_fp4_gemm(p, out_dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

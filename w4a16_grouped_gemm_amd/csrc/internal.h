@@ -205,9 +205,9 @@ struct Fp4GemmParams {
   int32_t E, N, K;
   int32_t a_rows;
   int32_t gather;         // A row of aligned row p: sorted[p] / topk, else p
-  int32_t topk, n_slots, capacity;
+  int32_t topk, n_slots, capacity, block_m;
 };
-hipError_t launch_fp4_gemm(int32_t block_m, const Fp4GemmParams& p, int32_t out_dtype, hipStream_t stream);
+hipError_t launch_fp4_gemm(const Fp4GemmParams& p, int32_t out_dtype, hipStream_t stream);
 
 // Compute units of the current device (cached per device).
 int device_cu_count();

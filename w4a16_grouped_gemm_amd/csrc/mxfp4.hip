@@ -65,21 +65,23 @@ template <typename T, bool SILU>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const T* x, int32_t rows, int32_t K,
                                                             const int32_t* num_rows, uint8_t* q, uint8_t* s) {
   const uint32_t per_row = (uint32_t)K / 8;
-  const int64_t total = live_rows(rows, num_rows) * per_row;  // a multiple of 4: quads are whole
+  const int64_t total = live_rows(rows, num_rows) * (int64_t)per_row;  // a multiple of 4: quads are whole
   for (int64_t g0 = (int64_t)blockIdx.x * kThreads * kUnroll + threadIdx.x; g0 < total;
        g0 += (int64_t)gridDim.x * kThreads * kUnroll) {
     Eight<T> a[kUnroll], b[SILU ? kUnroll : 1];
+    const int64_t r0 = SILU ? g0 / per_row : 0;
+    const uint32_t c0 = SILU ? (uint32_t)(g0 - r0 * per_row) : 0;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t g = g0 + u * kThreads;
       if (g >= total) continue;
       if (SILU) {
-        const int64_t r = g / per_row;
-        const T* at = x + 2 * r * K + 8 * (g - r * per_row);
-        a[u] = load8(at);
-        b[u] = load8(at + K);
+        const uint32_t c = c0 + u * kThreads, down = c / per_row;  // rows further down
+        const T* at = x + 2 * (r0 + down) * K + 8 * (c - down * per_row);
+        a[u] = load8<kStreamed>(at);
+        b[u] = load8<kStreamed>(at + K);
       } else {
-        a[u] = load8(x + 8 * g);
+        a[u] = load8<kStreamed>(x + 8 * g);
       }
     }
 #pragma unroll
@@ -124,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* q, 
       Eight<T> r;
 #pragma unroll
       for (int i = 0; i < 8; ++i) r.v[i] = (T)(v[i >> 1][i & 1] * scale);
-      store8(out + 8 * g, r);
+      store8<kStreamed>(out + 8 * g, r);
     }
   }
 }
@@ -167,7 +169,7 @@ template <bool SILU>
 hipError_t quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const int32_t* num_rows, uint8_t* q,
                     uint8_t* s, hipStream_t stream) {
   if (rows == 0) return hipSuccess;
-  const dim3 grid(grid_for((int64_t)rows * (K / 8), kUnroll, 16)), block(kThreads);
+  const dim3 grid(grid_for((int64_t)rows * (K / 8), kUnroll, 256)), block(kThreads);
   if (dtype == kBF16)
     hipLaunchKernelGGL((quantize_kernel<bf16_t, SILU>), grid, block, 0, stream, static_cast<const bf16_t*>(x), rows, K,
                        num_rows, q, s);
@@ -195,7 +197,7 @@ hipError_t launch_fp4_silu_mul_quantize(const void* gu, int32_t dtype, int32_t r
 hipError_t launch_fp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K, const int32_t* num_rows,
                                  void* out, int32_t dtype, hipStream_t stream) {
   if (rows == 0) return hipSuccess;
-  const dim3 grid(grid_for((int64_t)rows * (K / 8), kUnroll, 16)), block(kThreads);
+  const dim3 grid(grid_for((int64_t)rows * (K / 8), kUnroll, 256)), block(kThreads);
   if (dtype == kBF16)
     hipLaunchKernelGGL((dequantize_kernel<bf16_t>), grid, block, 0, stream, q, s, rows, K, num_rows,
                        static_cast<bf16_t*>(out));

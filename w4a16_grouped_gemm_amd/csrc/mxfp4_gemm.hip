@@ -70,7 +70,7 @@ __device__ __forceinline__ void store4(T* p, floatx4 v) {
 }
 
 // Weight streaming: a workgroup of four waves takes 4 / SPLIT units, a unit
-// being one row block (16 RB rows) times 64 columns; SPLIT waves share a unit's
+// being 16 RB rows of a row block times 64 columns; SPLIT waves share a unit's
 // steps of K = 128 and add up through LDS in wave order. Weights and rows go
 // from memory straight to the registers that the MFMAs read, D steps ahead.
 // TAIL: K may end inside a step, and what lies past it is zeroed, or the scales
@@ -84,13 +84,14 @@ __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int split = wave % SPLIT, local = wave / SPLIT;
   const int nblocks = fp4_nblocks(p.N), steps = fp4_steps(p.K);
-  const int used = min(p.capacity, *p.ntpp) / (16 * RB);
+  const int per_block = p.block_m / (16 * RB);
+  const int used = min(p.capacity, *p.ntpp) / p.block_m * per_block;
   const int64_t units = (int64_t)used * nblocks;
   for (int64_t u0 = (int64_t)blockIdx.x * kUnits; u0 < units; u0 += (int64_t)gridDim.x * kUnits) {
     const int64_t u = u0 + local;
     const bool active = u < units;
     const int b = (int)(u / nblocks), nb = (int)(u - (int64_t)b * nblocks);
-    const int e = active ? p.expert_ids[b] : -1;
+    const int e = active ? p.expert_ids[b / per_block] : -1;
     const bool known = (uint32_t)e < (uint32_t)p.E;
     floatx4 acc[RB][4] = {};
     bool real[RB] = {};
@@ -191,7 +192,7 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // its own: XCD x takes a contiguous eighth of the tiles, in groups of kGroupRows
 // row blocks with all their columns, row blocks innermost.
 constexpr int kXcds = 8;
-constexpr int kGroupRows = 8;
+constexpr int kGroupRows = 4;
 __device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
   const int64_t total = (int64_t)used * ntiles;
   const int64_t chunk = (total + kXcds - 1) / kXcds;
@@ -394,7 +395,7 @@ bool whole_steps(const Fp4GemmParams& p) {
 
 template <typename T, int RB, int SPLIT, int D>
 hipError_t launch_stream(const Fp4GemmParams& p, hipStream_t stream) {
-  const int64_t units = (int64_t)(p.capacity / (16 * RB)) * fp4_nblocks(p.N);
+  const int64_t units = (int64_t)(p.capacity / p.block_m) * (p.block_m / (16 * RB)) * fp4_nblocks(p.N);
   const int64_t groups = (units * SPLIT + 3) / 4;
   if (groups == 0) return hipSuccess;
   const int grid = (int)std::min<int64_t>(groups, (int64_t)device_cu_count() * 8);
@@ -431,26 +432,30 @@ hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
 }
 
 template <typename T>
-hipError_t launch(int32_t block_m, const Fp4GemmParams& p, hipStream_t stream) {
-  // the tile kernel's offsets into the rows are 32 bits
-  const bool tiles = whole_steps(p) && (int64_t)p.a_rows * (p.K / 2) < (int64_t)1 << 32;
-  if (tiles && block_m == 128) return launch_tile<T, 128>(p, stream);
-  if (tiles && block_m == 64) return launch_tile<T, 64>(p, stream);
-  switch (block_m) {
-    case 16: return launch_stream<T, 1, 4, 4>(p, stream);
-    case 32: return launch_stream<T, 2, 4, 3>(p, stream);
-    case 64: return launch_stream<T, 4, 1, 2>(p, stream);
-    case 128: return launch_stream<T, 8, 1, 1>(p, stream);
-    default: return hipErrorInvalidValue;
-  }
+hipError_t launch(const Fp4GemmParams& p, hipStream_t stream) {
+  if (p.block_m == 16) return launch_stream<T, 1, 4, 3>(p, stream);
+  if (p.block_m == 32) return launch_stream<T, 2, 4, 3>(p, stream);
+  // Tiles that the call is expected to have: its slots, half a block of padding an expert.
+  const int64_t rows = std::min<int64_t>(p.capacity, (int64_t)p.n_slots + (int64_t)p.E * (p.block_m / 2));
+  const int64_t tiles = (rows + p.block_m - 1) / p.block_m * ((fp4_nblocks(p.N) + 3) / 4);
+  // A tile goes through K alone, the streaming kernel's four waves share it: one expert,
+  // 128-row blocks, streaming against tiles: 32 tiles at K 7168 25 against 34 us, 64 tiles 46
+  // against 34; 32 tiles at K 2048 11 against 13, 64 tiles 19 against 13.
+  // The tile kernel's offsets into the rows are 32 bits.
+  if (tiles >= 48 && whole_steps(p) && (int64_t)p.a_rows * (p.K / 2) < (int64_t)1 << 32)
+    return p.block_m == 128 ? launch_tile<T, 128>(p, stream) : launch_tile<T, 64>(p, stream);
+  // K that ends inside a step: 64 rows a wave once there are many (2080 by 4096 columns:
+  // 500 rows 16 against 15 us, 4000 rows 69 against 113).
+  if (tiles >= 128) return launch_stream<T, 4, 1, 2>(p, stream);
+  return launch_stream<T, 2, 4, 3>(p, stream);
 }
 
 }  // namespace
 
-hipError_t launch_fp4_gemm(int32_t block_m, const Fp4GemmParams& p, int32_t out_dtype, hipStream_t stream) {
-  if (out_dtype == kBF16) return launch<bf16_t>(block_m, p, stream);
-  if (out_dtype == kFP16) return launch<f16_t>(block_m, p, stream);
-  return launch<float>(block_m, p, stream);
+hipError_t launch_fp4_gemm(const Fp4GemmParams& p, int32_t out_dtype, hipStream_t stream) {
+  if (out_dtype == kBF16) return launch<bf16_t>(p, stream);
+  if (out_dtype == kFP16) return launch<f16_t>(p, stream);
+  return launch<float>(p, stream);
 }
 
 }  // namespace w4a16
