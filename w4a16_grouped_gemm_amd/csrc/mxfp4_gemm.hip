@@ -398,11 +398,11 @@ hipError_t launch_stream(const Fp4GemmParams& p, hipStream_t stream) {
   const int64_t units = (int64_t)(p.capacity / p.block_m) * (p.block_m / (16 * RB)) * fp4_nblocks(p.N);
   const int64_t groups = (units * SPLIT + 3) / 4;
   if (groups == 0) return hipSuccess;
-  const int grid = (int)std::min<int64_t>(groups, (int64_t)device_cu_count() * 8);
+  const dim3 grid((unsigned)std::min<int64_t>(groups, (int64_t)device_cu_count() * 64)), threads(256);
   if (!whole_steps(p))
-    hipLaunchKernelGGL((fp4_stream_kernel<T, RB, SPLIT, D, true>), dim3(grid), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((fp4_stream_kernel<T, RB, SPLIT, D, true>), grid, threads, 0, stream, p);
   else
-    hipLaunchKernelGGL((fp4_stream_kernel<T, RB, SPLIT, D, false>), dim3(grid), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((fp4_stream_kernel<T, RB, SPLIT, D, false>), grid, threads, 0, stream, p);
   return hipGetLastError();
 }
 
