@@ -212,8 +212,8 @@ __device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
 // columns, a wave all of its rows times 64 columns, on 32 x 32 x 64 MFMAs. A
 // wave's weights are its own and go from memory to registers; the rows are shared,
 // so each wave fetches its part of them and all read them from LDS. Both are
-// fetched two steps of K = 128 ahead; one barrier per step. The loop goes by two
-// steps; one past the last repeats the last one's weights with zero rows.
+// fetched two steps of K = 128 ahead. The loop goes by turns of two steps with a
+// barrier each; a step past the last repeats the last one's weights with zero rows.
 //
 // Rows are fetched with four neighbouring lanes on a row's 64 bytes, since the
 // vector cache takes one line of four lanes at a time, and lie in LDS as they
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
   constexpr int kBlocks = BM / 32;  // row blocks
   constexpr int kMine = BM / 64;    // 16-row parts that a wave fetches
   constexpr int kAhead = 2;         // row fragments read from LDS before their use
-  __shared__ i32x4 rows_lds[D][BM][4];
+  __shared__ i32x4 rows_lds[2][D][BM][4];  // turn, step, row, chunk
   __shared__ uint32_t scales_lds[2][G][BM];  // group, step, row: the scales of its four k blocks
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
     for (int i = 0; i < kMine; ++i) {
       const int row = 16 * (wave * kMine + i) + (lane >> 2);
       aq[i] = source(row) * (uint32_t)(p.K / 2) + 16 * (lane & 3);
-      put[i] = &rows_lds[0][row][(lane & 3) ^ (row >> 1 & 3)];
+      put[i] = &rows_lds[0][0][row][(lane & 3) ^ (row >> 1 & 3)];
     }
     const bool scaler = wave < BM / 64;  // this wave fetches scales, a row a thread
     const uint32_t as = scaler ? source(tid) * (uint32_t)(p.K / 32) : 0;
@@ -271,19 +271,22 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
 #pragma unroll
       for (int i = 0; i < kMine; ++i) a[slot][i] = a_q.load4(aq[i], 64 * min(step, last));
     };
-    auto publish_rows = [&](int slot, int step) {
-      const int keep = step <= last ? -1 : 0;
+    auto publish_rows = [&](int turn) {
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) put[i][slot * BM * 4] = a[slot][i] & keep;
+      for (int d = 0; d < D; ++d) {
+        const int keep = D * turn + d <= last ? -1 : 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) put[i][((turn & 1) * D + d) * BM * 4] = a[d][i] & keep;
+      }
     };
-    auto fetch_scales = [&](int group) {  // last + 1 is a multiple of G
-      const int at = 4 * G * min(group, last / G);
-      if (G == 4) {
-        const i32x4 got = a_s.load4(as, at);
+    auto fetch_scales = [&](int group) {
+      if (G == 4) {  // last + 1 is a multiple of 4
+        const i32x4 got = a_s.load4(as, 4 * G * min(group, last / G));
 #pragma unroll
         for (int g = 0; g < G; ++g) sc[g] = (uint32_t)got[g];
       } else {
-        sc[0] = a_s.load(as, at);
+#pragma unroll
+        for (int g = 0; g < G; ++g) sc[g] = a_s.load(as, 4 * min(G * group + g, last));
       }
     };
     auto publish_scales = [&](int group) {
@@ -299,15 +302,8 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
         ws[slot][h] = wp.load(wscales + 128 * h, at);
       }
     };
-    // step s, in ring slot d: the slot written here was last read a barrier ago
-    auto compute = [&](int d, int s) {
-      const int next = (d + 1) % D;
-      publish_rows(next, s + 1);
-      fetch_rows(next, s + 1 + D);
-      if (scaler && s % G == 0) {
-        publish_scales(s / G + 1);
-        fetch_scales(s / G + 2);
-      }
+    auto compute = [&](int d, int turn) {
+      const int s = D * turn + d;
       // bytes 0 and 2: of the rows' scales, this lane's k block in each half of K; of the
       // columns', this lane's two columns
       uint32_t rs[kBlocks], cs[2];
@@ -319,7 +315,7 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
       i32x4 av[kAhead + 1];
       auto fragment = [&](int f) {
         const int row = 32 * (f % kBlocks) + (lane & 31), chunk = 2 * (f / kBlocks) + (lane >> 5);
-        av[f % (kAhead + 1)] = rows_lds[d][row][chunk ^ (row >> 1 & 3)];
+        av[f % (kAhead + 1)] = rows_lds[turn & 1][d][row][chunk ^ (row >> 1 & 3)];
       };
 #pragma unroll
       for (int f = 0; f < kAhead; ++f) fragment(f);
@@ -334,7 +330,6 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
         __builtin_amdgcn_sched_barrier(0);
       }
       fetch_weights(d, s + D);
-      lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
     };
     if (scaler) fetch_scales(0);
@@ -348,12 +343,23 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
       publish_scales(0);
       fetch_scales(1);
     }
-    publish_rows(0, 0);
-    fetch_rows(0, D);
-    lds_barrier();
-    for (int s = 0; s <= last; s += D) {
+    publish_rows(0);
 #pragma unroll
-      for (int d = 0; d < D; ++d) compute(d, s + d);
+    for (int d = 0; d < D; ++d) fetch_rows(d, D + d);
+    lds_barrier();
+    for (int turn = 0; D * turn <= last; ++turn) {
+      // the next turn's rows and scales, into what was last read a barrier ago
+      publish_rows(turn + 1);
+#pragma unroll
+      for (int d = 0; d < D; ++d) fetch_rows(d, D * (turn + 2) + d);
+      if (scaler && D * turn % G == 0) {
+        publish_scales(D * turn / G + 1);
+        fetch_scales(D * turn / G + 2);
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) compute(d, turn);
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -428,7 +434,7 @@ hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
 template <typename T, int BM>
 hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
   if (p.K / kFp4StepK % 4 == 0) return launch_tile<T, BM, 4>(p, stream);
-  return launch_tile<T, BM, 1>(p, stream);
+  return launch_tile<T, BM, 2>(p, stream);
 }
 
 template <typename T>
