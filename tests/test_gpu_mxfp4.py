@@ -390,3 +390,48 @@ def test_expert_layer_in_four_bits():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(y[:M], want_y), k
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 values quantised and back, and a product whose rows are more than 4 GiB of codes: the
+    last rows against the same rows alone."""
+    say("far offsets")
+    rows, K = 600064, 7168
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda").normal_()
+    assert rows * K > 2**32
+    q, s = torch.zeros(rows, K // 2, dtype=torch.uint8, device="cuda"), torch.zeros(rows, K // 32, dtype=torch.uint8, device="cuda")
+    w.mxfp4_quantize(x, q, s)
+    tail = x[-96:].clone()
+    tq, ts = run_quantize(tail)
+    assert torch.equal(q[-96:], tq) and torch.equal(s[-96:], ts)
+    w.mxfp4_dequantize(q, s, x)
+    back = torch.zeros_like(tail)
+    w.mxfp4_dequantize(tq, ts, back)
+    assert torch.equal(x[-96:], back)
+    h = torch.zeros(rows, K // 4, dtype=torch.uint8, device="cuda")
+    hs = torch.zeros(rows, K // 64, dtype=torch.uint8, device="cuda")
+    w.mxfp4_silu_mul_quantize(x, h, hs)
+    th, ths = torch.zeros(96, K // 4, dtype=torch.uint8, device="cuda"), torch.zeros(96, K // 64, dtype=torch.uint8, device="cuda")
+    w.mxfp4_silu_mul_quantize(back, th, ths)
+    assert torch.equal(h[-96:], th) and torch.equal(hs[-96:], ths)
+    del x, h, hs
+    # as a product's rows: twice as many, so that the codes pass 4 GiB
+    q, s = torch.cat([q, q]), torch.cat([s, s])
+    T = 2 * rows
+    assert T * K // 2 > 2**32
+    N, bm = 64, 128
+    c = Product(96, 1, 1, 1, N, K, bm, True, seed=14)
+    d = c.upload()
+    c.a_q, c.a_s = tq.cpu().numpy(), ts.cpu().numpy()
+    ref, size = c.reference()  # one expert, one slot a token: aligned row p is token p
+    srt = torch.arange(T + bm - 1, dtype=torch.int32, device="cuda").clamp(max=T)
+    eid = torch.zeros((T + bm - 1) // bm, dtype=torch.int32, device="cuda")
+    ntpp = dev(np.array([T], np.int32))
+    for gather in (True, False):
+        out = torch.full((T + bm - 1, N), 7.0, device="cuda")
+        a_q, a_s = (q, s) if gather else (torch.cat([q, q[: bm - 1]]), torch.cat([s, s[: bm - 1]]))
+        w.mxfp4_moe_gemm(a_q, a_s, T, 1, srt, eid, ntpp, bm, 1, d["packed"], out, gather=gather)
+        torch.cuda.synchronize()
+        assert np.all(np.abs(wide(out[T - 96 : T]) - ref[:96]) <= K * 2.0**-23 * size[:96])
+        assert torch.equal(out[rows - 96 : rows], out[T - 96 : T]) and bool((out[T:] == 7).all())
+        del a_q, a_s

@@ -319,3 +319,35 @@ def test_contiguous_layer_from_tokens():
     # each row and both outputs are off by at most half a bf16 step; the fp32 sums of the same terms by far less
     size = (wide(d.wts)[..., None] * y64).sum(1)
     assert np.all(np.abs(wide(out) - wide(routed)) <= 3.05 * 2.0**-8 * size)
+
+
+def test_offsets_past_32_bits():
+    """320000 rows of 7168: more elements than 2^31. Exact on the device: rows are copied, and with weights of
+    1/8 the weighted sum of eight equal rows is the row."""
+    T, topk, E, H, bm = 40000, 8, 16, 7168, 128
+    say("far offsets")
+    ids = torch.rand(T, E, device="cuda").topk(topk, dim=1)[1].int()
+    buf = w.align_buffers(T, topk, E, bm)
+    w.moe_align(ids, E, bm, buf["sorted_token_ids"], buf["expert_ids"], buf["num_tokens_post_padded"],
+                workspace=buf["workspace"])
+    srt, ntpp = buf["sorted_token_ids"], buf["num_tokens_post_padded"]
+    M = int(ntpp.item())
+    assert M * H > 2**31
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    xp = torch.full((M, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros(T, topk, dtype=torch.int32, device="cuda")
+    w.moe_permute(x, srt[:M], ntpp, topk, xp, rows)
+    real = srt[:M] < T * topk
+    at = torch.nonzero(real).flatten()[:: 997]
+    at = torch.cat([at, torch.nonzero(real).flatten()[-64:]])
+    assert torch.equal(xp[at], x[(srt[at] // topk).long()])
+    assert not bool(xp[torch.nonzero(~real).flatten()].any())
+    assert torch.equal(srt[rows.flatten().long()], torch.arange(T * topk, dtype=torch.int32, device="cuda"))
+    wt = torch.full((T, topk), 0.125, device="cuda")
+    out, dy, dw = torch.zeros_like(x), torch.full_like(xp, 7.0), torch.zeros_like(wt)
+    w.moe_unpermute(xp, rows, out, topk_weights=wt)
+    assert torch.equal(out, x)
+    w.moe_unpermute_backward(x, xp, rows, wt, srt[:M], ntpp, dy, dw)
+    assert torch.equal(dy[at], x[(srt[at] // topk).long()] / 8)
+    dot = (x[-64:].double() ** 2).sum(1, keepdim=True)
+    assert bool(((dw[-64:] - dot).abs() <= (H + 1) * 2.0**-24 * dot).all())

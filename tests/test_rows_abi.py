@@ -167,6 +167,8 @@ def test_binding_refuses_what_pointers_hide(lib):
     refused(INVALID, w.mxfp4_quantize, x, u8(4, 31), u8(4, 2))
     refused(UNSUPPORTED, w.mxfp4_quantize, x[:, :40], u8(4, 20), u8(4, 1))
     refused(INVALID, w.mxfp4_silu_mul_quantize, x, u8(4, 32), u8(4, 2))
+    refused(INVALID, w.mxfp4_quantize, x, u8(4, 32), u8(4, 2), num_rows=i32(0))  # not "all rows"
+    refused(INVALID, w.moe_permute, x, i32(32), i32(0), 2, xp, i32(4, 2))
     refused(INVALID, w.mxfp4_dequantize, u8(4, 32), u8(4, 3), x)
     refused(INVALID, w.mxfp4_repack, u8(2, 64, 32), u8(2, 64, 2), u8(10))
     packed = u8(w.mxfp4_packed_bytes(2, 64, 64))

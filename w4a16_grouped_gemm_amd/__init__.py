@@ -1,4 +1,4 @@
-"""W4A16 fused MoE layer for MI355X (gfx950): Python binding of the C ABI.
+"""W4A16 fused MoE layer for MI355X (gfx950), and operators for rows grouped by expert: Python binding of the C ABI.
 
 Every function here has the name of an entry point in include/w4a16_moe.h and
 does argument marshalling only: torch tensors supply device memory and the
@@ -308,6 +308,12 @@ def _int32(where: str, *tensors):
             _refuse(where, "indexes and counts are int32")
 
 
+def _count(where: str, t):
+    """A row count on the device: one int32 (an empty tensor's null pointer would mean that there is none)."""
+    if t is not None and (t.dtype is not _t().int32 or t.numel() < 1):
+        _refuse(where, "a row count is one int32")
+
+
 def _fp32(where: str, *tensors):
     float32 = _t().float32
     for t in tensors:
@@ -326,7 +332,8 @@ def moe_permute(x, sorted_token_ids, num_tokens_post_padded, topk: int, xp, slot
         _refuse(name, "xp is not [rows, hidden] of x's type")
     if rows < capacity:
         _refuse(name, "xp has fewer rows than sorted_token_ids", CAPACITY)
-    _int32(name, sorted_token_ids, num_tokens_post_padded, slot_rows)
+    _int32(name, sorted_token_ids, slot_rows)
+    _count(name, num_tokens_post_padded)
     _launch(load().moe_permute, name,
             (x.data_ptr(), _dtype(x, name), T, topk, H, sorted_token_ids.data_ptr(), capacity,
              num_tokens_post_padded.data_ptr(), xp.data_ptr(), slot_rows.data_ptr()),
@@ -380,7 +387,8 @@ def moe_unpermute_backward(dout, y, slot_rows, topk_weights, sorted_token_ids, n
         _refuse(name, "dweights is not [T, topk], or y is missing")
     if topk_weights is not None and topk_weights.shape != (T, topk):
         _refuse(name, "topk_weights is not [T, topk]")
-    _int32(name, slot_rows, sorted_token_ids, num_tokens_post_padded)
+    _int32(name, slot_rows, sorted_token_ids)
+    _count(name, num_tokens_post_padded)
     _fp32(name, topk_weights, dweights)
     capacity = 0 if sorted_token_ids is None else sorted_token_ids.numel()
     _launch(load().moe_unpermute_backward, name,
@@ -398,7 +406,7 @@ def _fp4_buffers(name: str, rows: int, K: int, q, s, num_rows):
         _refuse(name, "codes and scales are not [rows, K / 2] and [rows, K / 32]")
     if q.dtype is not uint8 or s.dtype is not uint8:
         _refuse(name, "codes and scales are uint8")
-    _int32(name, num_rows)
+    _count(name, num_rows)
 
 
 def mxfp4_quantize(x, q, s, num_rows=None, stream=None):
@@ -464,7 +472,8 @@ def mxfp4_moe_gemm(a_q, a_s, T: int, topk: int, sorted_token_ids, expert_ids, nu
         _refuse(name, "expert_ids has too few blocks")
     if _nbytes(packed) < mxfp4_packed_bytes(num_experts, N, K):
         _refuse(name, "packed is smaller than mxfp4_packed_bytes")
-    _int32(name, sorted_token_ids, expert_ids, num_tokens_post_padded)
+    _int32(name, sorted_token_ids, expert_ids)
+    _count(name, num_tokens_post_padded)
     _launch(load().mxfp4_moe_gemm, name,
             (num_experts, N, K, a_q.data_ptr(), a_s.data_ptr(), rows, 1 if gather else 0, T, topk,
              sorted_token_ids.data_ptr(), capacity, expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), block_m,
