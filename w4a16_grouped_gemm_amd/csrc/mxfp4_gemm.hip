@@ -347,6 +347,9 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
 #pragma unroll
     for (int d = 0; d < D; ++d) fetch_rows(d, D + d);
     lds_barrier();
+    // No load is on its way when the loop is entered: the compiler's waits in it would
+    // else count for this order of loads, rows last, as well and drain every turn.
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     for (int turn = 0; D * turn <= last; ++turn) {
       // the next turn's rows and scales, into what was last read a barrier ago
       publish_rows(turn + 1);
