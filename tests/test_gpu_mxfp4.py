@@ -226,6 +226,13 @@ GEMMS = [
     (700, 2, 4, 4, 1024, 512),
     (1100, 1, 1, 1, 768, 2048),
     (90, 6, 40, 64, 320, 7168),
+    # enough tiles of 256 columns for the tile kernel at block_m 64 and 128: K of one step, of odd
+    # and even numbers of steps, of whole groups of four; weights read by one row block and by several
+    (130, 8, 48, 96, 512, 128),
+    (900, 2, 6, 6, 1040, 384),
+    (640, 4, 20, 20, 272, 640),
+    (2100, 1, 1, 1, 1024, 7168),
+    (2000, 2, 4, 4, 1040, 96),  # as many, and K ends inside a step
 ]
 
 
@@ -246,21 +253,25 @@ def test_gemm_is_exact(shape, gather, bm):
         assert np.array_equal(got, rounded(ref, dtype)), (dtype, np.argwhere(got != rounded(ref, dtype))[:5])
 
 
+@pytest.mark.parametrize("shape", [(150, 2, 4, 4, 208, 672), (1000, 2, 4, 4, 1024, 1152)], ids=str)
 @pytest.mark.parametrize("bm", [16, 32, 64, 128])
-def test_gemm_wide_scales(bm):
+def test_gemm_wide_scales(shape, bm):
     """Scales over 40 powers of two: each of the K additions is off by at most one fp32 step of the terms' size."""
-    c = Product(150, 2, 4, 4, 208, 672, bm, True, seed=5, spread=40)
+    c = Product(*shape, bm, True, seed=5, spread=40)
     ref, size = c.reference()
     got = wide(c.run(torch.float32))
     assert np.all(np.abs(got - ref) <= c.K * 2.0**-23 * size)
 
 
-@pytest.mark.parametrize("bm", [16, 128])
-def test_gemm_scale_of_nan(bm):
+@pytest.mark.parametrize("shape", [(40, 2, 3, 3, 96, 320), (900, 2, 3, 3, 1024, 640), (900, 2, 3, 3, 1024, 512)], ids=str)
+@pytest.mark.parametrize("bm", [16, 64, 128])
+def test_gemm_scale_of_nan(shape, bm):
     """A scale byte of 255 makes NaN of exactly the outputs it enters: of a row, and of a column."""
-    c = Product(40, 2, 3, 3, 96, 320, bm, True, seed=6)
+    c = Product(*shape, bm, True, seed=6)
     c.a_s[7, 3] = 255
+    c.a_s[9, -1] = 255
     c.w_s[1, 17, 9] = 255
+    c.w_s[2, 95, -1] = 255
     ref, _ = c.reference()
     got = wide(c.run(torch.float32))
     assert np.isnan(ref).any() and np.array_equal(got, ref, equal_nan=True)
@@ -291,26 +302,28 @@ def test_gemm_one_expert_is_a_plain_product():
     assert np.all(np.abs(got - ref) <= c.K * 2.0**-23 * size)
 
 
-def test_gemm_unknown_blocks_and_rows():
+@pytest.mark.parametrize("T, N, bm", [(60, 64, 16), (900, 1024, 64), (900, 1024, 128)])
+def test_gemm_unknown_blocks_and_rows(T, N, bm):
     """Blocks whose expert id is outside the resident ones, and slots past T * topk, give zero rows."""
-    c = Product(60, 2, 4, 4, 64, 128, 16, True, seed=9)
+    c = Product(T, 2, 4, 4, N, 128, bm, True, seed=9)
     c.eid[1] = -1
     c.eid[2] = 4
-    c.srt[3] = 60 * 2 + 5
-    c.srt[50] = -1
+    c.srt[3] = T * 2 + 5
+    c.srt[3 * bm + 2] = -1
     got = wide(c.run(torch.float32))
-    a = values(c.a_q, c.a_s)
+    a, wt = values(c.a_q, c.a_s), [values(c.w_q[e], c.w_s[e]).T for e in range(4)]
     for p in range(c.rows):
-        s, e = c.srt[p], c.eid[p // 16]
-        ok = 0 <= s < 120 and 0 <= e < 4
-        want = a[s // 2] @ values(c.w_q[e], c.w_s[e]).T if ok else np.zeros(64)
+        s, e = c.srt[p], c.eid[p // bm]
+        ok = 0 <= s < 2 * T and 0 <= e < 4
+        want = a[s // 2] @ wt[e] if ok else np.zeros(N)
         assert np.array_equal(got[p], want), p
     assert np.all(got[c.rows :] == 7)
 
 
+@pytest.mark.parametrize("shape", [(300, 4, 8, 8, 448, 1056), (900, 2, 6, 6, 1040, 640)], ids=str)
 @pytest.mark.parametrize("bm", [16, 32, 64, 128])
-def test_gemm_runs_agree(bm):
-    c = Product(300, 4, 8, 8, 448, 1056, bm, True, seed=10, spread=30)
+def test_gemm_runs_agree(shape, bm):
+    c = Product(*shape, bm, True, seed=10, spread=30)
     first = c.run(torch.float32)
     for _ in range(5):
         assert torch.equal(c.run(torch.float32), first)
