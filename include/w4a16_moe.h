@@ -442,10 +442,10 @@ typedef enum { W4A16_BF16 = 0, W4A16_FP16 = 1, W4A16_FP32 = 2 } w4a16_dtype;
  *   xp                device [capacity, hidden] of `dtype`
  *   slot_rows         device int32 [T, topk], written: the row p of each slot, -1
  *                     where the slot has no row (expert not resident)
- * A row of 16-byte multiples in 16-byte aligned buffers moves 16 bytes at a
- * time, any other element by element; the buffers need only their element
- * type's alignment. Deterministic: the result does not depend on the order in
- * which rows are written. */
+ * The buffers need only their element type's alignment; none of them may overlap
+ * another. Deterministic: the result does not depend on the order in which rows
+ * are written. T + capacity / 32 (here and below T + rows / 32) must be under
+ * 2^23, hidden at most 2^20 (else W4A16_ERR_UNSUPPORTED). */
 int moe_permute(const void* x, int32_t dtype, int32_t T, int32_t topk, int32_t hidden,
                 const int32_t* sorted_token_ids, int32_t capacity, const int32_t* num_tokens_post_padded, void* xp,
                 int32_t* slot_rows, void* stream);
@@ -521,7 +521,8 @@ int mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const 
 
 /* The activation between the expert layer's two products, to 4 bits:
  * a = silu(gu[r, c]) * gu[r, I + c] in fp32, c in [0, I), quantised as above
- * (one rounding: a is not rounded to another type in between).
+ * (one rounding: a is not rounded to another type in between; where exp(g) is below
+ * 2^-126, a counts as zero).
  *   gu                device [rows, 2 I] of `dtype`; I a multiple of 32
  *   q, s              device uint8 [rows, I / 2] and [rows, I / 32] */
 int mxfp4_silu_mul_quantize(const void* gu, int32_t dtype, int32_t rows, int32_t I, const int32_t* num_rows,

@@ -53,7 +53,8 @@ def gemm(lib, E=4, N=64, K=64, a=FAKE, s=FAKE, a_rows=64, gather=0, T=4, topk=2,
 @pytest.mark.parametrize("change, status", [
     (dict(dtype=3), INVALID), (dict(dtype=-1), INVALID), (dict(T=-1), INVALID), (dict(topk=0), INVALID),
     (dict(H=0), INVALID), (dict(cap=-1), INVALID), (dict(topk=33), UNSUPPORTED), (dict(H=(1 << 20) + 1), UNSUPPORTED),
-    (dict(T=1 << 30, topk=2), UNSUPPORTED), (dict(cap=1 << 30), UNSUPPORTED), (dict(x=None), INVALID),
+    (dict(T=1 << 30, topk=2), UNSUPPORTED), (dict(cap=1 << 30), UNSUPPORTED), (dict(cap=1 << 28), UNSUPPORTED),
+    (dict(T=1 << 23), UNSUPPORTED), (dict(x=None), INVALID),
     (dict(srt=None), INVALID), (dict(ntpp=None), INVALID), (dict(xp=None), INVALID), (dict(rows=None), INVALID),
     (dict(x=ODD), INVALID), (dict(xp=ODD), INVALID), (dict(dtype=FP32, x=ctypes.c_void_p(0x1002)), INVALID),
 ])

@@ -698,7 +698,9 @@ bool aligned_to(const void* p, size_t size) { return (reinterpret_cast<uintptr_t
 int check_rows(int32_t T, int32_t topk, int32_t hidden, int32_t rows) {
   if (T < 0 || topk < 1 || hidden < 1 || rows < 0) return W4A16_ERR_INVALID_ARG;
   if (topk > W4A16_MAX_TOPK || hidden > kMaxRow) return W4A16_ERR_UNSUPPORTED;
-  if ((int64_t)T * topk > INT_MAX / 2 || rows > INT_MAX / 2) return W4A16_ERR_UNSUPPORTED;
+  if ((int64_t)T * topk > INT_MAX / 2) return W4A16_ERR_UNSUPPORTED;
+  // a workgroup a token and one for 32 rows; a launch has less than 2^32 threads
+  if ((int64_t)T + rows / 32 >= 1 << 23) return W4A16_ERR_UNSUPPORTED;
   return W4A16_OK;
 }
 
