@@ -4,6 +4,12 @@
 // block's largest magnitude is two DPP steps away, and the scale's exponent is
 // that magnitude's exponent less 2. Dividing by a power of two is exact, so the
 // only rounding is the conversion's (nearest, ties to even, saturating at 6).
+//
+// Bound by memory: each value is read once, 17 / 32 byte is written for it. 16384 x
+// 7168 bf16 to codes 47 us (6.3 TB/s), back 42 us (7.0 TB/s); the activation of 32768
+// rows of 2 x 2048 bf16 58 us (5.3 TB/s). Both ways together took 133 us with cached
+// accesses, 105 us with streamed loads, 90 us with streamed stores too and a grid of up
+// to 256 blocks a compute unit.
 #include "internal.h"
 #include "rows.h"
 
@@ -47,7 +53,7 @@ __device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& sca
   return code;
 }
 
-// silu(g) * u. For g < -88 exp(-g) is infinite and the result zero.
+// silu(g) * u. For g < -87 the reciprocal is below the normal numbers and the result zero.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u;
 }

@@ -76,6 +76,12 @@ __device__ __forceinline__ void store4(T* p, floatx4 v) {
 // TAIL: K may end inside a step, and what lies past it is zeroed, or the scales
 // are not aligned to 4 bytes: scales are then read one by one instead of the four
 // of a row and step at once.
+//
+// Bound by the weights' bytes, which are read once and never again, so past the
+// caches' retention: 128 tokens, top-8 of 384 experts, the 48 resident ones of 4096 x
+// 7168 (some 45 in use), 699 MB in 103 us, 6.8 TB/s of the 6.9 that such reads reach. A unit's share of memory is one
+// contiguous run of 4352 bytes a step, which is why the weights are laid out by
+// step inside a column block.
 template <typename T, int RB, int SPLIT, int D, bool TAIL>
 __global__ __launch_bounds__(256) void fp4_stream_kernel(Fp4GemmParams p) {
   constexpr int kUnits = 4 / SPLIT;
@@ -221,6 +227,14 @@ __device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
 // rows' chunks c then fall on all 32 banks. Row scales, a dword a step, are fetched
 // for G steps at once (4 where K allows it: a load of one row's scales per lane
 // takes the cache 64 lines).
+//
+// 33792 rows (16 experts) by 7168 columns, K 2048: 353 us, 2.8 PFLOP/s of the 9.4
+// that the instruction reaches by itself; 48 x 128 rows by 4096, K 7168: 136 us,
+// 5.9 TB/s. The loads of a step (24 KB a workgroup), the reads from LDS and the MFMAs
+// are each about half of its time, and the two workgroups of a compute unit
+// overlap them in part. A loop of 32 x 32 x 64 MFMAs reaches 8.9 PFLOP/s with one wave
+// a SIMD, one of 16 x 16 x 128 7.6. The accumulators of 128 x 64 values are half of a
+// wave's registers; 128 x 128 left room for one wave a SIMD: 391 against 364 us.
 template <typename T, int BM, int G, Policy W>
 __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int ntiles) {
   constexpr int D = 2;
@@ -421,12 +435,12 @@ hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
   const int64_t tiles = (int64_t)(p.capacity / BM) * ntiles;
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
   if (grid == 0) return hipSuccess;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid >= 1 << 24) return hipErrorInvalidValue;  // a launch has less than 2^32 threads
   const dim3 g((unsigned)grid), t(256);
   // Weights that one row block of their expert reads are streamed, what several read is
-  // kept in the caches: 48 x 128 rows take 151 us so and 158 us cached, 16 x 2048 rows
-  // 377 us cached and 457 us streamed. The counts are on the device; n_slots over E is
-  // the most that is to be expected.
+  // kept in the caches: 48 x 128 rows take 139 us so and 147 us cached, 16 x 2048 rows
+  // (with the activation) 358 us cached and 418 us streamed. The counts are on the
+  // device; n_slots over E is the most that is to be expected.
   if (p.n_slots <= (int64_t)p.E * BM * 3 / 2)
     hipLaunchKernelGGL((fp4_tile_kernel<T, BM, G, kStreamed>), g, t, 0, stream, p, ntiles);
   else
@@ -446,10 +460,11 @@ hipError_t launch(const Fp4GemmParams& p, hipStream_t stream) {
   if (p.block_m == 32) return launch_stream<T, 2, 4, 3>(p, stream);
   // Tiles that the call is expected to have: its slots, half a block of padding an expert.
   const int64_t rows = std::min<int64_t>(p.capacity, (int64_t)p.n_slots + (int64_t)p.E * (p.block_m / 2));
-  const int64_t tiles = (rows + p.block_m - 1) / p.block_m * ((fp4_nblocks(p.N) + 3) / 4);
-  // A tile goes through K alone, the streaming kernel's four waves share it: one expert,
-  // 128-row blocks, streaming against tiles: 32 tiles at K 7168 25 against 34 us, 64 tiles 46
-  // against 34; 32 tiles at K 2048 11 against 13, 64 tiles 19 against 13.
+  const int64_t tiles = rows * ((fp4_nblocks(p.N) + 3) / 4) / p.block_m;
+  // A tile goes through K alone, the streaming kernel's four waves share it. One expert,
+  // 128-row blocks, streaming against tiles: 32 tiles at K 7168 25 against 31 us, 56 tiles 44
+  // against 32; 32 tiles at K 2048 11 against 13, 56 tiles 18 against 13. 64-row blocks:
+  // 32 tiles at K 7168 14 against 20 us, 64 tiles 24 against 20.
   // The tile kernel's offsets into the rows are 32 bits.
   if (tiles >= 48 && whole_steps(p) && (int64_t)p.a_rows * (p.K / 2) < (int64_t)1 << 32)
     return p.block_m == 128 ? launch_tile<T, 128>(p, stream) : launch_tile<T, 64>(p, stream);

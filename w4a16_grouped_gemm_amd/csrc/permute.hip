@@ -149,7 +149,10 @@ __device__ __forceinline__ void in_groups(uint64_t has, F f) {
   if (left & 1) f(Width<1>{}, has);
 }
 
-// One block per token and `cols` columns, a multiple of 8.
+// One block per token and `cols` columns, a multiple of 8. Bound by reading y once:
+// 32768 rows of 7168 bf16 into 4096 tokens take 94 us, 5.6 TB/s; the rows of up to eight
+// slots are in flight at once, and the columns past whole groups are apart, for
+// with a test for them inside the loop the loads came one at a time (137 us).
 template <typename TY, typename TO>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(const TY* y, int32_t rows, const int32_t* slot_rows,
                                                              const float* weights, TO* out, int32_t topk, int32_t H,
@@ -211,7 +214,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // The first `pads` blocks zero the padding rows of dy; then one block per token: its
-// dy rows and weight gradients, up to eight slots at a time.
+// dy rows and weight gradients, up to eight slots at a time, so that dout and y are read
+// once for both. Bound by memory, half reads and half writes: 32768 rows of 4096
+// bf16 take 115 us, 5.0 TB/s, where a plain copy reaches 4.85.
 template <typename TO, typename TY>
 __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
     const TO* dout, const TY* y, int32_t rows, int32_t pads, const int32_t* slot_rows, const float* weights,
@@ -287,8 +292,11 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
   });
 }
 
-// Up to this many slots and aligned rows one block writes slot_rows while the others move rows.
-constexpr int32_t kByRowSlots = 4096, kByRowCapacity = 16384;
+// Up to this many slots and aligned rows one block writes slot_rows while the others move
+// rows, beyond it a token's row is read once for all of its slots. By row against by token,
+// bf16 on 48 experts, rows aligned to 128: 2048 slots of hidden 7168 16 against 23 us, 8192
+// slots 41 against 49 (hidden 1024: 10 against 15), 16384 slots 73 against 62 (16 against 15).
+constexpr int32_t kByRowSlots = 8192, kByRowCapacity = 16384;
 
 int blocks_for(int64_t items, int each) { return (int)((items + each - 1) / each); }
 
@@ -317,8 +325,9 @@ hipError_t permute(const void* x, int32_t tokens, int32_t topk, int32_t H, const
 template <typename TY, typename TO>
 hipError_t unpermute(const void* y, int32_t rows, int32_t T, int32_t topk, int32_t H, const int32_t* slot_rows,
                      const float* weights, void* out, hipStream_t stream) {
-  // few tokens: split rows over blocks for parallelism; many tokens: a block per row
-  const int32_t cols = T >= 1024 ? (H + 7) & ~7 : 8 * kThreads;
+  // A block's threads make one pass over their columns. Against a block per whole row,
+  // hidden 7168, top-8 bf16: 256 tokens 7.4 against 8.8 us, 2048 tokens 48 against 49.
+  const int32_t cols = 8 * kThreads;
   const int64_t blocks = (int64_t)T * ((H + cols - 1) / cols);
   hipLaunchKernelGGL((unpermute_kernel<TY, TO>), dim3((unsigned)blocks), dim3(kThreads), 0, stream,
                      static_cast<const TY*>(y), rows, slot_rows, weights, static_cast<TO*>(out), topk, H, cols);
