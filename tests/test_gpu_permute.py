@@ -23,6 +23,9 @@ SHAPES = [
     (300, 32, 40, 64, 40, 16),
     (2100, 8, 16, 32, 200, 128),
     (1200, 12, 13, 13, 2056, 32),
+    (1100, 8, 12, 15, 1001, 64),
+    (40, 4, 160, 160, 77, 128),
+    (2050, 5, 9, 9, 4101, 128),
 ]
 
 
@@ -351,3 +354,19 @@ def test_offsets_past_32_bits():
     assert torch.equal(dy[at], x[(srt[at] // topk).long()] / 8)
     dot = (x[-64:].double() ** 2).sum(1, keepdim=True)
     assert bool(((dw[-64:] - dot).abs() <= (H + 1) * 2.0**-24 * dot).all())
+
+
+def test_more_column_passes_than_a_launch_has_workgroups():
+    """4 Mi tokens of two passes of 2048 columns each: a workgroup takes a whole row. Exact: one slot a token, weight 1."""
+    T, H = (1 << 22) + 5, 2057
+    say("many tokens")
+    y = torch.randn(7, H, device="cuda").bfloat16()
+    rows = torch.full((T, 1), -1, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 1, 1 << 20, (1 << 21) - 1, 1 << 21, T - 2, T - 1], device="cuda")
+    rows[at, 0] = torch.arange(7, dtype=torch.int32, device="cuda")
+    out = torch.full((T, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    w.moe_unpermute(y, rows, out)
+    assert torch.equal(out[at], y)
+    out[at] = 0
+    for part in out.split(1 << 19):
+        assert not bool(part.any())
