@@ -228,9 +228,9 @@ __device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
 // for G steps at once (4 where K allows it: a load of one row's scales per lane
 // takes the cache 64 lines).
 //
-// 33792 rows (16 experts) by 7168 columns, K 2048: 353 us, 2.8 PFLOP/s of the 9.4
-// that the instruction reaches by itself; 48 x 128 rows by 4096, K 7168: 136 us,
-// 5.9 TB/s. The loads of a step (24 KB a workgroup), the reads from LDS and the MFMAs
+// 32768 rows (16 experts) by 7168 columns, K 2048: 359 us with the activation in
+// front, some 300 without, 3.2 PFLOP/s of the 9.4 that the instruction reaches by
+// itself; 48 x 128 rows by 4096, K 7168: 140 us, 5.7 TB/s. The loads of a step (24 KB a workgroup), the reads from LDS and the MFMAs
 // are each about half of its time, and the two workgroups of a compute unit
 // overlap them in part. A loop of 32 x 32 x 64 MFMAs reaches 8.9 PFLOP/s with one wave
 // a SIMD, one of 16 x 16 x 128 7.6. The accumulators of 128 x 64 values are half of a
