@@ -180,3 +180,52 @@ def test_binding_refuses_what_pointers_hide(lib):
     refused(CAPACITY, w.mxfp4_moe_gemm, *args, packed, out[:31])
     refused(UNSUPPORTED, w.mxfp4_moe_gemm, *args, packed, out.double())
     refused(INVALID, w.mxfp4_moe_gemm, u8(32, 32), u8(32, 2), 4, 2, i32(32), i32(1), i32(1), 16, 2, packed, out)
+
+
+BIG = 1 << 32  # a size of 2^32 + n is n in 32 bits
+
+
+def test_binding_refuses_sizes_past_32_bits(lib):
+    """A size that 32 bits do not hold is refused as the C ABI refuses one past its limits, not cut to its low
+    bits. Tensors of the meta device have shapes only; a call that gets past the sizes says that they are on no GPU."""
+    def meta(*shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    i32 = lambda *shape: meta(*shape, dtype=torch.int32)  # noqa: E731
+    u8 = lambda *shape: meta(*shape, dtype=torch.uint8)  # noqa: E731
+    f32 = lambda *shape: meta(*shape, dtype=torch.float32)  # noqa: E731
+    far, wide = BIG + 4, BIG + 64
+    # hidden, tokens, capacity
+    refused(UNSUPPORTED, w.moe_permute, meta(4, wide), i32(32), i32(1), 2, meta(32, wide), i32(4, 2))
+    refused(UNSUPPORTED, w.moe_permute, meta(far, 64), i32(32), i32(1), 2, meta(32, 64), i32(far, 2))
+    refused(UNSUPPORTED, w.moe_permute, meta(4, 64), i32(BIG + 32), i32(1), 2, meta(BIG + 32, 64), i32(4, 2))
+    refused(UNSUPPORTED, w.moe_permute, meta(4, 64), i32(32), i32(1), BIG + 2, meta(32, 64), i32(4, BIG + 2))
+    refused(UNSUPPORTED, w.moe_permute_backward, meta(BIG + 32, 64), i32(4, 2), meta(4, 64))
+    refused(UNSUPPORTED, w.moe_permute_backward, meta(32, wide), i32(4, 2), meta(4, wide))
+    refused(UNSUPPORTED, w.moe_unpermute, meta(BIG + 32, 64), i32(4, 2), meta(4, 64))
+    refused(UNSUPPORTED, w.moe_unpermute, meta(32, 64), i32(far, 2), meta(far, 64))
+    refused(UNSUPPORTED, w.moe_unpermute_backward, meta(4, 64), meta(BIG + 32, 64), i32(4, 2), None, i32(32), i32(1),
+            meta(BIG + 32, 64), f32(4, 2))
+    refused(UNSUPPORTED, w.moe_unpermute_backward, meta(4, wide), meta(32, wide), i32(4, 2), None, i32(32), i32(1),
+            meta(32, wide), f32(4, 2))
+    refused(UNSUPPORTED, w.moe_unpermute_backward, meta(4, 64), meta(32, 64), i32(4, 2), None, i32(BIG + 32), i32(1),
+            meta(32, 64), f32(4, 2))
+    for rows, K in [(far, 64), (4, wide)]:
+        q, s = u8(rows, K // 2), u8(rows, K // 32)
+        refused(UNSUPPORTED, w.mxfp4_quantize, meta(rows, K), q, s)
+        refused(UNSUPPORTED, w.mxfp4_silu_mul_quantize, meta(rows, 2 * K), q, s)
+        refused(UNSUPPORTED, w.mxfp4_dequantize, q, s, meta(rows, K))
+    for E, N, K in [(BIG + 1, 64, 64), (1, wide, 64), (1, 64, wide)]:
+        refused(UNSUPPORTED, w.mxfp4_packed_bytes, E, N, K)
+        refused(UNSUPPORTED, w.mxfp4_repack, u8(E, N, K // 2), u8(E, N, K // 32), u8(1 << 40))
+    good = dict(a_q=u8(32, 32), a_s=u8(32, 2), T=4, topk=2, sorted_token_ids=i32(32), expert_ids=i32(2),
+                num_tokens_post_padded=i32(1), block_m=16, num_experts=2, packed=u8(1 << 40), out=f32(32, 64))
+    refused(INVALID, w.mxfp4_moe_gemm, **good)  # on no GPU
+    for change in (dict(a_q=u8(far, 32), a_s=u8(far, 2)), dict(a_q=u8(32, wide // 2), a_s=u8(32, wide // 32)),
+                   dict(T=far), dict(topk=BIG + 2), dict(block_m=BIG + 16), dict(num_experts=BIG + 2),
+                   dict(out=f32(32, wide)),
+                   dict(sorted_token_ids=i32(BIG + 32), expert_ids=i32(BIG // 16 + 2), out=f32(BIG + 32, 64))):
+        refused(UNSUPPORTED, w.mxfp4_moe_gemm, **{**good, **change})
+    # what is too small stays an invalid argument
+    for change in (dict(T=-BIG + 4), dict(topk=-BIG + 2), dict(num_experts=-BIG + 2)):
+        refused(INVALID, w.mxfp4_moe_gemm, **{**good, **change})
