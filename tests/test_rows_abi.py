@@ -229,3 +229,37 @@ def test_binding_refuses_sizes_past_32_bits(lib):
     # what is too small stays an invalid argument
     for change in (dict(T=-BIG + 4), dict(topk=-BIG + 2), dict(num_experts=-BIG + 2)):
         refused(INVALID, w.mxfp4_moe_gemm, **{**good, **change})
+
+
+def test_readme_example_makes_what_it_reads():
+    """The README's 4-bit layer, with calls that only note their buffers: each buffer is the program's input or was
+    written by an earlier call."""
+    import os
+    import re
+
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
+        code, = [c for c in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "mxfp4_moe_gemm" in c]
+    made = {"topk_ids", "topk_weights", "x", "w13_packed", "w2_packed"}
+    writes = {"moe_align": ("sorted_token_ids", "expert_ids", "num_tokens_post_padded", "workspace"),
+              "moe_permute": ("xp", "slot_rows"), "mxfp4_quantize": ("q", "s"), "mxfp4_silu_mul_quantize": ("q", "s"),
+              "mxfp4_moe_gemm": ("out",), "moe_unpermute": ("out",)}
+    sizes = {"T": 4, "topk": 2, "E": 8, "bm": 16}
+
+    class Calls:
+        def __getattr__(self, name):
+            import inspect
+
+            def call(*args, **kw):
+                given = inspect.signature(getattr(w, name)).bind(*args, **kw).arguments
+                for k, v in given.items():
+                    if isinstance(v, str) and k not in writes[name]:
+                        assert v in made, f"{name} reads {v}, which no earlier call has written"
+                made.update(given[k] for k in writes[name] if k in given)
+            return call
+
+    class Names(dict):
+        def __missing__(self, name):
+            return name
+
+    exec(code, {}, Names(w=Calls(), **sizes))
+    assert "out" in made
