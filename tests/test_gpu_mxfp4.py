@@ -448,3 +448,160 @@ def test_offsets_past_32_bits():
         assert np.all(np.abs(wide(out[T - 96 : T]) - ref[:96]) <= K * 2.0**-23 * size[:96])
         assert torch.equal(out[rows - 96 : rows], out[T - 96 : T]) and bool((out[T:] == 7).all())
         del a_q, a_s
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_silu_mul_quantize_at_the_ends(dtype):
+    """Blocks of one g each, from the flush below exp(g) = 2^-126 to infinities and NaN, against rows of u over the
+    type's range. Tolerance of what stays finite: as in test_silu_mul_quantize; g of -87 is 126 halvings, an argument
+    of exp2 rounded by 2^-18 and a constant by 2^-25 of it, together within 2 * 87 * 2^-24 of the result."""
+    t = TYPES[dtype]
+    inf, nan = float("inf"), float("nan")
+    gs = torch.tensor([-inf, -1000, -100, -88, -87.5, -87, -50, -1, -0.0, 0, 1, 50, 87, 88, 100, 1000, inf, nan]).to(t)
+    gen = torch.Generator().manual_seed(15)
+    top = 14 if dtype == "fp16" else 120
+    us = [torch.randn(32, generator=gen) * 2.0**e for e in (0, top, -top, 5, -5)]
+    us += [torch.where(torch.arange(32) == 7, torch.tensor(v), torch.randn(32, generator=gen)) for v in (inf, -inf, nan)]
+    us = torch.stack(us).to(t)  # one row of the operator each
+    rows, I = len(us), 32 * len(gs)
+    gu = torch.cat([gs.repeat_interleave(32).expand(rows, I), us.repeat(1, len(gs))], 1).contiguous().cuda()
+    q = torch.full((rows, I // 2), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows, I // 32), 0x55, dtype=torch.uint8, device="cuda")
+    w.mxfp4_silu_mul_quantize(gu, q, s)
+    torch.cuda.synchronize()
+    g, u = wide(gu)[:, :I], wide(gu)[:, I:]
+    with np.errstate(over="ignore", invalid="ignore"):
+        flushed = np.exp(g) < 2.0**-126
+        a = np.where(flushed & np.isfinite(g), 0 * u, g / (1 + np.exp(-g)) * u)
+        a = np.where(np.abs(a) > 3.4028235e38, np.inf * a, a)  # none lies near fp32's largest value
+    blocks = a.reshape(rows, -1, 32)
+    assert not np.any(np.isfinite(blocks) & (np.abs(blocks) > 3.3e38))
+    finite = np.isfinite(blocks).all(-1)
+    got_s, got_q = s.cpu().numpy(), q.cpu().numpy()
+    code = np.stack((got_q & 15, got_q >> 4), -1).reshape(rows, I)
+    assert np.array_equal(got_s == 255, ~finite)
+    assert not finite[:, [0, -1, -2]].any() and finite[0, 1:-2].all() and not finite[5:].any()
+    assert not code.reshape(rows, -1, 32)[~finite].any()
+    zero = (np.abs(blocks) == 0).all(-1)
+    assert not got_s[zero].any() and not (code.reshape(rows, -1, 32)[zero] & 7).any()
+    rel = (8 + 2 * np.where(np.isfinite(g), np.abs(g), 0)) * 2.0**-24
+    kept = np.where(np.repeat(finite, 32, axis=1), a, 0)
+    low, high = quantize(kept * (1 - rel)), quantize(kept * (1 + rel))
+    live = finite & ~zero
+    assert np.all(((got_s == low[1]) | (got_s == high[1]))[live])
+    same = np.repeat(live & (low[1] == high[1]), 32, axis=1)
+    assert np.all(((code == low[0]) | (code == high[0]))[same])
+
+
+@pytest.mark.parametrize("bm", [16, 32, 64, 128])
+@pytest.mark.parametrize("shape", [(90, 6, 40, 64, 320, 7168), (2100, 1, 1, 1, 1024, 7168)], ids=str)
+def test_gemm_long_rows_in_fp16(shape, bm):
+    """As test_gemm_is_exact, with rows 2^6 smaller: 7168 products of at most 144 / 64 stay below fp16's largest value."""
+    c = Product(*shape, bm, True, seed=16)
+    c.a_s -= 6
+    ref, _ = c.reference()
+    assert np.array_equal(wide(c.run(torch.float16)), rounded(ref, torch.float16))
+
+
+@pytest.mark.parametrize("bm", [16, 64, 128])
+def test_gemm_smallest_scales(bm):
+    """The scale byte 0 is 2^-127. Products below 2^-126 may count as zero, each and each partial sum then off by that."""
+    for a_scale, w_scale in [(0, 227), (227, 0), (0, 0), (37, 90), (0, 120)]:
+        c = Product(900, 1, 2, 2, 1024, 128, bm, False, seed=17)
+        c.a_s[:], c.w_s[:] = a_scale, w_scale
+        ref, _ = c.reference()
+        got = wide(c.run(torch.float32))
+        if a_scale + w_scale == 227:
+            assert np.array_equal(got, rounded(ref, torch.float32)), (a_scale, w_scale)
+        assert np.all(np.abs(got - ref) <= 2 * c.K * 2.0**-126), (a_scale, w_scale)
+
+
+@pytest.mark.parametrize("bm", [16, 32, 64, 128])
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("shape", [(64, 8, 8, 8, 512, 1024), (900, 2, 6, 6, 1040, 384), (2100, 1, 1, 1, 1024, 512)], ids=str)
+def test_gemm_scales_at_any_byte(shape, gather, bm):
+    """Row scales that start one byte into their buffer, with K of whole steps."""
+    c = Product(*shape, bm, gather, seed=18)
+    ref, _ = c.reference()
+    d = c.upload()
+    d["a_s"] = torch.cat([d["a_s"].flatten()[:1], d["a_s"].flatten()])[1:].view(c.a_s.shape)
+    assert d["a_s"].data_ptr() % 4 == 1
+    assert np.array_equal(wide(c.run(torch.float32)), ref)
+
+
+@pytest.mark.parametrize("bm", [64, 128])
+def test_tile_kernel_offsets_past_31_bits(bm):
+    """Just under 4 GiB of row codes, the most that the tile kernel's 32-bit offsets take: the rows on both sides of
+    2 GiB, the last ones, and the slot order turned round, exactly."""
+    say("tile kernel, far offsets", bm)
+    T, N, K = 1198200, 64, 7168
+    rows = T + bm - 1
+    assert 2**32 - 2**20 < rows * (K // 2) < 2**32
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    a_q = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    a_s = torch.randint(127, 129, (rows, K // 32), dtype=torch.uint8, device="cuda", generator=gen)
+    c = Product(96, 1, 1, 1, N, K, bm, True, seed=20)
+    packed, wt = c.upload()["packed"], values(c.w_q[0], c.w_s[0]).T
+    srt = torch.arange(rows, dtype=torch.int32, device="cuda").clamp(max=T)
+    turned = torch.where(srt < T, T - 1 - srt, srt)
+    eid = torch.zeros((rows + bm - 1) // bm, dtype=torch.int32, device="cuda")
+    used = (T + bm - 1) // bm * bm
+    ntpp = dev(np.array([used], np.int32))
+    half = 2**31 // (K // 2)
+    at = torch.tensor([0, 1, half - 1, half, half + 1, T // 2, T - 65, T - 2, T - 1], device="cuda")
+    ref = values(a_q[at].cpu().numpy(), a_s[at].cpu().numpy()) @ wt
+    for gather, order in ((True, srt), (False, srt), (True, turned)):
+        out = torch.full((rows, N), 7.0, device="cuda")
+        w.mxfp4_moe_gemm(a_q, a_s, T, 1, order, eid, ntpp, bm, 1, packed, out, gather=gather)
+        torch.cuda.synchronize()
+        where = at if order is srt else T - 1 - at
+        assert np.array_equal(wide(out[where]), ref)
+        assert not bool(out[T:used].any()) and bool((out[used:] == 7).all())
+
+
+def test_the_stream_that_is_given():
+    """Each operator on a stream given by argument, behind work there that makes its inputs, while another stream is
+    current; a stream of another GPU is refused."""
+    from types import SimpleNamespace
+
+    c = Product(130, 4, 5, 10, 272, 416, 32, True, seed=21)
+    d = c.upload()
+    x0, x1 = (torch.randn(c.T, 2 * c.K, device="cuda").bfloat16() for _ in range(2))
+    x = x0.clone()
+    byte = lambda *shape: torch.zeros(*shape, dtype=torch.uint8, device="cuda")  # noqa: E731
+    q, s, hq, hs = byte(c.T, c.K), byte(c.T, c.K // 16), byte(c.T, c.K // 2), byte(c.T, c.K // 32)
+    back, out = torch.zeros_like(x), torch.zeros(c.capacity, c.N, device="cuda")
+    packed = torch.zeros_like(d["packed"])
+    w_q = torch.zeros_like(d["w_q"])
+
+    def step(stream=None):
+        w.mxfp4_quantize(x, q, s, stream=stream)
+        w.mxfp4_dequantize(q, s, back, stream=stream)
+        w.mxfp4_silu_mul_quantize(back, hq, hs, stream=stream)
+        w.mxfp4_repack(w_q, d["w_s"], packed, stream=stream)
+        w.mxfp4_moe_gemm(hq, hs, c.T, c.topk, d["srt"], d["eid"], d["ntpp"], c.bm, c.E, packed, out, gather=True,
+                         stream=stream)
+
+    x.copy_(x1), w_q.copy_(d["w_q"])
+    step()
+    torch.cuda.synchronize()
+    outputs = (q, s, back, hq, hs, packed, out)
+    want = [t.clone() for t in outputs]
+    x.copy_(x0), w_q.zero_()
+    for t in outputs:
+        t.zero_()
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big = (big @ big).clamp(-1, 1)
+        x.copy_(x1), w_q.copy_(d["w_q"])
+    step(side)
+    side.synchronize()
+    for a, b in zip(want, outputs):
+        assert torch.equal(a, b)
+    other = SimpleNamespace(device_index=torch.cuda.current_device() + 1, cuda_stream=0)
+    with pytest.raises(w.W4A16Error) as e:
+        w.mxfp4_quantize(x, q, s, stream=other)
+    assert e.value.status == w.INVALID_ARG

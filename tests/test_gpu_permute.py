@@ -370,3 +370,43 @@ def test_more_column_passes_than_a_launch_has_workgroups():
     out[at] = 0
     for part in out.split(1 << 19):
         assert not bool(part.any())
+
+
+@pytest.mark.parametrize("T", [70, 2100])
+def test_the_stream_that_is_given(T):
+    """Each row operator on a stream given by argument, behind work there that makes its inputs, while another stream
+    is current: the small permutes' one launch and the three of many slots."""
+    topk, E, H, bm = 8, 16, 264, 32
+    plan = Plan(T, topk, E, 16, bm, seed=10)
+    x0, x1 = (torch.randn(T, H, device="cuda") for _ in range(2))
+    x = x0.clone()
+    wt = torch.rand(T, topk, device="cuda")
+    xp = torch.zeros(len(plan.srt), H, device="cuda")
+    rows = torch.full((T, topk), -1, dtype=torch.int32, device="cuda")
+    out, dx, dy, dw = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(xp), torch.zeros_like(wt)
+
+    def step(stream=None):
+        w.moe_permute(x, plan.sorted, plan.ntpp, topk, xp, rows, stream=stream)
+        w.moe_unpermute(xp, rows, out, topk_weights=wt, stream=stream)
+        w.moe_unpermute_backward(out, xp, rows, wt, plan.sorted, plan.ntpp, dy, dw, stream=stream)
+        w.moe_permute_backward(dy, rows, dx, stream=stream)
+
+    x.copy_(x1)
+    step()
+    torch.cuda.synchronize()
+    outputs = (xp, rows, out, dy, dw, dx)
+    want = [t.clone() for t in outputs]
+    x.copy_(x0)
+    for t in outputs:
+        t.zero_()
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big = (big @ big).clamp(-1, 1)
+        x.copy_(x1)
+    step(side)
+    side.synchronize()
+    for a, b in zip(want, outputs):
+        assert torch.equal(a, b)
