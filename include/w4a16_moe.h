@@ -522,14 +522,16 @@ int mxfp4_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const 
 /* The activation between the expert layer's two products, to 4 bits:
  * a = silu(gu[r, c]) * gu[r, I + c] in fp32, c in [0, I), quantised as above
  * (one rounding: a is not rounded to another type in between; where exp(g) is below
- * 2^-126, a counts as zero).
+ * 2^-126, a counts as zero; a of g = -infinity is NaN, so its block gets s = 255).
  *   gu                device [rows, 2 I] of `dtype`; I a multiple of 32
  *   q, s              device uint8 [rows, I / 2] and [rows, I / 32] */
 int mxfp4_silu_mul_quantize(const void* gu, int32_t dtype, int32_t rows, int32_t I, const int32_t* num_rows,
                             uint8_t* q, uint8_t* s, void* stream);
 
-/* The values that codes and scales stand for, rounded once to `dtype` (exact
- * in bf16 and fp32; fp16 overflows to infinity and rounds below 2^-24).
+/* The values that codes and scales stand for, rounded once to `dtype`: exact in
+ * bf16 and fp32 for every scale that mxfp4_quantize writes (a scale byte of 253 or
+ * 254 makes infinities of the magnitudes that pass 2^128); fp16 overflows to
+ * infinity and rounds below 2^-24.
  *   out               device [rows, K] of `dtype`, 16-byte aligned; q 4-byte aligned */
 int mxfp4_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K, const int32_t* num_rows, void* out,
                      int32_t dtype, void* stream);
@@ -548,7 +550,8 @@ int mxfp4_repack(int32_t num_experts, int32_t N, int32_t K, const uint8_t* w_q, 
 /* The experts' product: for every aligned row p < num_tokens_post_padded whose
  * slot sorted_token_ids[p] is real, with e the expert of its block,
  *   out[p, n] = sum_k A[r, k] * W[e, n, k],   r = sorted_token_ids[p] / topk with gather, else p,
- * on the matrix cores' 4-bit operands: products exact, sums in fp32, one rounding to
+ * on the matrix cores' 4-bit operands: products exact where they are normal numbers of
+ * fp32 (below 2^-126 they may count as zero), sums in fp32, one rounding to
  * out_dtype. Padding rows p < num_tokens_post_padded (and rows of a block whose
  * expert id lies outside [0, num_experts)) are written as zeros; later rows are
  * left as they were. A scale byte of 255 makes NaN of the outputs it enters.
@@ -559,7 +562,8 @@ int mxfp4_repack(int32_t num_experts, int32_t N, int32_t K, const uint8_t* w_q, 
  *                     without a_rows >= capacity (aligned rows: down); else W4A16_ERR_INVALID_ARG
  *   T, topk           tokens and slots per token of the alignment
  *   sorted_token_ids, capacity, expert_ids, num_tokens_post_padded, block_m
- *                     moe_align's outputs and block size
+ *                     moe_align's outputs and block size; rows of a block that does not
+ *                     lie below capacity as a whole are not touched
  *   out               device [capacity, N] of out_dtype
  * a_q, packed and out must be 16-byte aligned. No workspace; sums have a fixed
  * order, so runs on the same inputs give the same bits. */

@@ -605,3 +605,19 @@ def test_the_stream_that_is_given():
     with pytest.raises(w.W4A16Error) as e:
         w.mxfp4_quantize(x, q, s, stream=other)
     assert e.value.status == w.INVALID_ARG
+
+
+@pytest.mark.parametrize("T, N, bm", [(60, 64, 16), (900, 1024, 64), (900, 1024, 128)])
+def test_gemm_shorter_sorted_list(T, N, bm):
+    """A list that ends inside a block: the whole blocks before its end are computed, nothing behind them is written."""
+    c = Product(T, 2, 4, 4, N, 128, bm, True, seed=22)
+    ref, _ = c.reference()
+    d = c.upload()
+    assert c.rows >= 4 * bm
+    cap = c.rows - bm - bm // 2
+    out = torch.full((c.capacity, N), 7.0, device="cuda")
+    w.mxfp4_moe_gemm(d["a_q"], d["a_s"], T, 2, d["srt"][:cap], d["eid"], d["ntpp"], bm, 4, d["packed"], out[:cap],
+                     gather=True)
+    torch.cuda.synchronize()
+    whole = cap // bm * bm
+    assert np.array_equal(wide(out)[:whole], ref[:whole]) and bool((out[whole:] == 7).all())
