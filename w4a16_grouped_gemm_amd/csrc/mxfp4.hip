@@ -7,7 +7,7 @@
 //
 // Bound by memory: each value is read once, 17 / 32 byte is written for it. 16384 x
 // 7168 bf16 to codes 47 us (6.3 TB/s), back 42 us (7.0 TB/s); the activation of 32768
-// rows of 2 x 2048 bf16 58 us (5.3 TB/s). Both ways together took 133 us with cached
+// rows of 2 x 2048 bf16 54 us (5.7 TB/s). Both ways together took 133 us with cached
 // accesses, 105 us with streamed loads, 90 us with streamed stores too and a grid of up
 // to 256 blocks a compute unit.
 #include "internal.h"

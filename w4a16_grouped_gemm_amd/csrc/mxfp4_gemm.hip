@@ -224,13 +224,16 @@ __device__ __forceinline__ bool tile_of(int used, int ntiles, int& b, int& nt) {
 // Rows are fetched with four neighbouring lanes on a row's 64 bytes, since the
 // vector cache takes one line of four lanes at a time, and lie in LDS as they
 // come, row by row, the 16-byte chunk c of row r in place c ^ (r / 2 % 4): eight
-// rows' chunks c then fall on all 32 banks. Row scales, a dword a step, are fetched
+// rows' chunks c then cover 128 bytes modulo 128, while rows r and r + 8 lie on the
+// same places modulo 256. Bank conflicts are 37% of the LDS's active cycles at 48 x
+// 128 rows and 38% at 32768 (K 7168 and 2048). Row scales, a dword a step, are fetched
 // for G steps at once (4 where K allows it: a load of one row's scales per lane
 // takes the cache 64 lines).
 //
-// 32768 rows (16 experts) by 7168 columns, K 2048: 359 us with the activation in
-// front, some 300 without, 3.2 PFLOP/s of the 9.4 that the instruction reaches by
-// itself; 48 x 128 rows by 4096, K 7168: 140 us, 5.7 TB/s. The loads of a step (24 KB a workgroup), the reads from LDS and the MFMAs
+// 32768 rows (16 experts) by 7168 columns, K 2048: 317 us on inputs that change from
+// call to call, 3.0 PFLOP/s of the 9.4 that the instruction reaches by itself (300 us
+// where they stay the same; the first twenty calls after a pause take up to 381); 48 x
+// 128 rows by 4096, K 7168: 137-143 us, 5.7 TB/s. The loads of a step (24 KB a workgroup), the reads from LDS and the MFMAs
 // are each about half of its time, and the two workgroups of a compute unit
 // overlap them in part. A loop of 32 x 32 x 64 MFMAs reaches 8.9 PFLOP/s with one wave
 // a SIMD, one of 16 x 16 x 128 7.6. The accumulators of 128 x 64 values are half of a
@@ -381,7 +384,8 @@ __global__ __launch_bounds__(256, 2) void fp4_tile_kernel(Fp4GemmParams p, int n
   }
 
   // A row block at a time through LDS, so that a store covers whole 128-byte
-  // lines: 32 rows of 64 columns, rows 16 bytes apart from a bank conflict.
+  // lines: 32 rows of 64 columns, 16 bytes between rows, so that rows begin on the same
+  // place modulo 256 no nearer than 16 apart (modulo 128, no nearer than 8).
   constexpr int kPitch = 64 * (int)sizeof(T) + 16;
   constexpr int kChunks = 64 * (int)sizeof(T) / 16;  // of a row
   constexpr int kRowsAtOnce = 64 / kChunks;
@@ -440,7 +444,9 @@ hipError_t launch_tile(const Fp4GemmParams& p, hipStream_t stream) {
   // Weights that one row block of their expert reads are streamed, what several read is
   // kept in the caches: 48 x 128 rows take 139 us so and 147 us cached, 16 x 2048 rows
   // (with the activation) 358 us cached and 418 us streamed. The counts are on the
-  // device; n_slots over E is the most that is to be expected.
+  // device, so an expert's rows are taken as n_slots over E: their mean where every
+  // routed expert is resident. On a slice of the experts n_slots counts the others'
+  // slots too, and a call of one row block an expert may read its weights cached.
   if (p.n_slots <= (int64_t)p.E * BM * 3 / 2)
     hipLaunchKernelGGL((fp4_tile_kernel<T, BM, G, kStreamed>), g, t, 0, stream, p, ntiles);
   else
@@ -459,6 +465,8 @@ hipError_t launch(const Fp4GemmParams& p, hipStream_t stream) {
   if (p.block_m == 16) return launch_stream<T, 1, 4, 3>(p, stream);
   if (p.block_m == 32) return launch_stream<T, 2, 4, 3>(p, stream);
   // Tiles that the call is expected to have: its slots, half a block of padding an expert.
+  // On a slice of the experts that is more than there are (the other experts' slots count
+  // too, up to the capacity), and the rule then takes tiles earlier than the figures below say.
   const int64_t rows = std::min<int64_t>(p.capacity, (int64_t)p.n_slots + (int64_t)p.E * (p.block_m / 2));
   const int64_t tiles = rows * ((fp4_nblocks(p.N) + 3) / 4) / p.block_m;
   // A tile goes through K alone, the streaming kernel's four waves share it. One expert,

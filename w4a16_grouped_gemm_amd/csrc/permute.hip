@@ -6,8 +6,9 @@
 //   permute's gradient is unpermute with weights of 1.
 //
 // All of it is bound by memory: one token row against its (at most topk) expert
-// rows. slot_rows, the inverse of the aligned order, lets every kernel go token by
-// token, so that a token's row is read or written once. Rows are moved eight
+// rows. slot_rows, the inverse of the aligned order, lets the kernels go token by
+// token, so that a token's row is read or written once; small permutes go row by row
+// and read it once for each slot. Rows are moved eight
 // elements a thread; the last hidden % 8 columns go one a thread, so that the
 // loop over whole groups has no branches.
 #include "internal.h"
