@@ -270,7 +270,8 @@ def _refuse(where: str, what: str, status: int = INVALID_ARG):
 
 
 def _sizes(where: str, *sizes: int):
-    """The C ABI's sizes are int32, and ctypes would pass the low 32 bits of a larger one."""
+    """The C ABI's sizes are int32, and ctypes would pass the low 32 bits of a larger one. Callers look at all of
+    theirs at once first (0.07 us instead of 0.23)."""
     if max(sizes) > 0x7FFFFFFF:
         _refuse(where, "a size is past 32 bits", UNSUPPORTED)
     if min(sizes) < -0x80000000:
@@ -340,7 +341,8 @@ def moe_permute(x, sorted_token_ids, num_tokens_post_padded, topk: int, xp, slot
         _refuse(name, "xp is not [rows, hidden] of x's type")
     if rows < capacity:
         _refuse(name, "xp has fewer rows than sorted_token_ids", CAPACITY)
-    _sizes(name, T, topk, H, capacity)
+    if (T | topk | H | capacity) >> 31:
+        _sizes(name, T, topk, H, capacity)
     _int32(name, sorted_token_ids, slot_rows)
     _count(name, num_tokens_post_padded)
     _launch(load().moe_permute, name,
@@ -355,7 +357,8 @@ def moe_permute_backward(dxp, slot_rows, dx, stream=None):
     T, topk = slot_rows.shape
     if dx.shape != (T, H) or dx.dtype is not dxp.dtype:
         _refuse(name, "dx is not [T, hidden] of dxp's type")
-    _sizes(name, rows, T, topk, H)
+    if (rows | T | topk | H) >> 31:
+        _sizes(name, rows, T, topk, H)
     _int32(name, slot_rows)
     _launch(load().moe_permute_backward, name,
             (dxp.data_ptr(), _dtype(dxp, name), rows, T, topk, H, slot_rows.data_ptr(), dx.data_ptr()),
@@ -370,7 +373,8 @@ def moe_unpermute(y, slot_rows, out, topk_weights=None, stream=None):
         _refuse(name, "out is not [T, hidden]")
     if topk_weights is not None and topk_weights.shape != (T, topk):
         _refuse(name, "topk_weights is not [T, topk]")
-    _sizes(name, rows, T, topk, H)
+    if (rows | T | topk | H) >> 31:
+        _sizes(name, rows, T, topk, H)
     _int32(name, slot_rows)
     _fp32(name, topk_weights)
     _launch(load().moe_unpermute, name,
@@ -402,7 +406,8 @@ def moe_unpermute_backward(dout, y, slot_rows, topk_weights, sorted_token_ids, n
     _count(name, num_tokens_post_padded)
     _fp32(name, topk_weights, dweights)
     capacity = 0 if sorted_token_ids is None else sorted_token_ids.numel()
-    _sizes(name, rows, T, topk, H, capacity)
+    if (rows | T | topk | H | capacity) >> 31:
+        _sizes(name, rows, T, topk, H, capacity)
     _launch(load().moe_unpermute_backward, name,
             (dout.data_ptr(), _dtype(dout, name), _ptr(y), _dtype(given, name), rows, T, topk, H,
              slot_rows.data_ptr(), _ptr(topk_weights), _ptr(sorted_token_ids), capacity,
@@ -414,7 +419,8 @@ def _fp4_buffers(name: str, rows: int, K: int, q, s, num_rows):
     uint8 = _t().uint8
     if K % 32:
         _refuse(name, "rows are not a multiple of 32 long", UNSUPPORTED)
-    _sizes(name, rows, K)
+    if (rows | K) >> 31:
+        _sizes(name, rows, K)
     if q.shape != (rows, K // 2) or s.shape != (rows, K // 32):
         _refuse(name, "codes and scales are not [rows, K / 2] and [rows, K / 32]")
     if q.dtype is not uint8 or s.dtype is not uint8:
@@ -452,7 +458,8 @@ def mxfp4_dequantize(q, s, out, num_rows=None, stream=None):
 
 
 def mxfp4_packed_bytes(num_experts: int, N: int, K: int) -> int:
-    _sizes("mxfp4_packed_bytes", num_experts, N, K)
+    if (num_experts | N | K) >> 31:
+        _sizes("mxfp4_packed_bytes", num_experts, N, K)
     n = ctypes.c_size_t(0)
     _check(load().mxfp4_packed_bytes(num_experts, N, K, ctypes.byref(n)), "mxfp4_packed_bytes")
     return n.value
@@ -479,7 +486,8 @@ def mxfp4_moe_gemm(a_q, a_s, T: int, topk: int, sorted_token_ids, expert_ids, nu
     out_rows, N = out.shape
     K = 2 * half
     capacity = sorted_token_ids.numel()
-    _sizes(name, T, topk, capacity, block_m)
+    if (T | topk | capacity | block_m) >> 31:
+        _sizes(name, T, topk, capacity, block_m)
     _fp4_buffers(name, rows, K, a_q, a_s, None)
     if out_rows < capacity:
         _refuse(name, "out has fewer rows than sorted_token_ids", CAPACITY)
