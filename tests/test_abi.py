@@ -208,3 +208,14 @@ def test_binding_raises(lib):
     with pytest.raises(w.W4A16Error) as ei:
         w.w4a16_packed_bytes(w.make_shape(8, 256, 128, 128))
     assert ei.value.status == 2
+
+
+def test_layer_sources_declare_no_other_operator():
+    """The benchmark reports the HBM bytes of profiles/ only while the sources of the layer's GEMMs are those that they
+    were counted on, so what these files hold is the layer's: the row and 4-bit operators' declarations are elsewhere."""
+    import bench
+
+    for name in bench.GEMM_SOURCES:
+        with open(os.path.join(bench.ROOT, "w4a16_grouped_gemm_amd", "csrc", name)) as f:
+            found = re.findall(r"\b\w*(?:[Ff]p4|permute)\w*", f.read())
+        assert not found, (name, found)

@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "row_ops.h"
 
 using namespace w4a16;
 

@@ -10,7 +10,7 @@
 // rows of 2 x 2048 bf16 54 us (5.7 TB/s). Both ways together took 133 us with cached
 // accesses, 105 us with streamed loads, 90 us with streamed stores too and a grid of up
 // to 256 blocks a compute unit.
-#include "internal.h"
+#include "row_ops.h"
 #include "rows.h"
 
 #include <algorithm>
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* q, 
   }
 }
 
-// One thread per lane of a packed unit (see internal.h).
+// One thread per lane of a packed unit (see row_ops.h).
 __global__ __launch_bounds__(kThreads) void repack_fp4_kernel(const uint8_t* w_q, const uint8_t* w_s, int32_t N,
                                                               int32_t K, int64_t units, uint8_t* packed) {
   const int32_t nblocks = fp4_nblocks(N), steps = fp4_steps(K);

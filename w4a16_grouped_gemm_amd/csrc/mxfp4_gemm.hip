@@ -5,7 +5,7 @@
 // adds in fp32. The weights are the instruction's first operand and the
 // activation rows its second, so a lane's four results are four
 // neighbouring output columns of one row.
-#include "internal.h"
+#include "row_ops.h"
 #include "rows.h"
 
 #include <algorithm>

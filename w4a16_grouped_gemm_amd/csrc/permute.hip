@@ -11,7 +11,7 @@
 // and read it once for each slot. Rows are moved eight
 // elements a thread; the last hidden % 8 columns go one a thread, so that the
 // loop over whole groups has no branches.
-#include "internal.h"
+#include "row_ops.h"
 #include "rows.h"
 
 #include <algorithm>
