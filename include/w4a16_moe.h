@@ -24,6 +24,10 @@
  *                       rows to 4-bit floating point with a scale per 32 values, and back
  *   mxfp4_repack / mxfp4_moe_gemm
  *                       the experts' product on such operands
+ *   moe_grouped_gemm / moe_grouped_gemm_wgrad
+ *                       the experts' product on bf16 or fp16 weights and its gradients
+ *   mxfp8_quantize / mxfp8_dequantize / mxfp8_silu_mul / mxfp8_silu_mul_backward
+ *                       activations kept in 8 bits for the backward pass
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -571,6 +575,127 @@ int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q
                    int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids, int32_t capacity,
                    const int32_t* expert_ids, const int32_t* num_tokens_post_padded, int32_t block_m,
                    const void* packed, void* out, int32_t out_dtype, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The experts' product on 16-bit weights, with gradients                    */
+/* ------------------------------------------------------------------------ */
+
+/* For every aligned row p < num_tokens_post_padded whose slot sorted_token_ids[p]
+ * is real, with e the expert of its block,
+ *   out[p, n] = sum_k a[r, k] * w[e, n, k],   r = sorted_token_ids[p] / topk with gather, else p,
+ * or with `transposed` the same with w[e, k, n]: given the forward product's own weights
+ * [E, N', K'] and the gradient of its outputs as a, that is the gradient of its rows
+ * (N = K', K = N'; where the forward call gathered, moe_permute_backward then
+ * sums the rows of a token). Products are exact, sums in fp32 (values below fp32's
+ * normal numbers may count as zero), one rounding to out_dtype. Padding rows
+ * p < num_tokens_post_padded, and rows of a block whose expert id lies outside
+ * [0, num_experts), are written as zeros, whatever a holds there; later rows are left
+ * as they were. Infinities and NaN enter the outputs whose sums they are in.
+ *
+ *   num_experts, N, K  N and K multiples of 8, at most 2^20 (else W4A16_ERR_UNSUPPORTED)
+ *   a                  device [a_rows, K] of `dtype` (bf16 or fp16; fp32 is
+ *                      W4A16_ERR_UNSUPPORTED); with gather a_rows >= T (token rows), without
+ *                      a_rows >= capacity (aligned rows); else W4A16_ERR_INVALID_ARG
+ *   T, topk            tokens and slots per token of the alignment
+ *   sorted_token_ids, capacity, expert_ids, num_tokens_post_padded, block_m
+ *                      moe_align's outputs and block size; rows of a block that does not
+ *                      lie below capacity as a whole are not touched
+ *   w                  device [E, N, K], or [E, K, N] with transposed, of `dtype`: the
+ *                      weights as they are trained, no repacking
+ *   out                device [capacity, N] of out_dtype (`dtype` or fp32)
+ * a, w and out must be 16-byte aligned; out overlaps neither. No workspace; sums have a
+ * fixed order, so runs on the same inputs give the same bits. capacity / block_m *
+ * ceil(N / 128) must be under 2^23 - 8 (else W4A16_ERR_UNSUPPORTED). */
+int moe_grouped_gemm(int32_t num_experts, int32_t N, int32_t K, const void* a, int32_t dtype, int32_t a_rows,
+                     int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids, int32_t capacity,
+                     const int32_t* expert_ids, const int32_t* num_tokens_post_padded, int32_t block_m, const void* w,
+                     int32_t transposed, void* out, int32_t out_dtype, void* stream);
+
+/* Device scratch bytes of moe_grouped_gemm_wgrad: the shares' fp32 sums where
+ * several workgroups go through one expert's rows (few weights, many rows), else 0.
+ * Also 0 for invalid arguments. */
+size_t moe_grouped_gemm_wgrad_workspace_bytes(int32_t num_experts, int32_t N, int32_t K, int32_t capacity);
+
+/* Gradient of moe_grouped_gemm's weights:
+ *   dw[e, n, k] = sum_p dout[p, n] * a[r, k]   over the real rows p of the blocks of expert e,
+ * r as there, in fp32, rounded once to dw_dtype; zeros for an expert without a row. Rows
+ * without a slot add nothing, whatever dout and a hold there. With `accumulate` the sum is
+ * added to what dw holds (in fp32, one rounding): gradients of several batches.
+ *
+ *   dout               device [capacity, N] of `dtype` (bf16 or fp16)
+ *   a, a_rows, gather  as given to moe_grouped_gemm (without `transposed`)
+ *   the alignment      as there
+ *   dw                 device [E, N, K] of dw_dtype (`dtype` or fp32), every element written
+ *   workspace          device, >= moe_grouped_gemm_wgrad_workspace_bytes(num_experts, N, K,
+ *                      capacity) bytes (may be NULL when that is 0; else
+ *                      W4A16_ERR_WORKSPACE); calls that overlap need one each
+ * dout, a, dw and workspace must be 16-byte aligned; dw overlaps none of them. Sums have a
+ * fixed order. Limits of sizes as above; num_experts * (ceil(N / 128) * ceil(K / 128) + 7)
+ * must be under 2^23 (else W4A16_ERR_UNSUPPORTED). */
+int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void* dout, const void* a, int32_t dtype,
+                           int32_t a_rows, int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids,
+                           int32_t capacity, const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
+                           int32_t block_m, void* dw, int32_t dw_dtype, int32_t accumulate, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Activation checkpoints in microscaled 8-bit floating point (MXFP8)        */
+/* ------------------------------------------------------------------------ */
+
+/* The format: as MXFP4's, 32 consecutive values of a row share one scale byte s, which
+ * stands for 2^(s - 127) (255: NaN, and then all 32 values are NaN); a code is a byte (sign,
+ * four exponent bits with bias 7, three mantissa bits): magnitudes from 2^-9 up to
+ * 448 times that scale. Codes are [rows, K], scale bytes [rows, K / 32].
+ *
+ * Quantisation of a block with largest magnitude m: the scale is the smallest power
+ * of two, at least 2^-127, with m / scale <= 448 (MXFP4's rule would let values above
+ * 448 saturate; here none does), each value is divided by it (exactly) and rounded to
+ * the nearest code, ties to the even one. So a value keeps half a step, 2^-4 of itself, down
+ * to 2^-6 of the scale, and 2^-10 of the scale below that. The sign of what rounds to zero is
+ * kept. A block of zeros gets s = 0; a block that holds an infinity or a NaN gets
+ * s = 255 with codes 0.
+ *
+ * mxfp8_quantize: rows kept for the backward pass (the token rows that an expert
+ * product's weight gradient reads again).
+ *   x                 device [rows, K] of `dtype`, contiguous
+ *   K                 a multiple of 32, at most 2^20 (else W4A16_ERR_UNSUPPORTED)
+ *   num_rows          device int32 [1] or NULL: rows from *num_rows on are neither
+ *                     read nor written (num_tokens_post_padded of aligned rows)
+ *   q, s              device uint8 [rows, K] and [rows, K / 32]
+ * Row buffers and q must be 16-byte aligned, here and below. */
+int mxfp8_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const int32_t* num_rows, uint8_t* q,
+                   uint8_t* s, void* stream);
+
+/* The values that codes and scales stand for, rounded once to `dtype`: exact in fp32, and
+ * in bf16 for scales from 2^-124 on; fp16 overflows to infinity and rounds below 2^-24. Magnitudes that
+ * pass 2^128 (scale bytes that mxfp8_quantize does not write) become infinities.
+ *   out               device [rows, K] of `dtype` */
+int mxfp8_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K, const int32_t* num_rows, void* out,
+                     int32_t dtype, void* stream);
+
+/* The activation between the expert layer's two products, keeping its input in 8 bits:
+ *   h[r, c] = silu(gu[r, c]) * gu[r, I + c]   in fp32, rounded once to `dtype`,
+ * silu(g) = g / (1 + exp(-g)), and gu quantised as mxfp8_quantize does. h is of the
+ * values as given, not of the quantised ones. Where exp(-|g|) is below 2^-126 it counts as
+ * zero; g = -infinity gives NaN.
+ *   gu                device [rows, 2 I] of `dtype`; I a multiple of 32
+ *   h                 device [rows, I] of `dtype`
+ *   q, s              device uint8 [rows, 2 I] and [rows, I / 16]: the checkpoint */
+int mxfp8_silu_mul(const void* gu, int32_t dtype, int32_t rows, int32_t I, const int32_t* num_rows, void* h, uint8_t* q,
+                   uint8_t* s, void* stream);
+
+/* Its gradient, from the checkpoint: with g, u the values that q and s stand for and
+ * y = 1 / (1 + exp(-g)),
+ *   dgu[r, c]     = dh[r, c] * u * y * (1 + g * (1 - y)),
+ *   dgu[r, I + c] = dh[r, c] * g * y,
+ *   h[r, c]       = g * y * u, the activation again (for the second product's weight gradient),
+ * in fp32, each rounded once to `dtype`.
+ *   dh                device [rows, I] of `dtype`
+ *   dgu               device [rows, 2 I] of `dtype`
+ *   h                 device [rows, I] of `dtype`, or NULL where it is not wanted
+ * No output overlaps an input or another output. */
+int mxfp8_silu_mul_backward(const uint8_t* q, const uint8_t* s, const void* dh, int32_t dtype, int32_t rows, int32_t I,
+                            const int32_t* num_rows, void* dgu, void* h, void* stream);
 
 #ifdef __cplusplus
 }

@@ -24,6 +24,8 @@ __all__ = [
     "moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
     "mxfp4_quantize", "mxfp4_silu_mul_quantize", "mxfp4_dequantize", "mxfp4_packed_bytes", "mxfp4_repack",
     "mxfp4_moe_gemm",
+    "moe_grouped_gemm", "moe_grouped_gemm_wgrad_workspace_bytes", "moe_grouped_gemm_wgrad",
+    "mxfp8_quantize", "mxfp8_dequantize", "mxfp8_silu_mul", "mxfp8_silu_mul_backward",
 ]
 
 OK = 0
@@ -502,6 +504,127 @@ def mxfp4_moe_gemm(a_q, a_s, T: int, topk: int, sorted_token_ids, expert_ids, nu
              sorted_token_ids.data_ptr(), capacity, expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), block_m,
              packed.data_ptr(), out.data_ptr(), _dtype(out, name)),
             (a_q, a_s, sorted_token_ids, expert_ids, num_tokens_post_padded, packed, out), stream)
+
+
+def moe_grouped_gemm(a, T: int, topk: int, sorted_token_ids, expert_ids, num_tokens_post_padded, block_m: int, w, out,
+                     gather: bool = False, transposed: bool = False, stream=None):
+    """gather: a holds token rows, read through sorted_token_ids. transposed: w is [E, K, N], for the rows' gradient."""
+    name = "moe_grouped_gemm"
+    rows, K = a.shape
+    out_rows, N = out.shape
+    E = w.shape[0]
+    capacity = sorted_token_ids.numel()
+    if w.shape != ((E, K, N) if transposed else (E, N, K)):
+        _refuse(name, "w is not [E, K, N]" if transposed else "w is not [E, N, K]")
+    if w.dtype is not a.dtype:
+        _refuse(name, "w is not of a's type")
+    if out_rows < capacity:
+        _refuse(name, "out has fewer rows than sorted_token_ids", CAPACITY)
+    if block_m > 0 and expert_ids.numel() < capacity // block_m:
+        _refuse(name, "expert_ids has too few blocks")
+    if (T | topk | capacity | block_m | rows | E | K | N) >> 31:
+        _sizes(name, T, topk, capacity, block_m, rows, E, K, N)
+    _int32(name, sorted_token_ids, expert_ids)
+    _count(name, num_tokens_post_padded)
+    _launch(load().moe_grouped_gemm, name,
+            (E, N, K, a.data_ptr(), _dtype(a, name), rows, 1 if gather else 0, T, topk, sorted_token_ids.data_ptr(),
+             capacity, expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), block_m, w.data_ptr(),
+             1 if transposed else 0, out.data_ptr(), _dtype(out, name)),
+            (a, sorted_token_ids, expert_ids, num_tokens_post_padded, w, out), stream)
+
+
+def moe_grouped_gemm_wgrad_workspace_bytes(num_experts: int, N: int, K: int, capacity: int) -> int:
+    if (num_experts | N | K | capacity) >> 31:
+        _sizes("moe_grouped_gemm_wgrad_workspace_bytes", num_experts, N, K, capacity)
+    return load().moe_grouped_gemm_wgrad_workspace_bytes(num_experts, N, K, capacity)
+
+
+def moe_grouped_gemm_wgrad(dout, a, T: int, topk: int, sorted_token_ids, expert_ids, num_tokens_post_padded,
+                           block_m: int, dw, gather: bool = False, accumulate: bool = False, workspace=None,
+                           stream=None):
+    """accumulate: the gradient is added to what dw holds."""
+    name = "moe_grouped_gemm_wgrad"
+    E, N, K = dw.shape
+    rows, width = a.shape
+    capacity = sorted_token_ids.numel()
+    if width != K or dout.dim() != 2 or dout.shape[1] != N:
+        _refuse(name, "a and dout are not [rows, K] and [rows, N] of dw's [E, N, K]")
+    if dout.dtype is not a.dtype:
+        _refuse(name, "dout is not of a's type")
+    if dout.shape[0] < capacity:
+        _refuse(name, "dout has fewer rows than sorted_token_ids", CAPACITY)
+    if block_m > 0 and expert_ids.numel() < capacity // block_m:
+        _refuse(name, "expert_ids has too few blocks")
+    if (T | topk | capacity | block_m | rows | E | K | N) >> 31:
+        _sizes(name, T, topk, capacity, block_m, rows, E, K, N)
+    _int32(name, sorted_token_ids, expert_ids)
+    _count(name, num_tokens_post_padded)
+    _launch(load().moe_grouped_gemm_wgrad, name,
+            (E, N, K, dout.data_ptr(), a.data_ptr(), _dtype(a, name), rows, 1 if gather else 0, T, topk,
+             sorted_token_ids.data_ptr(), capacity, expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), block_m,
+             dw.data_ptr(), _dtype(dw, name), 1 if accumulate else 0, _ptr(workspace), _nbytes(workspace)),
+            (dout, a, sorted_token_ids, expert_ids, num_tokens_post_padded, dw, workspace), stream)
+
+
+def _fp8_buffers(name: str, rows: int, K: int, q, s, num_rows):
+    uint8 = _t().uint8
+    if K % 32:
+        _refuse(name, "rows are not a multiple of 32 long", UNSUPPORTED)
+    if (rows | K) >> 31:
+        _sizes(name, rows, K)
+    if q.shape != (rows, K) or s.shape != (rows, K // 32):
+        _refuse(name, "codes and scales are not [rows, K] and [rows, K / 32]")
+    if q.dtype is not uint8 or s.dtype is not uint8:
+        _refuse(name, "codes and scales are uint8")
+    _count(name, num_rows)
+
+
+def mxfp8_quantize(x, q, s, num_rows=None, stream=None):
+    name = "mxfp8_quantize"
+    rows, K = x.shape
+    _fp8_buffers(name, rows, K, q, s, num_rows)
+    _launch(load().mxfp8_quantize, name,
+            (x.data_ptr(), _dtype(x, name), rows, K, _ptr(num_rows), q.data_ptr(), s.data_ptr()),
+            (x, q, s, num_rows), stream)
+
+
+def mxfp8_dequantize(q, s, out, num_rows=None, stream=None):
+    name = "mxfp8_dequantize"
+    rows, K = out.shape
+    _fp8_buffers(name, rows, K, q, s, num_rows)
+    _launch(load().mxfp8_dequantize, name,
+            (q.data_ptr(), s.data_ptr(), rows, K, _ptr(num_rows), out.data_ptr(), _dtype(out, name)),
+            (q, s, out, num_rows), stream)
+
+
+def mxfp8_silu_mul(gu, h, q, s, num_rows=None, stream=None):
+    """gu [rows, 2 I] -> h [rows, I], and gu in 8 bits (q [rows, 2 I], s [rows, I / 16]) for the backward pass."""
+    name = "mxfp8_silu_mul"
+    rows, I = h.shape
+    if gu.shape != (rows, 2 * I) or gu.dtype is not h.dtype:
+        _refuse(name, "gu is not [rows, 2 I] of h's type")
+    if I % 32:
+        _refuse(name, "rows are not a multiple of 32 long", UNSUPPORTED)
+    _fp8_buffers(name, rows, 2 * I, q, s, num_rows)
+    _launch(load().mxfp8_silu_mul, name,
+            (gu.data_ptr(), _dtype(gu, name), rows, I, _ptr(num_rows), h.data_ptr(), q.data_ptr(), s.data_ptr()),
+            (gu, h, q, s, num_rows), stream)
+
+
+def mxfp8_silu_mul_backward(q, s, dh, dgu, h=None, num_rows=None, stream=None):
+    name = "mxfp8_silu_mul_backward"
+    rows, I = dh.shape
+    if dgu.shape != (rows, 2 * I) or dgu.dtype is not dh.dtype:
+        _refuse(name, "dgu is not [rows, 2 I] of dh's type")
+    if h is not None and (h.shape != dh.shape or h.dtype is not dh.dtype):
+        _refuse(name, "h is not like dh")
+    if I % 32:
+        _refuse(name, "rows are not a multiple of 32 long", UNSUPPORTED)
+    _fp8_buffers(name, rows, 2 * I, q, s, num_rows)
+    _launch(load().mxfp8_silu_mul_backward, name,
+            (q.data_ptr(), s.data_ptr(), dh.data_ptr(), _dtype(dh, name), rows, I, _ptr(num_rows), dgu.data_ptr(),
+             _ptr(h)),
+            (q, s, dh, dgu, h, num_rows), stream)
 
 
 def align_buffers(T: int, topk: int, num_experts: int, block_m: int, device="cuda"):

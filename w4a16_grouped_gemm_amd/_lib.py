@@ -55,6 +55,14 @@ SIGNATURES = {
     "mxfp4_dequantize": (ctypes.c_int, [P, P, I32, I32, P, P, I32, P]),
     "mxfp4_packed_bytes": (ctypes.c_int, [I32, I32, I32, ctypes.POINTER(SZ)]),
     "mxfp4_repack": (ctypes.c_int, [I32, I32, I32, P, P, P, P]),
+    "moe_grouped_gemm": (ctypes.c_int, [I32, I32, I32, P, I32, I32, I32, I32, I32, P, I32, P, P, I32, P, I32, P, I32, P]),
+    "moe_grouped_gemm_wgrad_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+    "moe_grouped_gemm_wgrad": (ctypes.c_int, [I32, I32, I32, P, P, I32, I32, I32, I32, I32, P, I32, P, P, I32, P, I32,
+                                              I32, P, SZ, P]),
+    "mxfp8_quantize": (ctypes.c_int, [P, I32, I32, I32, P, P, P, P]),
+    "mxfp8_dequantize": (ctypes.c_int, [P, P, I32, I32, P, P, I32, P]),
+    "mxfp8_silu_mul": (ctypes.c_int, [P, I32, I32, I32, P, P, P, P, P]),
+    "mxfp8_silu_mul_backward": (ctypes.c_int, [P, P, P, I32, I32, I32, P, P, P, P]),
     "mxfp4_moe_gemm": (ctypes.c_int, [I32, I32, I32, P, P, I32, I32, I32, I32, P, I32, P, P, I32, P, P, I32, P]),
 }
 

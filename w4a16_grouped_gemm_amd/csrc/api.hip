@@ -7,6 +7,7 @@
 
 #include <algorithm>
 
+#include "grouped_gemm.h"
 #include "internal.h"
 #include "row_ops.h"
 
@@ -855,6 +856,145 @@ int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q
   p.capacity = capacity;
   p.block_m = block_m;
   return hip_status(launch_fp4_gemm(p, out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The experts' product on 16-bit weights with its gradients; 8-bit checkpoints
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxWorkgroups = 1 << 23;  // of 512 threads: a launch has less than 2^32 threads
+
+int check_products(int32_t E, int32_t N, int32_t K, int32_t dtype, int32_t out_dtype) {
+  if (E < 1 || N < 1 || K < 1 || !dtype_ok(dtype) || !dtype_ok(out_dtype)) return W4A16_ERR_INVALID_ARG;
+  if (E > W4A16_MAX_EXPERTS || N % 8 != 0 || K % 8 != 0 || N > kMaxRow || K > kMaxRow) return W4A16_ERR_UNSUPPORTED;
+  if (dtype == W4A16_FP32 || (out_dtype != dtype && out_dtype != W4A16_FP32)) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+int check_fp8_rows(int32_t dtype, int32_t rows, int32_t K) {
+  if (!dtype_ok(dtype) || rows < 0 || K < 1) return W4A16_ERR_INVALID_ARG;
+  if (K % 32 != 0 || K > kMaxRow) return W4A16_ERR_UNSUPPORTED;
+  return W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_grouped_gemm(int32_t num_experts, int32_t N, int32_t K, const void* a, int32_t dtype, int32_t a_rows,
+                     int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids, int32_t capacity,
+                     const int32_t* expert_ids, const int32_t* num_tokens_post_padded, int32_t block_m, const void* w,
+                     int32_t transposed, void* out, int32_t out_dtype, void* stream) {
+  int st = check_products(num_experts, N, K, dtype, out_dtype);
+  if (st != W4A16_OK) return st;
+  st = check_tokens(T, topk, num_experts, block_m);
+  if (st != W4A16_OK) return st;
+  if (capacity < 0 || a_rows < (gather ? T : capacity)) return W4A16_ERR_INVALID_ARG;
+  if (T == 0 || capacity == 0) return W4A16_OK;  // no slot, no row
+  if (!a || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !w || !out) return W4A16_ERR_INVALID_ARG;
+  if (!all_aligned16(a, w, out)) return W4A16_ERR_INVALID_ARG;
+  if (grouped_workgroups(N, capacity, block_m) >= kMaxWorkgroups) return W4A16_ERR_UNSUPPORTED;
+  GroupedParams p{};
+  p.a = a;
+  p.w = w;
+  p.out = out;
+  p.sorted = sorted_token_ids;
+  p.expert_ids = expert_ids;
+  p.ntpp = num_tokens_post_padded;
+  p.E = num_experts;
+  p.N = N;
+  p.K = K;
+  p.gather = gather != 0;
+  p.topk = topk;
+  p.n_slots = T * topk;
+  p.capacity = capacity;
+  p.block_m = block_m;
+  p.transposed = transposed != 0;
+  return hip_status(launch_grouped_gemm(p, dtype, out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_grouped_gemm_wgrad_workspace_bytes(int32_t num_experts, int32_t N, int32_t K, int32_t capacity) {
+  if (check_products(num_experts, N, K, W4A16_BF16, W4A16_FP32) != W4A16_OK || capacity < 0) return 0;
+  const int32_t splits = wgrad_splits(num_experts, N, K, capacity);
+  return splits == 1 ? 0 : (size_t)splits * num_experts * N * K * sizeof(float);
+}
+
+int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void* dout, const void* a, int32_t dtype,
+                           int32_t a_rows, int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids,
+                           int32_t capacity, const int32_t* expert_ids, const int32_t* num_tokens_post_padded,
+                           int32_t block_m, void* dw, int32_t dw_dtype, int32_t accumulate, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  int st = check_products(num_experts, N, K, dtype, dw_dtype);
+  if (st != W4A16_OK) return st;
+  st = check_tokens(T, topk, num_experts, block_m);
+  if (st != W4A16_OK) return st;
+  if (capacity < 0 || a_rows < (gather ? T : capacity) || !dw) return W4A16_ERR_INVALID_ARG;
+  if (T > 0 && capacity > 0 && (!dout || !a || !sorted_token_ids || !expert_ids || !num_tokens_post_padded))
+    return W4A16_ERR_INVALID_ARG;
+  if (!all_aligned16(dout, a, dw, workspace)) return W4A16_ERR_INVALID_ARG;
+  const int32_t splits = wgrad_splits(num_experts, N, K, capacity);
+  if (wgrad_workgroups(num_experts, N, K, splits) >= kMaxWorkgroups) return W4A16_ERR_UNSUPPORTED;
+  const size_t need = moe_grouped_gemm_wgrad_workspace_bytes(num_experts, N, K, capacity);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  WgradParams p{};
+  p.dout = dout;
+  p.a = a;
+  p.dw = dw;
+  p.partial = static_cast<float*>(workspace);
+  p.sorted = sorted_token_ids;
+  p.expert_ids = expert_ids;
+  p.ntpp = num_tokens_post_padded;
+  p.E = num_experts;
+  p.N = N;
+  p.K = K;
+  p.gather = gather != 0;
+  p.topk = topk;
+  p.n_slots = T * topk;
+  p.capacity = T == 0 ? 0 : capacity;  // no slot: zeros, or dw as it was
+  p.block_m = block_m;
+  p.accumulate = accumulate != 0;
+  p.splits = splits;
+  return hip_status(launch_grouped_wgrad(p, dtype, dw_dtype, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp8_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const int32_t* num_rows, uint8_t* q,
+                   uint8_t* s, void* stream) {
+  const int st = check_fp8_rows(dtype, rows, K);
+  if (st != W4A16_OK) return st;
+  if (rows > 0 && (!x || !q || !s)) return W4A16_ERR_INVALID_ARG;
+  if (!all_aligned16(x, q)) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_quantize(x, dtype, rows, K, num_rows, q, s, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp8_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K, const int32_t* num_rows, void* out,
+                     int32_t dtype, void* stream) {
+  const int st = check_fp8_rows(dtype, rows, K);
+  if (st != W4A16_OK) return st;
+  if (rows > 0 && (!q || !s || !out)) return W4A16_ERR_INVALID_ARG;
+  if (!all_aligned16(q, out)) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_dequantize(q, s, rows, K, num_rows, out, dtype, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp8_silu_mul(const void* gu, int32_t dtype, int32_t rows, int32_t I, const int32_t* num_rows, void* h, uint8_t* q,
+                   uint8_t* s, void* stream) {
+  const int st = check_fp8_rows(dtype, rows, I);
+  if (st != W4A16_OK) return st;
+  if (rows > 0 && (!gu || !h || !q || !s)) return W4A16_ERR_INVALID_ARG;
+  if (!all_aligned16(gu, h, q)) return W4A16_ERR_INVALID_ARG;
+  return hip_status(launch_fp8_silu_mul(gu, dtype, rows, I, num_rows, h, q, s, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp8_silu_mul_backward(const uint8_t* q, const uint8_t* s, const void* dh, int32_t dtype, int32_t rows, int32_t I,
+                            const int32_t* num_rows, void* dgu, void* h, void* stream) {
+  const int st = check_fp8_rows(dtype, rows, I);
+  if (st != W4A16_OK) return st;
+  if (rows > 0 && (!q || !s || !dh || !dgu)) return W4A16_ERR_INVALID_ARG;
+  if (!all_aligned16(q, dh, dgu, h)) return W4A16_ERR_INVALID_ARG;
+  return hip_status(
+      launch_fp8_silu_mul_backward(q, s, dh, dtype, rows, I, num_rows, dgu, h, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,304 @@
+// Activation checkpoints: rows in 8-bit floating point (four exponent bits,
+// three mantissa bits) with one power-of-two scale per 32 values, and the
+// activation between the experts' products with a backward pass that reads them.
+//
+// A quad of lanes owns a block of 32, eight values a lane. The scale is the
+// smallest power of two that brings the block's largest magnitude to 448, the
+// format's largest, or below, so no value saturates; dividing by it is exact,
+// and the conversion (nearest, ties to even) is the only rounding.
+#include "row_ops.h"
+#include "rows.h"
+
+#include <algorithm>
+
+namespace w4a16 {
+namespace {
+
+constexpr int kThreads = 256;
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, quad_dpp<0xB1>(v));  // lane ^ 1
+  return max(v, quad_dpp<0x4E>(v));  // lane ^ 2
+}
+
+struct Codes {
+  uint32_t v[2];  // eight codes
+  uint32_t scale;
+};
+
+// Eight values of a lane's quarter block -> their codes and the block's scale byte. Magnitudes
+// compare as integers, so that infinities and NaN come out on top: such a block is marked 255.
+__device__ __forceinline__ Codes encode8(const float (&x)[8]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  most = quad_max(most);
+  const bool finite = most < 0x7F800000u;
+  // 448 is 1.75 * 2^8: a mantissa above 1.75 (0x600000) takes the next power of two
+  const int32_t byte = max((int32_t)((most + 0x1FFFFFu) >> 23) - 8, 0);
+  const float inverse = __uint_as_float((uint32_t)(254 - byte) << 23);  // byte <= 247 where finite: a normal number
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = finite ? x[i] * inverse : 0.f;
+  Codes c;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int word = 0;
+    word = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], word, false);
+    word = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], word, true);
+    c.v[i] = (uint32_t)word;
+  }
+  c.scale = finite ? (uint32_t)byte : 255u;
+  return c;
+}
+
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  // 2^-127 is below the normal numbers
+  return __uint_as_float(byte == 255 ? 0x7FC00000u : byte ? byte << 23 : 0x00400000u);
+}
+
+__device__ __forceinline__ void decode8(const uint32_t (&code)[2], float scale, float (&out)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[i], false);
+    const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)code[i], true);
+    out[4 * i] = lo[0] * scale;
+    out[4 * i + 1] = lo[1] * scale;
+    out[4 * i + 2] = hi[0] * scale;
+    out[4 * i + 3] = hi[1] * scale;
+  }
+}
+
+// 1 / (1 + exp(-g)) and 1 less that, neither by a difference: with t = exp(-|g|) they are
+// 1 / (1 + t) and t / (1 + t). exp(-|g|) = 2^(-|g| log2 e) with the product's rounding error
+// and the constant's put back, so that it holds to a few units in the last place at any g.
+__device__ __forceinline__ void sigmoid(float g, float& sig, float& rest) {
+  constexpr float kLog2E = 1.44269504f, kLow = 1.92596299e-8f;
+  const float x = fmaxf(-fabsf(g), -200.f);  // exp(-200) is 0; keeps an infinity out of the differences
+  const float hi = x * kLog2E;
+  const float lo = __builtin_fmaf(x, kLow, __builtin_fmaf(x, kLog2E, -hi));
+  const float t = __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, 0.693147181f, 1.f);
+  const float d = 1.f + t;
+  float inverse = __builtin_amdgcn_rcpf(d);
+  inverse = __builtin_fmaf(__builtin_fmaf(-d, inverse, 1.f), inverse, inverse);
+  const float small = t * inverse;
+  sig = g < 0.f ? small : inverse;
+  rest = g < 0.f ? inverse : small;
+}
+
+__device__ __forceinline__ int64_t live_rows(int32_t rows, const int32_t* num_rows) {
+  return num_rows ? max(0, min(rows, *num_rows)) : rows;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* q, int64_t at, const Codes& c) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(u32x2{c.v[0], c.v[1]}, reinterpret_cast<u32x2*>(q + at));
+}
+
+__device__ __forceinline__ void load_codes(const uint8_t* q, int64_t at, uint32_t (&code)[2]) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(q + at));
+  code[0] = v[0];
+  code[1] = v[1];
+}
+
+// Groups of eight values, kUnroll of them per thread, a block of threads apart; the loads of all
+// come before the first use.
+constexpr int kUnroll = 4;
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const T* x, int32_t rows, int32_t K,
+                                                            const int32_t* num_rows, uint8_t* q, uint8_t* s) {
+  const int64_t total = live_rows(rows, num_rows) * (int64_t)(K / 8);  // a multiple of 4: quads are whole
+  for (int64_t g0 = (int64_t)blockIdx.x * kThreads * kUnroll + threadIdx.x; g0 < total;
+       g0 += (int64_t)gridDim.x * kThreads * kUnroll) {
+    Eight<T> a[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (g0 + u * kThreads < total) a[u] = load8<kStreamed>(x + 8 * (g0 + u * kThreads));
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t g = g0 + u * kThreads;
+      if (g >= total) continue;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (float)a[u].v[i];
+      const Codes c = encode8(v);
+      store_codes(q, 8 * g, c);
+      if ((g & 3) == 0) s[g >> 2] = (uint8_t)c.scale;
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* q, const uint8_t* s, int32_t rows,
+                                                              int32_t K, const int32_t* num_rows, T* out) {
+  const int64_t total = live_rows(rows, num_rows) * (int64_t)(K / 8);
+  for (int64_t g0 = (int64_t)blockIdx.x * kThreads * kUnroll + threadIdx.x; g0 < total;
+       g0 += (int64_t)gridDim.x * kThreads * kUnroll) {
+    uint32_t code[kUnroll][2], byte[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t g = g0 + u * kThreads;
+      if (g >= total) continue;
+      load_codes(q, 8 * g, code[u]);
+      byte[u] = s[g >> 2];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t g = g0 + u * kThreads;
+      if (g >= total) continue;
+      float v[8];
+      decode8(code[u], scale_of(byte[u]), v);
+      Eight<T> r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.v[i] = (T)v[i];
+      store8<kStreamed>(out + 8 * g, r);
+    }
+  }
+}
+
+// Where a thread's group of eight columns lies: row r, columns c on of [rows, I].
+struct Place {
+  int64_t row;
+  int32_t column;
+};
+__device__ __forceinline__ Place place_of(int64_t group, uint32_t per_row) {
+  const int64_t row = group / per_row;
+  return {row, 8 * (int32_t)(group - row * per_row)};
+}
+
+// h = silu(gate) * up, and gate and up in 8 bits.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void silu_mul_kernel(const T* gu, int32_t rows, int32_t I,
+                                                            const int32_t* num_rows, T* h, uint8_t* q, uint8_t* s) {
+  const uint32_t per_row = (uint32_t)I / 8;
+  const int64_t total = live_rows(rows, num_rows) * (int64_t)per_row;
+  for (int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x; g < total; g += (int64_t)gridDim.x * kThreads) {
+    const Place at = place_of(g, per_row);
+    const int64_t gate_at = 2 * at.row * I + at.column, up_at = gate_at + I;
+    const Eight<T> a = load8<kStreamed>(gu + gate_at), b = load8<kStreamed>(gu + up_at);
+    float gate[8], up[8];
+    Eight<T> r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      gate[i] = (float)a.v[i];
+      up[i] = (float)b.v[i];
+      float sig, rest;
+      sigmoid(gate[i], sig, rest);
+      r.v[i] = (T)(gate[i] * sig * up[i]);
+    }
+    store8<kStreamed>(h + at.row * I + at.column, r);
+    const Codes cg = encode8(gate), cu = encode8(up);
+    store_codes(q, gate_at, cg);
+    store_codes(q, up_at, cu);
+    if ((g & 3) == 0) {
+      s[gate_at / 32] = (uint8_t)cg.scale;
+      s[up_at / 32] = (uint8_t)cu.scale;
+    }
+  }
+}
+
+// From the checkpoint: dgate = dh up sig (1 + gate (1 - sig)), dup = dh gate sig, and h again.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void silu_mul_backward_kernel(const uint8_t* q, const uint8_t* s, const T* dh,
+                                                                     int32_t rows, int32_t I, const int32_t* num_rows,
+                                                                     T* dgu, T* h) {
+  const uint32_t per_row = (uint32_t)I / 8;
+  const int64_t total = live_rows(rows, num_rows) * (int64_t)per_row;
+  for (int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x; g < total; g += (int64_t)gridDim.x * kThreads) {
+    const Place at = place_of(g, per_row);
+    const int64_t gate_at = 2 * at.row * I + at.column, up_at = gate_at + I;
+    uint32_t gate_code[2], up_code[2];
+    load_codes(q, gate_at, gate_code);
+    load_codes(q, up_at, up_code);
+    const uint32_t gate_scale = s[gate_at / 32], up_scale = s[up_at / 32];
+    const Eight<T> d = load8<kStreamed>(dh + at.row * I + at.column);
+    float gate[8], up[8];
+    decode8(gate_code, scale_of(gate_scale), gate);
+    decode8(up_code, scale_of(up_scale), up);
+    Eight<T> dg, du, again;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float sig, rest;
+      sigmoid(gate[i], sig, rest);
+      const float silu = gate[i] * sig, grad = (float)d.v[i];
+      dg.v[i] = (T)(grad * up[i] * __builtin_fmaf(silu, rest, sig));
+      du.v[i] = (T)(grad * silu);
+      again.v[i] = (T)(silu * up[i]);
+    }
+    store8<kStreamed>(dgu + gate_at, dg);
+    store8<kStreamed>(dgu + up_at, du);
+    if (h) store8<kStreamed>(h + at.row * I + at.column, again);
+  }
+}
+
+// Blocks for `items` of work of `each` per thread, up to `per_cu` a compute unit.
+dim3 grid_for(int64_t items, int each, int per_cu) {
+  const int64_t per_block = (int64_t)kThreads * each;
+  return dim3((unsigned)std::min<int64_t>((items + per_block - 1) / per_block, (int64_t)device_cu_count() * per_cu));
+}
+
+// f with a value of the type that `dtype` names.
+template <typename F>
+hipError_t typed(int32_t dtype, F f) {
+  if (dtype == kBF16)
+    f(bf16_t());
+  else if (dtype == kFP16)
+    f(f16_t());
+  else
+    f(float());
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const int32_t* num_rows,
+                               uint8_t* q, uint8_t* s, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  return typed(dtype, [&](auto t) {
+    typedef decltype(t) T;
+    hipLaunchKernelGGL((quantize_kernel<T>), grid_for((int64_t)rows * (K / 8), kUnroll, 256), dim3(kThreads), 0, stream,
+                       static_cast<const T*>(x), rows, K, num_rows, q, s);
+  });
+}
+
+hipError_t launch_fp8_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K, const int32_t* num_rows,
+                                 void* out, int32_t dtype, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  return typed(dtype, [&](auto t) {
+    typedef decltype(t) T;
+    hipLaunchKernelGGL((dequantize_kernel<T>), grid_for((int64_t)rows * (K / 8), kUnroll, 256), dim3(kThreads), 0,
+                       stream, q, s, rows, K, num_rows, static_cast<T*>(out));
+  });
+}
+
+hipError_t launch_fp8_silu_mul(const void* gu, int32_t dtype, int32_t rows, int32_t I, const int32_t* num_rows, void* h,
+                               uint8_t* q, uint8_t* s, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  return typed(dtype, [&](auto t) {
+    typedef decltype(t) T;
+    hipLaunchKernelGGL((silu_mul_kernel<T>), grid_for((int64_t)rows * (I / 8), 1, 256), dim3(kThreads), 0, stream,
+                       static_cast<const T*>(gu), rows, I, num_rows, static_cast<T*>(h), q, s);
+  });
+}
+
+hipError_t launch_fp8_silu_mul_backward(const uint8_t* q, const uint8_t* s, const void* dh, int32_t dtype, int32_t rows,
+                                        int32_t I, const int32_t* num_rows, void* dgu, void* h, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  return typed(dtype, [&](auto t) {
+    typedef decltype(t) T;
+    hipLaunchKernelGGL((silu_mul_backward_kernel<T>), grid_for((int64_t)rows * (I / 8), 1, 256), dim3(kThreads), 0,
+                       stream, q, s, static_cast<const T*>(dh), rows, I, num_rows, static_cast<T*>(dgu),
+                       static_cast<T*>(h));
+  });
+}
+
+}  // namespace w4a16

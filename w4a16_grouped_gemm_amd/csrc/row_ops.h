@@ -56,4 +56,14 @@ struct Fp4GemmParams {
 };
 hipError_t launch_fp4_gemm(const Fp4GemmParams& p, int32_t out_dtype, hipStream_t stream);
 
+// 8-bit floating point checkpoints (mxfp8.hip).
+hipError_t launch_fp8_quantize(const void* x, int32_t dtype, int32_t rows, int32_t K, const int32_t* num_rows,
+                               uint8_t* q, uint8_t* s, hipStream_t stream);
+hipError_t launch_fp8_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K, const int32_t* num_rows,
+                                 void* out, int32_t dtype, hipStream_t stream);
+hipError_t launch_fp8_silu_mul(const void* gu, int32_t dtype, int32_t rows, int32_t I, const int32_t* num_rows, void* h,
+                               uint8_t* q, uint8_t* s, hipStream_t stream);
+hipError_t launch_fp8_silu_mul_backward(const uint8_t* q, const uint8_t* s, const void* dh, int32_t dtype, int32_t rows,
+                                        int32_t I, const int32_t* num_rows, void* dgu, void* h, hipStream_t stream);
+
 }  // namespace w4a16
