@@ -908,7 +908,7 @@ int moe_grouped_gemm(int32_t num_experts, int32_t N, int32_t K, const void* a, i
   p.N = N;
   p.K = K;
   p.gather = gather != 0;
-  p.topk = topk;
+  p.by_topk = Divisor::by((uint32_t)topk);
   p.n_slots = T * topk;
   p.capacity = capacity;
   p.block_m = block_m;
@@ -951,7 +951,7 @@ int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void
   p.N = N;
   p.K = K;
   p.gather = gather != 0;
-  p.topk = topk;
+  p.by_topk = Divisor::by((uint32_t)topk);
   p.n_slots = T * topk;
   p.capacity = T == 0 ? 0 : capacity;  // no slot: zeros, or dw as it was
   p.block_m = block_m;

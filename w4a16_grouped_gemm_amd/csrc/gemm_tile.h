@@ -79,26 +79,21 @@ struct RowPanel {
   static constexpr int kUnits = kOuter / 8;  // copies of a stage, 8 rows each
   static constexpr int kMine = (kUnits + kWaves - 1) / kWaves;
   const uint8_t* at[kMine];
-  int32_t left[kMine];  // steps of r from `at` to the end
+  int32_t first[kMine];  // this lane's first step of r in a stage
 
   static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 8 * (kMine * wave + i) + lane / 8; }
   static __device__ __forceinline__ int swizzle(int row) { return row >> 1 & 7; }
 
-  // row: the start of row row_of(i, ...), or null
-  __device__ __forceinline__ void set(int i, const void* row, int32_t steps, int wave, int lane) {
-    const int chunk = (lane & 7) ^ swizzle(row_of(i, wave, lane));
-    at[i] = static_cast<const uint8_t*>(row) + 16 * chunk;
-    left[i] = row ? steps - 8 * chunk : 0;
+  // row: the start of row row_of(i, ...)
+  __device__ __forceinline__ void set(int i, const void* row, int wave, int lane) {
+    first[i] = 8 * ((lane & 7) ^ swizzle(row_of(i, wave, lane)));
+    at[i] = static_cast<const uint8_t*>(row) + 2 * first[i];
   }
-  // the next stage's copies
-  __device__ __forceinline__ void issue(uint32_t lds, int wave) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      if (kUnits >= kWaves || wave < kUnits)
-        copy16(left[i] > 0 ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * (kMine * wave + i));
-      at[i] += 2 * kStep;
-      left[i] -= kStep;
-    }
+  // copy i of the next stage, of which `left` steps are in the operand
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave) {
+    if (kUnits >= kWaves || wave < kUnits)
+      copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * (kMine * wave + i));
+    at[i] += 2 * kStep;
   }
   // steps 16 k + 8 (lane / 32) + 0..7 of row outer0 + lane % 32; outer0 a multiple of 32
   template <typename T>
@@ -110,49 +105,37 @@ struct RowPanel {
 
 // kOuter columns, contiguous at each step of r: kOuter * 2 bytes a step, in parts of 64 bytes,
 // the part c of step r in place c ^ (r % 4) (where a step has that many). Four steps' 64 bytes,
-// which half a wave reads, then lie in four places modulo 256.
-template <int kOuter>
+// which half a wave reads, then lie in four places modulo 256. kPitch: bytes between steps.
+template <int kOuter, int kPitch = kOuter * 2>
 struct ColumnPanel {
   static constexpr int kBytes = kOuter * 128;
   static constexpr int kUnits = kOuter / 8;
   static constexpr int kMine = (kUnits + kWaves - 1) / kWaves;
-  static constexpr int kPitch = kOuter * 2;
   static constexpr int kLanes = kOuter / 8;  // that copy a step
   static constexpr int kParts = kOuter / 32;
   const uint8_t* at[kMine];
-  int32_t left[kMine];
+  int32_t first[kMine];
   int64_t stride;  // bytes a stage
 
-  static __device__ __forceinline__ int step_of(int i, int wave, int lane) {
-    return (64 / kLanes) * (kMine * wave + i) + lane / kLanes;
-  }
   static __device__ __forceinline__ int swizzle(int step) {
     return kParts >= 4 ? step & 3 : kParts == 2 ? step >> 1 & 1 : 0;
   }
-  // the first of the eight columns that this lane copies
-  static __device__ __forceinline__ int column_of(int i, int wave, int lane) {
-    return 8 * ((lane % kLanes) ^ (swizzle(step_of(i, wave, lane)) << 2));
-  }
-
-  // base: step 0, column 0 of the panel; steps of ld columns, `columns` of them from `base` on
+  // base: step 0, column 0 of the panel; steps of ld columns, `columns` of them from `base` on. Columns past
+  // those are copies of column 0.
   template <typename T>
-  __device__ __forceinline__ void set(const T* base, int64_t ld, int32_t columns, int32_t steps, int wave, int lane) {
+  __device__ __forceinline__ void set(const T* base, int64_t ld, int32_t columns, int wave, int lane) {
     stride = ld * kStep * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      const int step = step_of(i, wave, lane), column = column_of(i, wave, lane);
-      at[i] = reinterpret_cast<const uint8_t*>(base + step * ld + column);
-      left[i] = column < columns ? steps - step : 0;
+      first[i] = (64 / kLanes) * (kMine * wave + i) + lane / kLanes;
+      const int column = 8 * ((lane % kLanes) ^ (swizzle(first[i]) << 2));
+      at[i] = reinterpret_cast<const uint8_t*>(base + first[i] * ld + (column < columns ? column : 0));
     }
   }
-  __device__ __forceinline__ void issue(uint32_t lds, int wave) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      if (kUnits >= kWaves || wave < kUnits)
-        copy16(left[i] > 0 ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * (kMine * wave + i));
-      at[i] += stride;
-      left[i] -= kStep;
-    }
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave) {
+    if (kUnits >= kWaves || wave < kUnits)
+      copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * (kMine * wave + i));
+    at[i] += stride;
   }
   // As RowPanel's, by two transposing reads: sixteen lanes read four steps of sixteen columns,
   // lane i the columns 4 (i % 4) + 0..3 of step i / 4, and get column i's four steps.
@@ -175,40 +158,58 @@ struct ColumnPanel {
   }
 };
 
-// One stage: 32 MT rows by 32 NT columns a wave.
-template <typename T, typename M, typename N, int MT, int NT>
-__device__ __forceinline__ void multiply(const uint8_t* stage, int m0, int n0, int lane, floatx16 (&acc)[MT][NT]) {
-  vec8<T> m[2][MT], n[2][NT];
-  auto fetch = [&](int k) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) n[k & 1][j] = N::template fragment<T>(stage + M::kBytes, n0 + 32 * j, k, lane);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) m[k & 1][i] = M::template fragment<T>(stage, m0 + 32 * i, k, lane);
-  };
-  fetch(0);
-#pragma unroll
-  for (int k = 0; k < kStep / 16; ++k) {
-    if (k + 1 < kStep / 16) fetch(k + 1);
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma(n[k & 1][j], m[k & 1][i], acc[i][j]);
-  }
-}
-
-// All stages. issue(slot address) copies the next stage; ring: two stages.
-template <typename T, typename M, typename N, int MT, int NT, typename Issue>
+// All stages of a wave's 32 MT rows by 32 NT columns. copy(q, slot's LDS address, stage) is this wave's copy q
+// of kCopies of a stage; the panel N lies kOffset bytes behind M in a slot of kBytes; ring: two slots.
+//
+// A stage is multiplied in four parts of 16 steps. A part's fragments are read from LDS while the
+// part before it is multiplied. Before the last part all waves meet: by then every wave has read all of the stage,
+// so that its slot takes the copies of the stage after the next, which are issued one by one
+// between the last part's MFMAs, and the next stage has landed. Copies past the last stage
+// are of zeros.
+template <typename T, typename M, typename N, int MT, int NT, int kCopies, int kOffset, int kBytes, typename Copy>
 __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, int lane, floatx16 (&acc)[MT][NT],
-                                     Issue issue) {
-  constexpr int kBytes = M::kBytes + N::kBytes;
+                                     Copy copy) {
+  constexpr int kParts = kStep / 16;
   const uint32_t base = lds_address(ring);
-  issue(base);
+  vec8<T> m[2][MT], n[2][NT];
+  auto fetch = [&](int stage, int k) {
+    const uint8_t* slot = ring + (stage & 1) * kBytes;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) n[k & 1][j] = N::template fragment<T>(slot + kOffset, n0 + 32 * j, k, lane);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) m[k & 1][i] = M::template fragment<T>(slot, m0 + 32 * i, k, lane);
+  };
+#pragma unroll
+  for (int q = 0; q < kCopies; ++q) copy(q, base, 0);
+  wait_copies<0>();
+  lds_barrier();
+#pragma unroll
+  for (int q = 0; q < kCopies; ++q) copy(q, base + kBytes, 1);
+  fetch(0, 0);
   for (int s = 0; s < stages; ++s) {
+#pragma unroll
+    for (int k = 0; k < kParts - 1; ++k) {
+      fetch(s, k + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mfma(n[k & 1][j], m[k & 1][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     wait_copies<0>();
-    lds_barrier();  // the stage has landed, and the other one has been read
-    if (s + 1 < stages) issue(base + ((s + 1) & 1) * kBytes);
-    multiply<T, M, N, MT, NT>(ring + (s & 1) * kBytes, m0, n0, lane, acc);
+    lds_barrier();
+    constexpr int k = kParts - 1;
+    fetch(s + 1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < (kCopies > MT * NT ? kCopies : MT * NT); ++q) {
+      if (q < kCopies) copy(q, base + (s & 1) * kBytes, s + 2);
+      if (q < MT * NT) acc[q / NT][q % NT] = mfma(n[k & 1][q % NT], m[k & 1][q / NT], acc[q / NT][q % NT]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
+  wait_copies<0>();
   lds_barrier();
 }
 

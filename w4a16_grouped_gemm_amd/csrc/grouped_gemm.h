@@ -7,6 +7,19 @@
 
 namespace w4a16 {
 
+// Division of numbers below 2^31 by d <= 2^16: with 2^l >= d and m = ceil(2^(31+l) / d) <= 2^32,
+// n / d = floor(n m / 2^(31+l)), since n (m d - 2^(31+l)) < 2^31 2^l.
+struct Divisor {
+  uint32_t m;
+  int32_t l;
+  static Divisor by(uint32_t d) {
+    int32_t l = 0;
+    while ((1u << l) < d) ++l;
+    return {(uint32_t)(((uint64_t)1 << (31 + l)) / d + (((uint64_t)1 << (31 + l)) % d != 0)), l};
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t n) const { return __umulhi(2 * n, m) >> l; }
+};
+
 struct GroupedParams {
   const void* a;          // rows [a_rows, K]
   const void* w;          // [E, N, K], or [E, K, N] with `transposed`
@@ -16,7 +29,8 @@ struct GroupedParams {
   const int32_t* ntpp;
   int32_t E, N, K;
   int32_t gather;         // row of aligned row p: sorted[p] / topk, else p
-  int32_t topk, n_slots, capacity, block_m;
+  Divisor by_topk;
+  int32_t n_slots, capacity, block_m;
   int32_t transposed;
 };
 // Workgroups that a call launches at most, of 512 threads; a launch has less than 2^32 threads.
@@ -33,7 +47,8 @@ struct WgradParams {
   const int32_t* ntpp;
   int32_t E, N, K;
   int32_t gather;
-  int32_t topk, n_slots, capacity, block_m;
+  Divisor by_topk;
+  int32_t n_slots, capacity, block_m;
   int32_t accumulate;
   int32_t splits;         // wgrad_splits
 };

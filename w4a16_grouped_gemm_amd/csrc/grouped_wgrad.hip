@@ -39,12 +39,16 @@ __device__ __forceinline__ bool tile_of(int mtiles, int ntiles, int& e, int& mt,
   return true;
 }
 
-// kTile x kTile values a workgroup, its waves 2 deep and 4 wide.
+// kTile x kTile values a workgroup, its waves 2 deep and 4 wide. In LDS a row's kTile values of dout
+// and of a lie side by side, so that one copy of a wave fetches both.
 template <typename T, typename O, int kTile>
 __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(WgradParams p, int mtiles, int ntiles) {
   constexpr int MT = kTile / 64, NT = kTile / 128;
-  typedef ColumnPanel<kTile> Panel;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[4 * Panel::kBytes];
+  constexpr int kPitch = 4 * kTile;
+  typedef ColumnPanel<kTile, kPitch> Panel;
+  constexpr int kRowLanes = kPitch / 16, kUnitRows = 64 / kRowLanes;
+  constexpr int kMine = kStep / kUnitRows / kWaves;  // copies a wave and stage
+  __shared__ __attribute__((aligned(16))) uint8_t ring[2 * kStep * kPitch];
   __shared__ int run[2];
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -74,33 +78,35 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
   const int m0 = mt * kTile, n0 = nt * kTile;
   floatx16 acc[MT][NT] = {};
   if (stages > 0) {
-    // the rows of the next stage to be copied: their slots and their blocks' experts
-    int32_t slot[Panel::kMine], owner[Panel::kMine];
-    int row = begin;
-    auto look = [&]() {
+    // Each lane copies 16 bytes of dout or of a: rows `wave_row` + kUnitRows q + my_row of a stage.
+    const int my_row = lane / kRowLanes, part = lane % kRowLanes;
+    const bool of_a = part >= kRowLanes / 2;
+    const int wave_row = wave * kMine * kUnitRows;
+    const int chunk = part % (kRowLanes / 2);
+    const uint32_t ld = (uint32_t)(of_a ? p.K : p.N) * (uint32_t)sizeof(T);
+    const uint8_t* base = static_cast<const uint8_t*>(of_a ? p.a : p.dout) + (of_a ? n0 : m0) * (int)sizeof(T);
+    const int columns = of_a ? p.K - n0 : p.N - m0;
+    const bool by_slot = of_a && p.gather;
+    const Divisor by_topk = p.by_topk;
+    // The slots of the rows to be copied next. A wave's rows of a stage are eight, so in one block.
+    int32_t slot[kMine], owner;
+    auto look = [&](int stage) {
+      const int row = begin + stage * kStep + wave_row;
 #pragma unroll
-      for (int i = 0; i < Panel::kMine; ++i) {
-        const int at = min(row + Panel::step_of(i, wave, lane), stop - 1);
-        slot[i] = p.sorted[at];
-        owner[i] = p.expert_ids[at / p.block_m];
-      }
+      for (int q = 0; q < kMine; ++q) slot[q] = p.sorted[min(row + kUnitRows * q + my_row, stop - 1)];
+      owner = p.expert_ids[min(row, stop - 1) / p.block_m];
     };
-    look();
-    loop<T, Panel, Panel>(ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc, [&](uint32_t lds) {
-#pragma unroll
-      for (int i = 0; i < Panel::kMine; ++i) {
-        const int at = row + Panel::step_of(i, wave, lane), column = Panel::column_of(i, wave, lane);
-        const bool real = at < stop && (uint32_t)slot[i] < (uint32_t)p.n_slots && owner[i] == e;
-        const int64_t from = p.gather ? (int64_t)((uint32_t)slot[i] / (uint32_t)p.topk) : at;
-        const void* m = static_cast<const T*>(p.dout) + (int64_t)at * p.N + m0 + column;
-        const void* n = static_cast<const T*>(p.a) + from * p.K + n0 + column;
-        const uint32_t to = lds + 1024 * (Panel::kMine * wave + i);
-        copy16(real && m0 + column < p.N ? m : (const void*)kZeros, to);
-        copy16(real && n0 + column < p.K ? n : (const void*)kZeros, to + Panel::kBytes);
-      }
-      row += kStep;
-      look();
-    });
+    look(0);
+    loop<T, Panel, Panel, MT, NT, kMine, 2 * kTile, kStep * kPitch>(
+        ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc, [&](int q, uint32_t lds, int stage) {
+          const int step = wave_row + kUnitRows * q + my_row, row = begin + stage * kStep + step;
+          const bool real = (row < stop) & ((uint32_t)slot[q] < (uint32_t)p.n_slots) & (owner == e);
+          const uint32_t from = by_slot ? by_topk.of((uint32_t)slot[q]) : (uint32_t)row;
+          const int column = 8 * (chunk ^ (Panel::swizzle(step) << 2));
+          const uint8_t* at = base + (uint64_t)from * ld + 2 * (column < columns ? column : 0);
+          copy16(real ? (const void*)at : (const void*)kZeros, lds + 1024 * (kMine * wave + q));
+          if (q == kMine - 1) look(stage + 1);
+        });
   }
 
   const int64_t size = (int64_t)p.E * p.N * p.K;
