@@ -954,7 +954,7 @@ int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void
   p.by_topk = Divisor::by((uint32_t)topk);
   p.n_slots = T * topk;
   p.capacity = T == 0 ? 0 : capacity;  // no slot: zeros, or dw as it was
-  p.block_m = block_m;
+  p.log_block = __builtin_ctz((unsigned)block_m);
   p.accumulate = accumulate != 0;
   p.splits = splits;
   return hip_status(launch_grouped_wgrad(p, dtype, dw_dtype, static_cast<hipStream_t>(stream)));

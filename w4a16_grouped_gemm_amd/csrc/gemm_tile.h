@@ -2,9 +2,9 @@
 // with either operand held in memory along r (a row panel) or along m or n (a
 // column panel, whose rows are steps of r).
 //
-// A workgroup of eight waves computes a tile in stages of 64 steps of r. A
-// stage of both operands is copied from memory straight to LDS
-// (global_load_lds_dwordx4), while the stage before it is multiplied. A copy
+// A workgroup of eight waves computes a tile in stages of 64 steps of r, a
+// line of 128 bytes of each row. A stage of both operands is copied from memory straight to LDS
+// (global_load_lds_dwordx4) while the stage before it is multiplied. A copy
 // writes 64 x 16 bytes side by side in lane order, so where a 16-byte chunk
 // lies in LDS is chosen by which lane fetches it: the places are swizzled by
 // row so that the fragments' reads hit the banks evenly. What lies outside an
@@ -44,8 +44,8 @@ __device__ __forceinline__ floatx16 mfma(vec8<f16_t> a, vec8<f16_t> b, floatx16 
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// What copies from outside an operand read.
-static __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+// What copies from outside an operand read: as long as a row of a tile.
+static __device__ __attribute__((aligned(16))) const uint32_t kZeros[128] = {};
 
 // 16 bytes a lane to LDS at `lds` + 16 * lane. Issued from an asm block: the compiler would
 // count a builtin's copy as an LDS access and make every later LDS read wait for it. It
@@ -71,17 +71,19 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)(p);
 }
 
-// kOuter rows, each contiguous along r: 128 bytes a row and stage, the chunk c of row i in
-// place c ^ (i / 2 % 8).
+// kOuter rows, each contiguous along r: 128 bytes a row and stage, the chunk c of row i in place
+// c ^ (i / 2 % 8), so that sixteen rows' chunks c lie in sixteen places modulo 256.
 template <int kOuter>
 struct RowPanel {
-  static constexpr int kBytes = kOuter * 128;
+  static constexpr int kBytes = kOuter * 2 * kStep;
   static constexpr int kUnits = kOuter / 8;  // copies of a stage, 8 rows each
   static constexpr int kMine = (kUnits + kWaves - 1) / kWaves;
   const uint8_t* at[kMine];
   int32_t first[kMine];  // this lane's first step of r in a stage
 
-  static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 8 * (kMine * wave + i) + lane / 8; }
+  // where there are fewer copies than waves, two waves make the same one
+  static __device__ __forceinline__ int unit_of(int i, int wave) { return (kMine * wave + i) % kUnits; }
+  static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 8 * unit_of(i, wave) + lane / 8; }
   static __device__ __forceinline__ int swizzle(int row) { return row >> 1 & 7; }
 
   // row: the start of row row_of(i, ...)
@@ -91,15 +93,14 @@ struct RowPanel {
   }
   // copy i of the next stage, of which `left` steps are in the operand
   __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave) {
-    if (kUnits >= kWaves || wave < kUnits)
-      copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * (kMine * wave + i));
+    copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
     at[i] += 2 * kStep;
   }
   // steps 16 k + 8 (lane / 32) + 0..7 of row outer0 + lane % 32; outer0 a multiple of 32
   template <typename T>
   static __device__ __forceinline__ vec8<T> fragment(const uint8_t* panel, int outer0, int k, int lane) {
     const int row = outer0 + (lane & 31);
-    return *reinterpret_cast<const vec8<T>*>(panel + row * 128 + (((2 * k + (lane >> 5)) ^ swizzle(row)) << 4));
+    return *reinterpret_cast<const vec8<T>*>(panel + row * (2 * kStep) + (((2 * k + (lane >> 5)) ^ swizzle(row)) << 4));
   }
 };
 
@@ -108,8 +109,8 @@ struct RowPanel {
 // which half a wave reads, then lie in four places modulo 256. kPitch: bytes between steps.
 template <int kOuter, int kPitch = kOuter * 2>
 struct ColumnPanel {
-  static constexpr int kBytes = kOuter * 128;
-  static constexpr int kUnits = kOuter / 8;
+  static constexpr int kBytes = kOuter * 2 * kStep;
+  static constexpr int kUnits = kBytes / 1024;
   static constexpr int kMine = (kUnits + kWaves - 1) / kWaves;
   static constexpr int kLanes = kOuter / 8;  // that copy a step
   static constexpr int kParts = kOuter / 32;
@@ -117,6 +118,7 @@ struct ColumnPanel {
   int32_t first[kMine];
   int64_t stride;  // bytes a stage
 
+  static __device__ __forceinline__ int unit_of(int i, int wave) { return (kMine * wave + i) % kUnits; }
   static __device__ __forceinline__ int swizzle(int step) {
     return kParts >= 4 ? step & 3 : kParts == 2 ? step >> 1 & 1 : 0;
   }
@@ -127,14 +129,13 @@ struct ColumnPanel {
     stride = ld * kStep * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      first[i] = (64 / kLanes) * (kMine * wave + i) + lane / kLanes;
+      first[i] = (64 / kLanes) * unit_of(i, wave) + lane / kLanes;
       const int column = 8 * ((lane % kLanes) ^ (swizzle(first[i]) << 2));
       at[i] = reinterpret_cast<const uint8_t*>(base + first[i] * ld + (column < columns ? column : 0));
     }
   }
   __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave) {
-    if (kUnits >= kWaves || wave < kUnits)
-      copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * (kMine * wave + i));
+    copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
     at[i] += stride;
   }
   // As RowPanel's, by two transposing reads: sixteen lanes read four steps of sixteen columns,
@@ -158,56 +159,73 @@ struct ColumnPanel {
   }
 };
 
-// All stages of a wave's 32 MT rows by 32 NT columns. copy(q, slot's LDS address, stage) is this wave's copy q
-// of kCopies of a stage; the panel N lies kOffset bytes behind M in a slot of kBytes; ring: two slots.
+// Bytes of LDS of the loop below: three stages of the panel M, two of N.
+template <typename M, typename N>
+constexpr int kRingBytes = 3 * M::kBytes + 2 * N::kBytes;
+
+// All stages of a wave's 32 MT rows by 32 NT columns. copy_m(q, LDS address, stage) makes this wave's copy q of a
+// stage's panel M (M::kMine of them), copy_n of N. On return the ring is free.
 //
-// A stage is multiplied in four parts of 16 steps. A part's fragments are read from LDS while the
-// part before it is multiplied. Before the last part all waves meet: by then every wave has read all of the stage,
-// so that its slot takes the copies of the stage after the next, which are issued one by one
-// between the last part's MFMAs, and the next stage has landed. Copies past the last stage
-// are of zeros.
-template <typename T, typename M, typename N, int MT, int NT, int kCopies, int kOffset, int kBytes, typename Copy>
+// A stage is multiplied in four parts of 16 steps, a part's fragments being read from LDS while the part before
+// it is multiplied. Before the last part all waves meet: by then every wave has read all of stage s, and stage s + 1
+// has landed. N's slot then takes stage s + 2, copied at once so as to land within a stage; M's slot
+// takes stage s + 3, copied in the parts that follow and not waited for until a stage later. So the copies, which at
+// 64 bytes a cycle keep the vector cache busy for more than half of the time, are spread over the
+// stage, and none is waited for less than three parts after its issue. (Both panels in two slots, all
+// copies of a stage in one part: MEASURED.) Copies past the last stage are of zeros. settle() is where the wave
+// has no LDS read on its way: scalar loads for the next copies are waited for there.
+template <typename T, typename M, typename N, int MT, int NT, typename CopyM, typename CopyN, typename Settle>
 __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, int lane, floatx16 (&acc)[MT][NT],
-                                     Copy copy) {
-  constexpr int kParts = kStep / 16;
-  const uint32_t base = lds_address(ring);
+                                     CopyM copy_m, CopyN copy_n, Settle settle) {
+  constexpr int kMfmas = MT * NT, kFragments = MT + NT;
+  uint8_t* const ring_n = ring + 3 * M::kBytes;
+  const uint32_t base_m = lds_address(ring), base_n = base_m + 3 * M::kBytes;
   vec8<T> m[2][MT], n[2][NT];
-  auto fetch = [&](int stage, int k) {
-    const uint8_t* slot = ring + (stage & 1) * kBytes;
+  auto fetch = [&](int f, const uint8_t* slot_m, const uint8_t* slot_n, int k) {
+    if (f < NT)
+      n[k & 1][f] = N::template fragment<T>(slot_n, n0 + 32 * f, k, lane);
+    else
+      m[k & 1][f - NT] = M::template fragment<T>(slot_m, m0 + 32 * (f - NT), k, lane);
+  };
+  // Part k. Behind its MFMAs, one by one, the next part's fragments and the copies first..last: the matrix
+  // cores have work from the first instruction after the barrier on.
+  auto part = [&](int k, const uint8_t* slot_m, const uint8_t* slot_n, int to_k, int first, int last, auto copy) {
+    int f = 0, q = first;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) n[k & 1][j] = N::template fragment<T>(slot + kOffset, n0 + 32 * j, k, lane);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) m[k & 1][i] = M::template fragment<T>(slot, m0 + 32 * i, k, lane);
+    for (int i = 0; i < kMfmas; ++i) {
+      acc[i / NT][i % NT] = mfma(n[k & 1][i % NT], m[k & 1][i / NT], acc[i / NT][i % NT]);
+      __builtin_amdgcn_sched_barrier(0);
+      for (; f * kMfmas < (i + 1) * kFragments && f < kFragments; ++f) fetch(f, slot_m, slot_n, to_k);
+      for (; (q - first) * kMfmas < (i + 1) * (last - first) && q < last; ++q) copy(q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 #pragma unroll
-  for (int q = 0; q < kCopies; ++q) copy(q, base, 0);
-  wait_copies<0>();
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int q = 0; q < M::kMine; ++q) copy_m(q, base_m + s * M::kBytes, s);
+#pragma unroll
+    for (int q = 0; q < N::kMine; ++q) copy_n(q, base_n + s * N::kBytes, s);
+  }
+  wait_copies<M::kMine + N::kMine>();
   lds_barrier();
 #pragma unroll
-  for (int q = 0; q < kCopies; ++q) copy(q, base + kBytes, 1);
-  fetch(0, 0);
+  for (int f = 0; f < kFragments; ++f) fetch(f, ring, ring_n, 0);
+  int slot = 0;  // M's, in bytes
   for (int s = 0; s < stages; ++s) {
-#pragma unroll
-    for (int k = 0; k < kParts - 1; ++k) {
-      fetch(s, k + 1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma(n[k & 1][j], m[k & 1][i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    wait_copies<0>();
+    const int next = slot == 2 * M::kBytes ? 0 : slot + M::kBytes, after = next == 2 * M::kBytes ? 0 : next + M::kBytes;
+    const uint8_t *now_m = ring + slot, *now_n = ring_n + (s & 1) * N::kBytes;
+    auto far = [&](int q) { copy_m(q, base_m + after, s + 2); };
+    constexpr int kThird = (M::kMine + 2) / 3, kTwoThirds = 2 * M::kMine / 3 > kThird ? 2 * M::kMine / 3 : kThird;
+    part(0, now_m, now_n, 1, 0, kThird, far);
+    part(1, now_m, now_n, 2, kThird, kTwoThirds, far);
+    part(2, now_m, now_n, 3, kTwoThirds, M::kMine, far);
+    wait_copies<M::kMine>();
     lds_barrier();
-    constexpr int k = kParts - 1;
-    fetch(s + 1, 0);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int q = 0; q < (kCopies > MT * NT ? kCopies : MT * NT); ++q) {
-      if (q < kCopies) copy(q, base + (s & 1) * kBytes, s + 2);
-      if (q < MT * NT) acc[q / NT][q % NT] = mfma(n[k & 1][q % NT], m[k & 1][q / NT], acc[q / NT][q % NT]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    settle();
+    part(3, ring + next, ring_n + ((s + 1) & 1) * N::kBytes, 0, 0, N::kMine,
+         [&](int q) { copy_n(q, base_n + (s & 1) * N::kBytes, s + 2); });
+    slot = next;
   }
   wait_copies<0>();
   lds_barrier();

@@ -48,7 +48,8 @@ struct WgradParams {
   int32_t E, N, K;
   int32_t gather;
   Divisor by_topk;
-  int32_t n_slots, capacity, block_m;
+  int32_t n_slots, capacity;
+  int32_t log_block;      // of block_m, to base 2
   int32_t accumulate;
   int32_t splits;         // wgrad_splits
 };

@@ -79,6 +79,7 @@ __device__ __forceinline__ int64_t find_tile(const int32_t* expert_ids, int used
   }
   __syncthreads();
   block = __builtin_amdgcn_readfirstlane(scan.found);
+  __syncthreads();  // the ring's copies go where the counts are
   blocks = 0;
   if (block >= 0) {
     const int i = block + lane;
@@ -119,17 +120,19 @@ __device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, i
       n.set(i, w + (int64_t)min(n0 + N::row_of(i, wave, lane), p.N - 1) * p.K, wave, lane);
   }
   const int at_m = wave / WN * 32 * MT, at_n = wave % WN * 32 * NT;
-  loop<T, M, N, MT, NT, M::kMine + N::kMine, M::kBytes, M::kBytes + N::kBytes>(
-      ring, (p.K + kStep - 1) / kStep, at_m, at_n, lane, acc, [&](int q, uint32_t slot, int stage) {
-        const int left = p.K - stage * kStep;
-        if (q < M::kMine)
-          m.copy(q, slot, left, wave);
-        else
-          n.copy(q - M::kMine, slot + M::kBytes, left, wave);
-      });
+  loop<T, M, N>(
+      ring, (p.K + kStep - 1) / kStep, at_m, at_n, lane, acc,
+      [&](int q, uint32_t slot, int stage) { m.copy(q, slot, p.K - stage * kStep, wave); },
+      [&](int q, uint32_t slot, int stage) { n.copy(q, slot, p.K - stage * kStep, wave); }, [] {});
+  uint32_t slotted[MT];  // which of 32 rows have a slot
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int row = at_m + 32 * i + (lane & 31);
+    slotted[i] = (uint32_t)__ballot(row < rows && (uint32_t)p.sorted[first + min(row, rows - 1)] < (uint32_t)p.n_slots);
+  }
   drain(ring, at_m, at_n, wave, lane, acc, [&](int row, int column, const float (&v)[8]) {
     if (row >= rows || n0 + column >= p.N) return;
-    const bool real = (uint32_t)p.sorted[first + row] < (uint32_t)p.n_slots;
+    const bool real = slotted[(row - at_m) / 32] >> (row & 31) & 1;
     float sums[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sums[i] = real ? v[i] : 0.f;
@@ -142,8 +145,7 @@ template <typename T, typename O, bool TRANSPOSED, int WM, int MT>
 __global__ __launch_bounds__(kThreads, MT == 4 ? 2 : 4) void grouped_kernel(GroupedParams p, int ntiles, int row_tiles,
                                                                             int log_per) {
   constexpr int kRows = 32 * WM * MT;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[2 * (kRows + kTileN) * 128];
-  __shared__ Scan scan;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes<RowPanel<kRows>, RowPanel<kTileN>>];
   const int used = min(p.capacity, *p.ntpp) / p.block_m;
   int64_t target;
   int nt;
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(kThreads, MT == 4 ? 2 : 4) void grouped_kernel(Grou
   // more tiles than moe_align's order can have: go round again
   for (; target < used; target += row_tiles) {
     int b, blocks;
-    const int64_t total = find_tile(p.expert_ids, used, log_per, target, scan, b, blocks);
+    const int64_t total = find_tile(p.expert_ids, used, log_per, target, *reinterpret_cast<Scan*>(ring), b, blocks);
     if (blocks == 0) return;
     const int e = p.expert_ids[b];
     const int first = b * p.block_m, rows = blocks * p.block_m, n0 = nt * kTileN;

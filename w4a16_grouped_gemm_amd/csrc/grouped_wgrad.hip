@@ -39,24 +39,23 @@ __device__ __forceinline__ bool tile_of(int mtiles, int ntiles, int& e, int& mt,
   return true;
 }
 
-// kTile x kTile values a workgroup, its waves 2 deep and 4 wide. In LDS a row's kTile values of dout
-// and of a lie side by side, so that one copy of a wave fetches both.
+// kTile x kTile values a workgroup, its waves 2 deep and 4 wide.
 template <typename T, typename O, int kTile>
 __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(WgradParams p, int mtiles, int ntiles) {
   constexpr int MT = kTile / 64, NT = kTile / 128;
-  constexpr int kPitch = 4 * kTile;
-  typedef ColumnPanel<kTile, kPitch> Panel;
-  constexpr int kRowLanes = kPitch / 16, kUnitRows = 64 / kRowLanes;
-  constexpr int kMine = kStep / kUnitRows / kWaves;  // copies a wave and stage
-  __shared__ __attribute__((aligned(16))) uint8_t ring[2 * kStep * kPitch];
-  __shared__ int run[2];
+  typedef ColumnPanel<kTile> Panel;
+  constexpr int kRows = 64 / Panel::kLanes;  // of a copy
+  constexpr int kMine = Panel::kMine;
+  static_assert(kMine * kRows == 8, "eight rows a wave");
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes<Panel, Panel>];
+  int* const run = reinterpret_cast<int*>(ring);
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   int e, mt, nt;
   if (!tile_of(mtiles, ntiles, e, mt, nt)) return;
 
   // the expert's first and last block
-  const int used = p.capacity > 0 ? min(p.capacity, *p.ntpp) / p.block_m : 0;
+  const int used = p.capacity > 0 ? min(p.capacity, *p.ntpp) >> p.log_block : 0;
   if (threadIdx.x == 0) run[0] = INT_MAX, run[1] = -1;
   __syncthreads();
   int lo = INT_MAX, hi = -1;
@@ -68,8 +67,10 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
   }
   __syncthreads();
   const int last = __builtin_amdgcn_readfirstlane(run[1]);
-  const int first = last < 0 ? 0 : __builtin_amdgcn_readfirstlane(run[0]) * p.block_m;
-  const int end = last < 0 ? 0 : (last + 1) * p.block_m;
+  const int begun = __builtin_amdgcn_readfirstlane(run[0]);
+  __syncthreads();  // the ring's copies go where the run is
+  const int first = last < 0 ? 0 : begun << p.log_block;
+  const int end = last < 0 ? 0 : (last + 1) << p.log_block;
   const int share = (((end - first + kStep - 1) / kStep + p.splits - 1) / p.splits) * kStep;
   const int begin = min((int64_t)first + (int64_t)share * blockIdx.y, (int64_t)end);
   const int stop = min((int64_t)begin + share, (int64_t)end);
@@ -78,34 +79,61 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
   const int m0 = mt * kTile, n0 = nt * kTile;
   floatx16 acc[MT][NT] = {};
   if (stages > 0) {
-    // Each lane copies 16 bytes of dout or of a: rows `wave_row` + kUnitRows q + my_row of a stage.
-    const int my_row = lane / kRowLanes, part = lane % kRowLanes;
-    const bool of_a = part >= kRowLanes / 2;
-    const int wave_row = wave * kMine * kUnitRows;
-    const int chunk = part % (kRowLanes / 2);
-    const uint32_t ld = (uint32_t)(of_a ? p.K : p.N) * (uint32_t)sizeof(T);
-    const uint8_t* base = static_cast<const uint8_t*>(of_a ? p.a : p.dout) + (of_a ? n0 : m0) * (int)sizeof(T);
-    const int columns = of_a ? p.K - n0 : p.N - m0;
-    const bool by_slot = of_a && p.gather;
-    const Divisor by_topk = p.by_topk;
-    // The slots of the rows to be copied next. A wave's rows of a stage are eight, so in one block.
-    int32_t slot[kMine], owner;
-    auto look = [&](int stage) {
-      const int row = begin + stage * kStep + wave_row;
+    // Which rows a wave copies comes by scalar loads: a vector load's wait would be for every copy issued before it
+    // too. They are eight of a stage, of one block.
+    const int my_row = lane / Panel::kLanes;
+    int32_t offset_m[kMine], offset_n[kMine];  // this lane's bytes from the tile's first column
 #pragma unroll
-      for (int q = 0; q < kMine; ++q) slot[q] = p.sorted[min(row + kUnitRows * q + my_row, stop - 1)];
-      owner = p.expert_ids[min(row, stop - 1) / p.block_m];
+    for (int q = 0; q < kMine; ++q) {
+      const int column = 8 * (lane % Panel::kLanes ^ (Panel::swizzle(kRows * q + my_row) << 2));
+      offset_m[q] = column < p.N - m0 ? 2 * column : 0;
+      offset_n[q] = column < p.K - n0 ? 2 * column : 0;
+    }
+    typedef const __attribute__((address_space(4))) int32_t* scalar_i32;
+    const scalar_i32 sorted = (scalar_i32)(uintptr_t)p.sorted, expert_ids = (scalar_i32)(uintptr_t)p.expert_ids;
+    struct Rows {
+      int32_t slot[8], owner;  // of a wave's rows of a stage, and their block's expert
     };
-    look(0);
-    loop<T, Panel, Panel, MT, NT, kMine, 2 * kTile, kStep * kPitch>(
-        ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc, [&](int q, uint32_t lds, int stage) {
-          const int step = wave_row + kUnitRows * q + my_row, row = begin + stage * kStep + step;
-          const bool real = (row < stop) & ((uint32_t)slot[q] < (uint32_t)p.n_slots) & (owner == e);
-          const uint32_t from = by_slot ? by_topk.of((uint32_t)slot[q]) : (uint32_t)row;
-          const int column = 8 * (chunk ^ (Panel::swizzle(step) << 2));
-          const uint8_t* at = base + (uint64_t)from * ld + 2 * (column < columns ? column : 0);
-          copy16(real ? (const void*)at : (const void*)kZeros, lds + 1024 * (kMine * wave + q));
-          if (q == kMine - 1) look(stage + 1);
+    Rows of_m, of_n;
+    auto look = [&](Rows& r, int stage) {
+      const int row = min(begin + stage * kStep + 8 * wave, stop - 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.slot[i] = sorted[row + i];
+      r.owner = expert_ids[row >> p.log_block];
+    };
+    // copy q of a stage's rows, of `at` + row * ld; by_slot: of the slots' tokens
+    auto copy = [&](const Rows& r, const T* base, int32_t ld, bool by_slot, int32_t offset, int q, uint32_t lds, int stage) {
+      const uint8_t* at = nullptr;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int row = begin + stage * kStep + 8 * wave + kRows * q + i;
+        const uint32_t slot = (uint32_t)r.slot[kRows * q + i];
+        const bool real = (row < stop) & (slot < (uint32_t)p.n_slots) & (r.owner == e);
+        const T* row_at = base + (int64_t)(by_slot ? p.by_topk.of(slot) : (uint32_t)row) * ld;
+        if (!real) row_at = reinterpret_cast<const T*>(kZeros);
+        at = i == 0 || my_row == i ? reinterpret_cast<const uint8_t*>(row_at) : at;
+      }
+      copy16(at + offset, lds + 1024 * (kMine * wave + q));
+    };
+    look(of_m, 0);
+    look(of_n, 0);
+    loop<T, Panel, Panel>(
+        ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc,
+        [&](int q, uint32_t lds, int stage) {
+          copy(of_m, static_cast<const T*>(p.dout) + m0, p.N, false, offset_m[q], q, lds, stage);
+          if (q == kMine - 1) look(of_m, stage + 1);
+        },
+        [&](int q, uint32_t lds, int stage) {
+          copy(of_n, static_cast<const T*>(p.a) + n0, p.K, p.gather, offset_n[q], q, lds, stage);
+          if (q == kMine - 1) look(of_n, stage + 1);
+        },
+        [&] {
+          asm volatile(""
+                       : "+s"(of_m.slot[0]), "+s"(of_m.slot[1]), "+s"(of_m.slot[2]), "+s"(of_m.slot[3]),
+                         "+s"(of_m.slot[4]), "+s"(of_m.slot[5]), "+s"(of_m.slot[6]), "+s"(of_m.slot[7]), "+s"(of_m.owner));
+          asm volatile(""
+                       : "+s"(of_n.slot[0]), "+s"(of_n.slot[1]), "+s"(of_n.slot[2]), "+s"(of_n.slot[3]),
+                         "+s"(of_n.slot[4]), "+s"(of_n.slot[5]), "+s"(of_n.slot[6]), "+s"(of_n.slot[7]), "+s"(of_n.owner));
         });
   }
 
