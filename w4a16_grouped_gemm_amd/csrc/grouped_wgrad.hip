@@ -40,7 +40,7 @@ __device__ __forceinline__ bool tile_of(int mtiles, int ntiles, int& e, int& mt,
 }
 
 // kTile x kTile values a workgroup, its waves 2 deep and 4 wide.
-template <typename T, typename O, int kTile>
+template <typename T, typename O, int kTile, bool GATHER>
 __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(WgradParams p, int mtiles, int ntiles) {
   constexpr int MT = kTile / 64, NT = kTile / 128;
   typedef ColumnPanel<kTile> Panel;
@@ -81,50 +81,53 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
   if (stages > 0) {
     // Which rows a wave copies comes by scalar loads: a vector load's wait would be for every copy issued before it
     // too. They are eight of a stage, of one block.
-    const int my_row = lane / Panel::kLanes;
-    int32_t offset_m[kMine], offset_n[kMine];  // this lane's bytes from the tile's first column
-#pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-      const int column = 8 * (lane % Panel::kLanes ^ (Panel::swizzle(kRows * q + my_row) << 2));
-      offset_m[q] = column < p.N - m0 ? 2 * column : 0;
-      offset_n[q] = column < p.K - n0 ? 2 * column : 0;
-    }
     typedef const __attribute__((address_space(4))) int32_t* scalar_i32;
     const scalar_i32 sorted = (scalar_i32)(uintptr_t)p.sorted, expert_ids = (scalar_i32)(uintptr_t)p.expert_ids;
     struct Rows {
       int32_t slot[8], owner;  // of a wave's rows of a stage, and their block's expert
+      bool inside;
     };
     Rows of_m, of_n;
     auto look = [&](Rows& r, int stage) {
-      const int row = min(begin + stage * kStep + 8 * wave, stop - 8);
+      const int row = begin + stage * kStep + 8 * wave, at = min(row, stop - 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r.slot[i] = sorted[row + i];
-      r.owner = expert_ids[row >> p.log_block];
+      for (int i = 0; i < 8; ++i) r.slot[i] = sorted[at + i];
+      r.owner = expert_ids[at >> p.log_block];
+      r.inside = row < stop;
     };
-    // copy q of a stage's rows, of `at` + row * ld; by_slot: of the slots' tokens
-    auto copy = [&](const Rows& r, const T* base, int32_t ld, bool by_slot, int32_t offset, int q, uint32_t lds, int stage) {
-      const uint8_t* at = nullptr;
+    const int my_row = lane / Panel::kLanes;
+    const int64_t row_m = (int64_t)p.N * (int)sizeof(T), row_n = (int64_t)p.K * (int)sizeof(T);
+    const uint8_t *at_m[kMine], *at_n[kMine];  // this lane's 16 bytes in the copies of the next stage (GATHER: of token 0)
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int row = begin + stage * kStep + 8 * wave + kRows * q + i;
-        const uint32_t slot = (uint32_t)r.slot[kRows * q + i];
-        const bool real = (row < stop) & (slot < (uint32_t)p.n_slots) & (r.owner == e);
-        const T* row_at = base + (int64_t)(by_slot ? p.by_topk.of(slot) : (uint32_t)row) * ld;
-        if (!real) row_at = reinterpret_cast<const T*>(kZeros);
-        at = i == 0 || my_row == i ? reinterpret_cast<const uint8_t*>(row_at) : at;
-      }
-      copy16(at + offset, lds + 1024 * (kMine * wave + q));
+    for (int q = 0; q < kMine; ++q) {
+      const int64_t row = begin + 8 * wave + kRows * q + my_row;
+      const int column = 8 * (lane % Panel::kLanes ^ (Panel::swizzle(kRows * q + my_row) << 2));
+      at_m[q] = static_cast<const uint8_t*>(p.dout) + row * row_m + 2 * (m0 + (column < p.N - m0 ? column : 0));
+      at_n[q] = static_cast<const uint8_t*>(p.a) + (GATHER ? 0 : row * row_n) + 2 * (n0 + (column < p.K - n0 ? column : 0));
+    }
+    auto copy = [&](const Rows& r, const uint8_t* at, uint32_t slot, int q, uint32_t lds) {
+      const bool real = (slot < (uint32_t)p.n_slots) & (r.owner == e) & r.inside;
+      copy16(real ? (const void*)at : (const void*)kZeros, lds + 1024 * (kMine * wave + q));
+    };
+    auto slot_of = [&](const Rows& r, int q) {  // of this lane's row
+      int32_t slot = r.slot[kRows * q];
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) slot = my_row == i ? r.slot[kRows * q + i] : slot;
+      return (uint32_t)slot;
     };
     look(of_m, 0);
     look(of_n, 0);
     loop<T, Panel, Panel>(
         ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc,
         [&](int q, uint32_t lds, int stage) {
-          copy(of_m, static_cast<const T*>(p.dout) + m0, p.N, false, offset_m[q], q, lds, stage);
+          copy(of_m, at_m[q], slot_of(of_m, q), q, lds);
+          at_m[q] += kStep * row_m;
           if (q == kMine - 1) look(of_m, stage + 1);
         },
         [&](int q, uint32_t lds, int stage) {
-          copy(of_n, static_cast<const T*>(p.a) + n0, p.K, p.gather, offset_n[q], q, lds, stage);
+          const uint32_t slot = slot_of(of_n, q);
+          copy(of_n, GATHER ? at_n[q] + (uint64_t)p.by_topk.of(slot) * (uint32_t)row_n : at_n[q], slot, q, lds);
+          if (!GATHER) at_n[q] += kStep * row_n;
           if (q == kMine - 1) look(of_n, stage + 1);
         },
         [&] {
@@ -183,8 +186,11 @@ hipError_t launch_tile(const WgradParams& p, hipStream_t stream) {
   const int mtiles = (p.N + kTile - 1) / kTile, ntiles = (p.K + kTile - 1) / kTile;
   const int64_t chunk = ((int64_t)mtiles * ntiles + kXcds - 1) / kXcds;
   const int64_t grid = chunk * kXcds * p.E;
-  hipLaunchKernelGGL((wgrad_kernel<T, O, kTile>), dim3((unsigned)grid, (unsigned)p.splits), dim3(kThreads), 0, stream,
-                     p, mtiles, ntiles);
+  const dim3 g((unsigned)grid, (unsigned)p.splits), t(kThreads);
+  if (p.gather)
+    hipLaunchKernelGGL((wgrad_kernel<T, O, kTile, true>), g, t, 0, stream, p, mtiles, ntiles);
+  else
+    hipLaunchKernelGGL((wgrad_kernel<T, O, kTile, false>), g, t, 0, stream, p, mtiles, ntiles);
   return hipGetLastError();
 }
 
