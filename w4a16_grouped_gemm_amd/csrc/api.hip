@@ -918,8 +918,8 @@ int moe_grouped_gemm(int32_t num_experts, int32_t N, int32_t K, const void* a, i
 
 size_t moe_grouped_gemm_wgrad_workspace_bytes(int32_t num_experts, int32_t N, int32_t K, int32_t capacity) {
   if (check_products(num_experts, N, K, W4A16_BF16, W4A16_FP32) != W4A16_OK || capacity < 0) return 0;
-  const int32_t splits = wgrad_splits(num_experts, N, K, capacity);
-  return splits == 1 ? 0 : (size_t)splits * num_experts * N * K * sizeof(float);
+  const WgradCut cut = wgrad_cut(num_experts, N, K, capacity);
+  return cut.splits == 1 ? 0 : (size_t)cut.splits * num_experts * N * K * sizeof(float);
 }
 
 int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void* dout, const void* a, int32_t dtype,
@@ -935,8 +935,8 @@ int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void
   if (T > 0 && capacity > 0 && (!dout || !a || !sorted_token_ids || !expert_ids || !num_tokens_post_padded))
     return W4A16_ERR_INVALID_ARG;
   if (!all_aligned16(dout, a, dw, workspace)) return W4A16_ERR_INVALID_ARG;
-  const int32_t splits = wgrad_splits(num_experts, N, K, capacity);
-  if (wgrad_workgroups(num_experts, N, K, splits) >= kMaxWorkgroups) return W4A16_ERR_UNSUPPORTED;
+  const WgradCut cut = wgrad_cut(num_experts, N, K, capacity);
+  if (wgrad_workgroups(num_experts, N, K, cut.splits) >= kMaxWorkgroups) return W4A16_ERR_UNSUPPORTED;
   const size_t need = moe_grouped_gemm_wgrad_workspace_bytes(num_experts, N, K, capacity);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
   WgradParams p{};
@@ -956,7 +956,7 @@ int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void
   p.capacity = T == 0 ? 0 : capacity;  // no slot: zeros, or dw as it was
   p.log_block = __builtin_ctz((unsigned)block_m);
   p.accumulate = accumulate != 0;
-  p.splits = splits;
+  p.cut = cut;
   return hip_status(launch_grouped_wgrad(p, dtype, dw_dtype, static_cast<hipStream_t>(stream)));
 }
 

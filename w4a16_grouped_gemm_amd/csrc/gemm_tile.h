@@ -71,45 +71,49 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)(p);
 }
 
-// kOuter rows, each contiguous along r: 128 bytes a row and stage, the chunk c of row i in place
-// c ^ (i / 2 % 8), so that sixteen rows' chunks c lie in sixteen places modulo 256.
-template <int kOuter>
+// kOuter rows, each contiguous along r: 2 kSteps bytes a row and stage, a line or two. Sixteen rows' chunks of
+// 16 bytes c lie in sixteen places modulo 256: chunk c of row i in place c ^ (i / 2 % 8), with two lines
+// c ^ (i % 16).
+template <int kOuter, int kSteps = kStep>
 struct RowPanel {
-  static constexpr int kBytes = kOuter * 2 * kStep;
-  static constexpr int kUnits = kOuter / 8;  // copies of a stage, 8 rows each
+  static constexpr int kPitch = 2 * kSteps;
+  static constexpr int kBytes = kOuter * kPitch;
+  static constexpr int kUnits = kBytes / 1024;  // copies of a stage
   static constexpr int kMine = (kUnits + kWaves - 1) / kWaves;
+  static constexpr int kLanes = kPitch / 16;  // that copy a row
   const uint8_t* at[kMine];
   int32_t first[kMine];  // this lane's first step of r in a stage
 
   // where there are fewer copies than waves, two waves make the same one
   static __device__ __forceinline__ int unit_of(int i, int wave) { return (kMine * wave + i) % kUnits; }
-  static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 8 * unit_of(i, wave) + lane / 8; }
-  static __device__ __forceinline__ int swizzle(int row) { return row >> 1 & 7; }
+  static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 64 / kLanes * unit_of(i, wave) + lane / kLanes; }
+  static __device__ __forceinline__ int swizzle(int row) { return kSteps == 64 ? row >> 1 & 7 : row & 15; }
 
   // row: the start of row row_of(i, ...)
   __device__ __forceinline__ void set(int i, const void* row, int wave, int lane) {
-    first[i] = 8 * ((lane & 7) ^ swizzle(row_of(i, wave, lane)));
+    first[i] = 8 * (lane % kLanes ^ swizzle(row_of(i, wave, lane)));
     at[i] = static_cast<const uint8_t*>(row) + 2 * first[i];
   }
   // copy i of the next stage, of which `left` steps are in the operand
   __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave) {
     copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
-    at[i] += 2 * kStep;
+    at[i] += kPitch;
   }
   // steps 16 k + 8 (lane / 32) + 0..7 of row outer0 + lane % 32; outer0 a multiple of 32
   template <typename T>
   static __device__ __forceinline__ vec8<T> fragment(const uint8_t* panel, int outer0, int k, int lane) {
     const int row = outer0 + (lane & 31);
-    return *reinterpret_cast<const vec8<T>*>(panel + row * (2 * kStep) + (((2 * k + (lane >> 5)) ^ swizzle(row)) << 4));
+    return *reinterpret_cast<const vec8<T>*>(panel + row * kPitch + (((2 * k + (lane >> 5)) ^ swizzle(row)) << 4));
   }
 };
 
 // kOuter columns, contiguous at each step of r: kOuter * 2 bytes a step, in parts of 64 bytes,
 // the part c of step r in place c ^ (r % 4) (where a step has that many). Four steps' 64 bytes,
-// which half a wave reads, then lie in four places modulo 256. kPitch: bytes between steps.
-template <int kOuter, int kPitch = kOuter * 2>
+// which half a wave reads, then lie in four places modulo 256.
+template <int kOuter, int kSteps = kStep>
 struct ColumnPanel {
-  static constexpr int kBytes = kOuter * 2 * kStep;
+  static constexpr int kPitch = kOuter * 2;
+  static constexpr int kBytes = kPitch * kSteps;
   static constexpr int kUnits = kBytes / 1024;
   static constexpr int kMine = (kUnits + kWaves - 1) / kWaves;
   static constexpr int kLanes = kOuter / 8;  // that copy a step
@@ -126,7 +130,7 @@ struct ColumnPanel {
   // those are copies of column 0.
   template <typename T>
   __device__ __forceinline__ void set(const T* base, int64_t ld, int32_t columns, int wave, int lane) {
-    stride = ld * kStep * (int)sizeof(T);
+    stride = ld * kSteps * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       first[i] = (64 / kLanes) * unit_of(i, wave) + lane / kLanes;
@@ -159,27 +163,29 @@ struct ColumnPanel {
   }
 };
 
-// Bytes of LDS of the loop below: three stages of the panel M, two of N.
-template <typename M, typename N>
-constexpr int kRingBytes = 3 * M::kBytes + 2 * N::kBytes;
+// Bytes of LDS of the loop below.
+template <typename M, typename N, int kAhead>
+constexpr int kRingBytes = (kAhead + 1) * M::kBytes + kAhead * N::kBytes;
 
 // All stages of a wave's 32 MT rows by 32 NT columns. copy_m(q, LDS address, stage) makes this wave's copy q of a
-// stage's panel M (M::kMine of them), copy_n of N. On return the ring is free.
+// stage's panel M (M::kMine of them), copy_n of N. ring: kAhead + 1 stages of M, kAhead of N; free on return.
 //
 // A stage is multiplied in four parts of 16 steps, a part's fragments being read from LDS while the part before
 // it is multiplied. Before the last part all waves meet: by then every wave has read all of stage s, and stage s + 1
-// has landed. N's slot then takes stage s + 2, copied at once so as to land within a stage; M's slot
-// takes stage s + 3, copied in the parts that follow and not waited for until a stage later. So the copies, which at
-// 64 bytes a cycle keep the vector cache busy for more than half of the time, are spread over the
-// stage, and none is waited for less than three parts after its issue. (Both panels in two slots, all
-// copies of a stage in one part: MEASURED.) Copies past the last stage are of zeros. settle() is where the wave
-// has no LDS read on its way: scalar loads for the next copies are waited for there.
-template <typename T, typename M, typename N, int MT, int NT, typename CopyM, typename CopyN, typename Settle>
+// has landed. N's slot then takes stage s + kAhead, copied at once so as to land in time; M's slot takes stage
+// s + kAhead + 1, copied in the parts that follow. So the copies, which at 64 bytes a cycle keep the vector cache busy
+// for more than half of a 256 x 256 tile's time, are spread over the stage, and none is waited for less than three
+// parts after its issue. (32768 rows, 16 experts, 4096 x 7168, kAhead 2: 1618 us; both panels in two slots with
+// the copies in one part 1805, in two parts 1732, in all four 1904.) Copies past the last stage are of zeros.
+// settle() is where the wave has no LDS read on its way: scalar loads for the next copies are waited for there.
+template <typename T, typename M, typename N, int kAhead, int MT, int NT, typename CopyM, typename CopyN,
+          typename Settle>
 __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, int lane, floatx16 (&acc)[MT][NT],
                                      CopyM copy_m, CopyN copy_n, Settle settle) {
+  static_assert(kAhead >= 2, "a stage is read while the next one lands");
   constexpr int kMfmas = MT * NT, kFragments = MT + NT;
-  uint8_t* const ring_n = ring + 3 * M::kBytes;
-  const uint32_t base_m = lds_address(ring), base_n = base_m + 3 * M::kBytes;
+  uint8_t* const ring_n = ring + (kAhead + 1) * M::kBytes;
+  const uint32_t base_m = lds_address(ring), base_n = base_m + (kAhead + 1) * M::kBytes;
   vec8<T> m[2][MT], n[2][NT];
   auto fetch = [&](int f, const uint8_t* slot_m, const uint8_t* slot_n, int k) {
     if (f < NT)
@@ -201,44 +207,74 @@ __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, 
     }
   };
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < kAhead; ++s) {
 #pragma unroll
     for (int q = 0; q < M::kMine; ++q) copy_m(q, base_m + s * M::kBytes, s);
 #pragma unroll
     for (int q = 0; q < N::kMine; ++q) copy_n(q, base_n + s * N::kBytes, s);
   }
-  wait_copies<M::kMine + N::kMine>();
+  wait_copies<(kAhead - 1) * (M::kMine + N::kMine)>();
   lds_barrier();
 #pragma unroll
   for (int f = 0; f < kFragments; ++f) fetch(f, ring, ring_n, 0);
-  int slot = 0;  // M's, in bytes
+  int at_m = 0, at_n = 0;  // the slots of stage s, in bytes
   for (int s = 0; s < stages; ++s) {
-    const int next = slot == 2 * M::kBytes ? 0 : slot + M::kBytes, after = next == 2 * M::kBytes ? 0 : next + M::kBytes;
-    const uint8_t *now_m = ring + slot, *now_n = ring_n + (s & 1) * N::kBytes;
-    auto far = [&](int q) { copy_m(q, base_m + after, s + 2); };
+    const int next_m = at_m == kAhead * M::kBytes ? 0 : at_m + M::kBytes;
+    const int next_n = at_n == (kAhead - 1) * N::kBytes ? 0 : at_n + N::kBytes;
+    const uint8_t *slot_m = ring + at_m, *slot_n = ring_n + at_n;
+    const uint32_t free_m = base_m + (at_m == 0 ? kAhead * M::kBytes : at_m - M::kBytes);  // of stage s - 1
+    auto far = [&](int q) { copy_m(q, free_m, s + kAhead); };
     constexpr int kThird = (M::kMine + 2) / 3, kTwoThirds = 2 * M::kMine / 3 > kThird ? 2 * M::kMine / 3 : kThird;
-    part(0, now_m, now_n, 1, 0, kThird, far);
-    part(1, now_m, now_n, 2, kThird, kTwoThirds, far);
-    part(2, now_m, now_n, 3, kTwoThirds, M::kMine, far);
-    wait_copies<M::kMine>();
+    part(0, slot_m, slot_n, 1, 0, kThird, far);
+    part(1, slot_m, slot_n, 2, kThird, kTwoThirds, far);
+    part(2, slot_m, slot_n, 3, kTwoThirds, M::kMine, far);
+    // a wave's copies land in order: younger than stage s + 1's are M's of kAhead - 1 stages and N's of kAhead - 2
+    wait_copies<(kAhead - 1) * M::kMine + (kAhead - 2) * N::kMine>();
     lds_barrier();
     settle();
-    part(3, ring + next, ring_n + ((s + 1) & 1) * N::kBytes, 0, 0, N::kMine,
-         [&](int q) { copy_n(q, base_n + (s & 1) * N::kBytes, s + 2); });
-    slot = next;
+    part(3, ring + next_m, ring_n + next_n, 0, 0, N::kMine, [&](int q) { copy_n(q, base_n + at_n, s + kAhead); });
+    at_m = next_m;
+    at_n = next_n;
+  }
+  wait_copies<0>();
+  lds_barrier();
+}
+
+// All stages of a tile of 32 rows by 32 NT columns that the eight waves share along r: of each stage of 128 steps
+// wave w multiplies 16. Few steps follow each other, so a tile of little work streams its operands with kAhead
+// stages on their way. Returns each wave's share of the sums. ring: kAhead slots.
+template <typename T, typename M, typename N, int kAhead, int NT, typename Copy>
+__device__ __forceinline__ void shared_loop(uint8_t* ring, int stages, int wave, int lane, floatx16 (&acc)[NT],
+                                            Copy copy) {
+  constexpr int kBytes = M::kBytes + N::kBytes, kCopies = M::kMine + N::kMine;
+  const uint32_t base = lds_address(ring);
+#pragma unroll
+  for (int s = 0; s < kAhead - 1; ++s) copy(base + s * kBytes, s);
+  int slot = 0, free = (kAhead - 1) * kBytes;
+  for (int s = 0; s < stages; ++s) {
+    wait_copies<(kAhead - 2) * kCopies>();
+    lds_barrier();  // stage s has landed, stage s - 1 has been read
+    copy(base + free, s + kAhead - 1);
+    const vec8<T> m = M::template fragment<T>(ring + slot, 0, wave, lane);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      acc[j] = mfma(N::template fragment<T>(ring + slot + M::kBytes, 32 * j, wave, lane), m, acc[j]);
+    free = slot;
+    slot = slot == (kAhead - 1) * kBytes ? 0 : slot + kBytes;
   }
   wait_copies<0>();
   lds_barrier();
 }
 
 // Sums leave through LDS, 32 rows of a wave's columns at a time, so that a store covers whole
-// lines; put(row, column, eight sums) stores those of the tile's row `row`, column `column` on.
-template <int MT, int NT, typename Put>
+// lines; put(row, column, sums) stores those of the tile's row `row`, column `column` on: 16 bytes of O.
+template <typename O, int MT, int NT, typename Put>
 __device__ __forceinline__ void drain(uint8_t* ring, int m0, int n0, int wave, int lane, const floatx16 (&acc)[MT][NT],
                                       Put put) {
   constexpr int kPitch = 32 * NT * 4 + 16;  // 16 bytes between rows: rows begin on other banks
   uint8_t* mine = ring + wave * 32 * kPitch;
-  constexpr int kLanes = 4 * NT;  // a row
+  constexpr int kEach = 16 / (int)sizeof(O);
+  constexpr int kLanes = 32 * NT / kEach;  // a row
   constexpr int kRows = 64 / kLanes;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -250,22 +286,37 @@ __device__ __forceinline__ void drain(uint8_t* ring, int m0, int n0, int wave, i
             floatx4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
 #pragma unroll
     for (int r = 0; r < 32 / kRows; ++r) {
-      const int row = r * kRows + lane / kLanes, column = 8 * (lane % kLanes);
+      const int row = r * kRows + lane / kLanes, column = kEach * (lane % kLanes);
       const floatx4* at = reinterpret_cast<const floatx4*>(mine + row * kPitch + column * 4);
-      const floatx4 lo = at[0], hi = at[1];
-      const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      float v[kEach];
+#pragma unroll
+      for (int c = 0; c < kEach; c += 4) {
+        const floatx4 part = at[c / 4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[c + k] = part[k];
+      }
       put(m0 + 32 * i + row, n0 + column, v);
     }
   }
 }
 
+// 16 bytes of O, to and from an aligned place.
 template <typename O>
-__device__ __forceinline__ void store(O* p, const float (&v)[8]) {
-  Eight<O> r;
+struct Line {
+  static constexpr int kEach = 16 / (int)sizeof(O);
+  typedef O vec __attribute__((ext_vector_type(kEach)));
+  static __device__ __forceinline__ void store(O* p, const float (&v)[kEach]) {
+    vec r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = (O)v[i];
-  store8<kStreamed>(p, r);
-}
+    for (int i = 0; i < kEach; ++i) r[i] = (O)v[i];
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, r), reinterpret_cast<u32x4*>(p));
+  }
+  static __device__ __forceinline__ void add(const O* p, float (&v)[kEach]) {
+    const vec r = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) v[i] += (float)r[i];
+  }
+};
 
 }  // namespace tile
 }  // namespace w4a16

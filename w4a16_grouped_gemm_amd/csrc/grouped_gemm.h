@@ -41,7 +41,7 @@ struct WgradParams {
   const void* dout;       // [capacity, N]
   const void* a;          // rows [a_rows, K]
   void* dw;               // [E, N, K]
-  float* partial;         // [splits, E, N, K] where splits > 1
+  float* partial;         // [splits, E, N, K] where there are several
   const int32_t* sorted;
   const int32_t* expert_ids;
   const int32_t* ntpp;
@@ -51,10 +51,14 @@ struct WgradParams {
   int32_t n_slots, capacity;
   int32_t log_block;      // of block_m, to base 2
   int32_t accumulate;
-  int32_t splits;         // wgrad_splits
+  WgradCut cut;
 };
-// How many workgroups share an expert's rows, a rule on sizes alone.
-int32_t wgrad_splits(int32_t E, int32_t N, int32_t K, int32_t capacity);
+// How the weights' gradient is cut, a rule on sizes alone: tiles of tile x tile values, and how many workgroups share an
+// expert's rows.
+struct WgradCut {
+  int32_t tile, splits;
+};
+WgradCut wgrad_cut(int32_t E, int32_t N, int32_t K, int32_t capacity);
 int64_t wgrad_workgroups(int32_t E, int32_t N, int32_t K, int32_t splits);
 hipError_t launch_grouped_wgrad(const WgradParams& p, int32_t dtype, int32_t dw_dtype, hipStream_t stream);
 

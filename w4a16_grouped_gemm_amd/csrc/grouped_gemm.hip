@@ -3,9 +3,10 @@
 //   out[p, n] = sum_k A[r(p), k] W[e(p), n, k]     (or W[e(p), k, n])
 // with e(p) the expert of p's block and r(p) the row itself or its slot's token.
 //
+// Weights and rows go from memory straight to LDS (global_load_lds) and from there to the mfma
+// instructions (gemm_tile.h).
 // An expert's blocks lie side by side, so a tile takes as many of them as its rows hold, whatever
 // block_m is.
-// The copies to LDS (global_load_lds) and the mfma loop are in gemm_tile.h.
 #include "gemm_tile.h"
 #include "grouped_gemm.h"
 #include "row_ops.h"
@@ -17,8 +18,6 @@ namespace w4a16 {
 namespace {
 
 using namespace tile;
-
-constexpr int kTileN = 256;
 
 // Tile (row tile, column tile) of this workgroup: row tiles go in groups of kTileGroup with all their columns,
 // row tiles innermost. Workgroups go round-robin to the 8 XCDs, each with an L2 of its own, so XCD x
@@ -37,23 +36,45 @@ __device__ __forceinline__ void tile_of(int ntiles, int64_t& row_tile, int& colu
 }
 
 // Row tile `target`: the tiles are the runs of blocks of one expert, cut into 1 << log_per
-// blocks. Returns how many tiles there are, and of this one its first block and its number of blocks (0 where
-// there is none). All threads of the workgroup call it. Counting here needs no launch or memory of its
-// own. (A workgroup for every block, of which those inside a tile end at once, costs more: they went to every
-// other shader engine and left its compute units idle, 2880 us instead of 1805 at 32768 rows, 16 experts,
-// 4096 x 7168.)
+// blocks. All threads of the workgroup call it. Counting here needs no launch or memory of its own. (A workgroup for every
+// block, of which those inside a tile end at once, costs more: they went to every other shader engine and left its
+// compute units idle, 2880 us instead of 1805 at 32768 rows, 16 experts, 4096 x 7168.)
 struct Scan {
   int last[kWaves];   // last block of a wave's 64 where a run begins, or -1
   int count[kWaves];  // tiles that begin in a wave's blocks
   int found;
 };
-__device__ __forceinline__ int64_t find_tile(const int32_t* expert_ids, int used, int log_per, int64_t target,
-                                             Scan& scan, int& block, int& blocks) {
+struct RowTile {
+  int64_t total;  // tiles there are
+  int block;      // the first block
+  int blocks;     // 0: no such tile
+  int expert;
+};
+__device__ __forceinline__ RowTile find_tile(const GroupedParams& p, int log_per, int64_t target, Scan& scan) {
   const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int per = 1 << log_per, held = p.capacity / p.block_m;
+  const int32_t* expert_ids = p.expert_ids;
   const uint64_t up_to = ~0ull >> (63 - lane);  // this lane and those below
+  const int first64 = expert_ids[min(lane, held - 1)];  // on its way together with the count
+  const int used = min(p.capacity, *p.ntpp) / p.block_m;
+  RowTile t = {0, 0, 0, 0};
+  if (used <= 64) {  // a lane a block, every wave by itself
+    const int previous = __shfl_up(first64, 1);
+    const uint64_t begins = __ballot(lane < used && (lane == 0 || first64 != previous));
+    const int start = 63 - __builtin_clzll((begins & up_to) | 1);
+    const uint64_t heads = __ballot(lane < used && ((lane - start) & (per - 1)) == 0);
+    t.total = __builtin_popcountll(heads);
+    if (target >= t.total) return t;
+    const uint64_t found = __ballot((heads >> lane & 1) && __builtin_popcountll(heads & up_to) == target + 1);
+    t.block = __builtin_ctzll(found);
+    const uint64_t after = t.block == 63 ? 0 : (begins | heads) >> (t.block + 1);  // where the next tile begins
+    t.blocks = min(after ? __builtin_ctzll(after) + 1 : used - t.block, used - t.block);
+    t.expert = __builtin_amdgcn_readlane(first64, t.block);
+    return t;
+  }
+  if (target >= used) return t;
   if (threadIdx.x == 0) scan.found = -1;
-  int begun = 0;       // where the run at the chunk's start begins
-  int64_t before = 0;  // tiles in the chunks before
+  int begun = 0;  // where the run at the chunk's start begins
   for (int chunk = 0; chunk < used; chunk += kThreads) {
     const int b = chunk + (int)threadIdx.x;
     const int e = expert_ids[min(b, used - 1)], previous = expert_ids[max(min(b, used) - 1, 0)];
@@ -67,51 +88,52 @@ __device__ __forceinline__ int64_t find_tile(const int32_t* expert_ids, int used
     }
     const uint64_t mine = begins & up_to;
     if (mine) start = b - lane + 63 - __builtin_clzll(mine);
-    const uint64_t heads = __ballot(b < used && ((b - start) & ((1 << log_per) - 1)) == 0);
+    const uint64_t heads = __ballot(b < used && ((b - start) & (per - 1)) == 0);
     if (lane == 0) scan.count[wave] = __builtin_popcountll(heads);
     __syncthreads();
-    int64_t index = before + __builtin_popcountll(heads & up_to) - 1;
+    int64_t index = t.total + __builtin_popcountll(heads & up_to) - 1;
     for (int i = 0; i < kWaves; ++i) {
       if (i < wave) index += scan.count[i];
-      before += scan.count[i];
+      t.total += scan.count[i];
     }
     if (index == target && (heads >> lane & 1)) scan.found = b;
   }
   __syncthreads();
-  block = __builtin_amdgcn_readfirstlane(scan.found);
+  t.block = __builtin_amdgcn_readfirstlane(scan.found);
   __syncthreads();  // the ring's copies go where the counts are
-  blocks = 0;
-  if (block >= 0) {
-    const int i = block + lane;
-    const uint64_t other =
-        ~__ballot(lane < 1 << log_per && i < used && expert_ids[min(i, used - 1)] == expert_ids[block]);
-    blocks = __builtin_ctzll(other);  // at most 16 to a tile, so lane 16 is another
-  }
-  return before;
+  if (t.block < 0) return t;
+  t.expert = expert_ids[t.block];
+  const int i = t.block + lane;
+  const uint64_t other = ~__ballot(lane < per && i < used && expert_ids[min(i, used - 1)] == t.expert);
+  t.blocks = __builtin_ctzll(other);  // at most 16 to a tile, so lane 16 is another
+  return t;
 }
 
-// A tile of up to 32 WM MT rows and 256 columns; waves lie WM deep, 8 / WM wide.
-template <typename T, typename O, bool TRANSPOSED, int WM, int MT>
-__device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, int first, int rows, int e, int n0) {
-  constexpr int WN = kWaves / WM;
-  constexpr int NT = kTileN / (32 * WN);
-  typedef RowPanel<32 * WM * MT> M;
-  typedef std::conditional_t<TRANSPOSED, ColumnPanel<kTileN>, RowPanel<kTileN>> N;
-  int lane = (int)threadIdx.x & 63;
-  asm volatile("" : "+v"(lane));  // addresses made of it are made here: before the loop around this they would spill
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  floatx16 acc[MT][NT] = {};
-  M m;
+// A way to compute tiles: 64 MT rows by 128 NT columns, waves two deep and four wide, kAhead stages in LDS.
+template <int MT_, int NT_, int kAhead_>
+struct Way {
+  static constexpr int MT = MT_, NT = NT_, kAhead = kAhead_;
+  static constexpr int kRows = 64 * MT, kTileN = 128 * NT;
+  static constexpr int kRing = kRingBytes<RowPanel<kRows>, RowPanel<kTileN>, kAhead>;
+  typedef Way<(MT + 1) / 2, NT, kAhead> Half;
+};
+
+// Where the wave's copies of rows come from: row i of the tile, or row 0 where it has no slot (zeroed at the store).
+template <typename T, typename M>
+__device__ __forceinline__ void set_rows(M& m, const GroupedParams& p, int first, int rows, int wave, int lane) {
 #pragma unroll
   for (int i = 0; i < M::kMine; ++i) {
-    // a row without a slot reads row 0 and is zeroed at the store
     const int row = M::row_of(i, wave, lane);
     const uint32_t slot = row < rows ? (uint32_t)p.sorted[first + row] : ~0u;
     const int64_t from = slot >= (uint32_t)p.n_slots ? 0 : p.gather ? (int64_t)p.by_topk.of(slot) : first + row;
     m.set(i, static_cast<const T*>(p.a) + from * p.K, wave, lane);
   }
+}
+
+// Of weights: expert e's columns from n0 on; a column past the last is a copy of another, and not stored.
+template <typename T, bool TRANSPOSED, typename N>
+__device__ __forceinline__ void set_weights(N& n, const GroupedParams& p, int e, int n0, int wave, int lane) {
   const T* w = static_cast<const T*>(p.w) + (int64_t)e * p.N * p.K;
-  N n;
   if constexpr (TRANSPOSED) {
     n.set(w + n0, (int64_t)p.N, p.N - n0, wave, lane);
   } else {
@@ -119,8 +141,23 @@ __device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, i
     for (int i = 0; i < N::kMine; ++i)
       n.set(i, w + (int64_t)min(n0 + N::row_of(i, wave, lane), p.N - 1) * p.K, wave, lane);
   }
-  const int at_m = wave / WN * 32 * MT, at_n = wave % WN * 32 * NT;
-  loop<T, M, N>(
+}
+
+template <typename T, typename O, bool TRANSPOSED, typename W>
+__device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, int first, int rows, int e, int n0) {
+  constexpr int MT = W::MT, NT = W::NT;
+  typedef RowPanel<W::kRows> M;
+  typedef std::conditional_t<TRANSPOSED, ColumnPanel<W::kTileN>, RowPanel<W::kTileN>> N;
+  int lane = (int)threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // addresses made of it are made here: before the loop around this they would spill
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  floatx16 acc[MT][NT] = {};
+  M m;
+  set_rows<T>(m, p, first, rows, wave, lane);
+  N n;
+  set_weights<T, TRANSPOSED>(n, p, e, n0, wave, lane);
+  const int at_m = wave / 4 * 32 * MT, at_n = wave % 4 * 32 * NT;
+  loop<T, M, N, W::kAhead>(
       ring, (p.K + kStep - 1) / kStep, at_m, at_n, lane, acc,
       [&](int q, uint32_t slot, int stage) { m.copy(q, slot, p.K - stage * kStep, wave); },
       [&](int q, uint32_t slot, int stage) { n.copy(q, slot, p.K - stage * kStep, wave); }, [] {});
@@ -130,63 +167,173 @@ __device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, i
     const int row = at_m + 32 * i + (lane & 31);
     slotted[i] = (uint32_t)__ballot(row < rows && (uint32_t)p.sorted[first + min(row, rows - 1)] < (uint32_t)p.n_slots);
   }
-  drain(ring, at_m, at_n, wave, lane, acc, [&](int row, int column, const float (&v)[8]) {
+  drain<O>(ring, at_m, at_n, wave, lane, acc, [&](int row, int column, float (&v)[Line<O>::kEach]) {
     if (row >= rows || n0 + column >= p.N) return;
     const bool real = slotted[(row - at_m) / 32] >> (row & 31) & 1;
-    float sums[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[i] = real ? v[i] : 0.f;
-    store(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + n0 + column, sums);
+    for (int i = 0; i < Line<O>::kEach; ++i) v[i] = real ? v[i] : 0.f;
+    Line<O>::store(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + n0 + column, v);
   });
 }
 
-// Tiles of 32 WM MT rows; a run's last tile takes the half of them where it has no more.
-template <typename T, typename O, bool TRANSPOSED, int WM, int MT>
-__global__ __launch_bounds__(kThreads, MT == 4 ? 2 : 4) void grouped_kernel(GroupedParams p, int ntiles, int row_tiles,
-                                                                            int log_per) {
-  constexpr int kRows = 32 * WM * MT;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes<RowPanel<kRows>, RowPanel<kTileN>>];
-  const int used = min(p.capacity, *p.ntpp) / p.block_m;
+// A run's last tile takes half of the rows where it has no more.
+template <typename T, typename O, bool TRANSPOSED, typename W>
+__global__ __launch_bounds__(kThreads, W::kRing > 80 * 1024 ? 2 : 4) void grouped_kernel(GroupedParams p, int ntiles,
+                                                                                         int row_tiles, int log_per,
+                                                                                         int log_cut) {
+  constexpr int kRows = W::kRows, kTileN = W::kTileN;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[W::kRing];
   int64_t target;
   int nt;
   tile_of(ntiles, target, nt);
   if (target >= row_tiles) return;
   // more tiles than moe_align's order can have: go round again
-  for (; target < used; target += row_tiles) {
-    int b, blocks;
-    const int64_t total = find_tile(p.expert_ids, used, log_per, target, *reinterpret_cast<Scan*>(ring), b, blocks);
-    if (blocks == 0) return;
-    const int e = p.expert_ids[b];
-    const int first = b * p.block_m, rows = blocks * p.block_m, n0 = nt * kTileN;
+  for (;; target += row_tiles) {
+    const RowTile tile = find_tile(p, log_per, target >> log_cut, *reinterpret_cast<Scan*>(ring));
+    if (tile.blocks == 0) return;
+    const int e = tile.expert;
+    const int first = tile.block * p.block_m + (int)(target & ((1 << log_cut) - 1)) * kRows;
+    const int rows = min(tile.blocks * p.block_m, kRows), n0 = nt * kTileN;
     if ((uint32_t)e >= (uint32_t)p.E) {  // no such expert
-      const float zero[8] = {};
-      for (int i = (int)threadIdx.x; i < rows * (kTileN / 8); i += kThreads) {
-        const int row = i / (kTileN / 8), column = n0 + 8 * (i % (kTileN / 8));
-        if (column < p.N) store(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + column, zero);
+      constexpr int kEach = Line<O>::kEach, kLanes = kTileN / kEach;
+      const float zero[kEach] = {};
+      for (int i = (int)threadIdx.x; i < rows * kLanes; i += kThreads) {
+        const int row = i / kLanes, column = n0 + kEach * (i % kLanes);
+        if (column < p.N) Line<O>::store(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + column, zero);
       }
-    } else if (MT > 1 && rows <= kRows / 2) {
-      product<T, O, TRANSPOSED, WM, (MT + 1) / 2>(p, ring, first, rows, e, n0);
+    } else if (W::MT > 1 && rows <= kRows / 2) {
+      product<T, O, TRANSPOSED, typename W::Half>(p, ring, first, rows, e, n0);
     } else {
-      product<T, O, TRANSPOSED, WM, MT>(p, ring, first, rows, e, n0);
+      product<T, O, TRANSPOSED, W>(p, ring, first, rows, e, n0);
     }
-    if (target + row_tiles >= total) return;
+    if (target + row_tiles >= tile.total << log_cut) return;
     __syncthreads();
   }
 }
 
+// Few rows an expert, or little work at all: a tile of 32 rows by 32 NT columns, shared by the waves along K.
+template <typename T, typename O, bool TRANSPOSED, int NT, int kAhead>
+__global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, int ntiles, int row_tiles, int log_per,
+                                                          int log_cut) {
+  constexpr int kRows = 32, kTileN = 32 * NT, kSteps = 128;
+  typedef RowPanel<kRows, kSteps> M;
+  typedef std::conditional_t<TRANSPOSED, ColumnPanel<kTileN, kSteps>, RowPanel<kTileN, kSteps>> N;
+  constexpr int kRing = kAhead * (M::kBytes + N::kBytes), kSums = kWaves * kRows * kTileN * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kRing > kSums ? kRing : kSums];
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  int64_t target;
+  int nt;
+  tile_of(ntiles, target, nt);
+  if (target >= row_tiles) return;
+  for (;; target += row_tiles) {
+    const RowTile tile = find_tile(p, log_per, target >> log_cut, *reinterpret_cast<Scan*>(ring));
+    if (tile.blocks == 0) return;
+    const int e = tile.expert;
+    const int first = tile.block * p.block_m + (int)(target & ((1 << log_cut) - 1)) * kRows;
+    const int rows = min(tile.blocks * p.block_m, kRows), n0 = nt * kTileN;
+    floatx16 acc[NT] = {};
+    const bool known = (uint32_t)e < (uint32_t)p.E;
+    if (known) {
+      M m;
+      set_rows<T>(m, p, first, rows, wave, lane);
+      N n;
+      set_weights<T, TRANSPOSED>(n, p, e, n0, wave, lane);
+      shared_loop<T, M, N, kAhead>(ring, (p.K + kSteps - 1) / kSteps, wave, lane, acc, [&](uint32_t slot, int stage) {
+        const int left = p.K - stage * kSteps;
+#pragma unroll
+        for (int i = 0; i < M::kMine; ++i) m.copy(i, slot, left, wave);
+#pragma unroll
+        for (int i = 0; i < N::kMine; ++i) n.copy(i, slot + M::kBytes, left, wave);
+      });
+    }
+    // the waves' shares, added in wave order; a thread's four columns
+    floatx4* sums = reinterpret_cast<floatx4*>(ring);  // [wave][32 rows][8 NT]
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int row = lane & 31, c = 8 * j + 2 * g + (lane >> 5);
+        sums[(wave * 32 + row) * (8 * NT) + (c ^ (row & 7))] =
+            floatx4{acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+      }
+    __syncthreads();
+    for (int i = (int)threadIdx.x; i < 32 * 8 * NT; i += kThreads) {
+      const int row = i / (8 * NT), c = i % (8 * NT);
+      floatx4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) v += sums[(k * 32 + row) * (8 * NT) + (c ^ (row & 7))];
+      if (row < rows && n0 + 4 * c < p.N) {
+        const bool real = known && (uint32_t)p.sorted[first + row] < (uint32_t)p.n_slots;
+        typedef O vec __attribute__((ext_vector_type(4)));
+        vec out;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = (O)(real ? v[k] : 0.f);
+        *reinterpret_cast<vec*>(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + n0 + 4 * c) = out;
+      }
+    }
+    if (target + row_tiles >= tile.total << log_cut) return;
+    __syncthreads();
+  }
+}
+
+// How the call is cut into tiles of `rows` rows by `columns` columns.
+struct Cut {
+  int ntiles, row_tiles, log_per, log_cut;
+  dim3 grid;
+};
+Cut cut(const GroupedParams& p, int rows, int columns) {
+  const int per = std::max(1, rows / p.block_m), pieces = std::max(1, p.block_m / rows), blocks = p.capacity / p.block_m;
+  Cut c;
+  c.ntiles = (p.N + columns - 1) / columns;
+  // an expert's last tile may be of fewer blocks
+  c.row_tiles = (std::min(blocks, blocks / per + p.E) * pieces + kTileGroup - 1) / kTileGroup * kTileGroup;
+  c.log_per = __builtin_ctz((unsigned)per);
+  c.log_cut = __builtin_ctz((unsigned)pieces);
+  const int64_t tiles = (int64_t)c.row_tiles * c.ntiles;
+  c.grid = dim3((unsigned)((tiles + kXcds * kChunk - 1) / (kXcds * kChunk) * (kXcds * kChunk)));
+  return c;
+}
+
+template <typename T, typename O, bool TRANSPOSED, typename W>
+hipError_t launch_tiles(const GroupedParams& p, hipStream_t stream) {
+  const Cut c = cut(p, W::kRows, W::kTileN);
+  hipLaunchKernelGGL((grouped_kernel<T, O, TRANSPOSED, W>), c.grid, dim3(kThreads), 0, stream, p, c.ntiles, c.row_tiles,
+                     c.log_per, c.log_cut);
+  return hipGetLastError();
+}
+
+template <typename T, typename O, bool TRANSPOSED, int NT, int kAhead>
+hipError_t launch_narrow(const GroupedParams& p, hipStream_t stream) {
+  const Cut c = cut(p, 32, 32 * NT);
+  hipLaunchKernelGGL((narrow_kernel<T, O, TRANSPOSED, NT, kAhead>), c.grid, dim3(kThreads), 0, stream, p, c.ntiles,
+                     c.row_tiles, c.log_per, c.log_cut);
+  return hipGetLastError();
+}
+
+// Which way, by the tiles that the call is expected to have. The counts are on the device, so an expert's rows are taken
+// as n_slots over E, their mean where every routed expert is resident; on a slice of the experts that counts
+// the others' slots too, and larger tiles may be taken than the slice's rows fill. Results do not
+// depend on the way but for the order of their sums. Measured, us by (256 x 256, 128 x 128, 64 x 128, 32 x 64) tiles,
+// bf16, K last: one expert of 4096 rows, 4096 x 4096: 118, 149, 192, 358; 8 experts of 256, 2048 x 2048: 55, 36,
+// 42, 64; 48 of 85, 7168 x 2048: 392, 397, 465, 879; one of 512 rows, 2048 x 2048: 45, 21, 18, 14; 10 of 77, 1384 x 1000
+// transposed: 23, 16, 18, 17; 384 of 11, 512 x 7168: 589, 548, 543, 528, and 7168 x 512 transposed: 721, 674, 628, 776;
+// 48 of 3 (384 routed), 4096 x 7168: 544, 497, 493, 481, transposed 579, 518, 504, 515; 8 experts of one row, 512 x
+// 7168: 82, 62, 50, 28, and by 32 x 32 tiles 21.
 template <typename T, typename O, bool TRANSPOSED>
 hipError_t launch(const GroupedParams& p, hipStream_t stream) {
-  constexpr int kRows = 256;
-  const int ntiles = (p.N + kTileN - 1) / kTileN, per = std::max(1, kRows / p.block_m);
-  const int blocks = p.capacity / p.block_m;
-  if (blocks == 0) return hipSuccess;
-  // an expert's last tile may be of fewer blocks
-  const int row_tiles = (std::min(blocks, blocks / per + p.E) + kTileGroup - 1) / kTileGroup * kTileGroup;
-  const int64_t tiles = (int64_t)row_tiles * ntiles;
-  const int64_t grid = (tiles + kXcds * kChunk - 1) / (kXcds * kChunk) * (kXcds * kChunk);
-  hipLaunchKernelGGL((grouped_kernel<T, O, TRANSPOSED, 2, 4>), dim3((unsigned)grid), dim3(kThreads), 0, stream, p,
-                     ntiles, row_tiles, __builtin_ctz(per));
-  return hipGetLastError();
+  const int64_t experts = std::min(p.E, p.n_slots), rows = (p.n_slots + experts - 1) / experts;
+  auto tiles = [&](int64_t r, int64_t columns) {
+    return experts * ((rows + r / 2 - 1) / r + (rows <= r / 2)) * ((p.N + columns - 1) / columns);
+  };
+  if (rows <= 48) {  // an expert's rows are one tile or two: what counts is the weights' stream
+    if (TRANSPOSED && tiles(64, 128) >= 64) return launch_tiles<T, O, TRANSPOSED, Way<1, 1, 3>>(p, stream);
+  } else {
+    if (tiles(256, 256) >= 112 && p.N > 128) return launch_tiles<T, O, TRANSPOSED, Way<4, 2, 2>>(p, stream);
+    if (tiles(128, 128) >= 96) return launch_tiles<T, O, TRANSPOSED, Way<2, 1, 2>>(p, stream);
+  }
+  if (!TRANSPOSED && tiles(32, 64) < 128) return launch_narrow<T, O, TRANSPOSED, 1, 5>(p, stream);
+  return launch_narrow<T, O, TRANSPOSED, 2, 3>(p, stream);
 }
 
 template <typename T, typename O>
@@ -201,6 +348,7 @@ int64_t grouped_workgroups(int32_t N, int32_t capacity, int32_t block_m) {
 }
 
 hipError_t launch_grouped_gemm(const GroupedParams& p, int32_t dtype, int32_t out_dtype, hipStream_t stream) {
+  if (p.capacity < p.block_m) return hipSuccess;  // no whole block
   if (dtype == kBF16)
     return out_dtype == kFP32 ? launch<bf16_t, float>(p, stream) : launch<bf16_t, bf16_t>(p, stream);
   return out_dtype == kFP32 ? launch<f16_t, float>(p, stream) : launch<f16_t, f16_t>(p, stream);

@@ -5,14 +5,14 @@
 // A workgroup computes a square tile of one expert's dW over all of its rows (or, where the tiles
 // are few, a share of them, and a second kernel adds the shares in their order). Both operands
 // are column panels: the rows are the steps of the sum. Rows without a slot, whatever they
-// hold, are replaced by zeros as they are copied to LDS.
-// The copies to LDS (global_load_lds) and the mfma loop are in gemm_tile.h.
+// hold, are replaced by zeros as they are copied to LDS (global_load_lds); the mfma loop is in gemm_tile.h.
 #include "gemm_tile.h"
 #include "grouped_gemm.h"
 #include "row_ops.h"
 
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 
 namespace w4a16 {
 namespace {
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
   constexpr int kRows = 64 / Panel::kLanes;  // of a copy
   constexpr int kMine = Panel::kMine;
   static_assert(kMine * kRows == 8, "eight rows a wave");
-  __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes<Panel, Panel>];
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes<Panel, Panel, 2>];
   int* const run = reinterpret_cast<int*>(ring);
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
   __syncthreads();  // the ring's copies go where the run is
   const int first = last < 0 ? 0 : begun << p.log_block;
   const int end = last < 0 ? 0 : (last + 1) << p.log_block;
-  const int share = (((end - first + kStep - 1) / kStep + p.splits - 1) / p.splits) * kStep;
+  const int share = (((end - first + kStep - 1) / kStep + p.cut.splits - 1) / p.cut.splits) * kStep;
   const int begin = min((int64_t)first + (int64_t)share * blockIdx.y, (int64_t)end);
   const int stop = min((int64_t)begin + share, (int64_t)end);
   const int stages = (stop - begin + kStep - 1) / kStep;
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
     };
     look(of_m, 0);
     look(of_n, 0);
-    loop<T, Panel, Panel>(
+    loop<T, Panel, Panel, 2>(
         ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc,
         [&](int q, uint32_t lds, int stage) {
           copy(of_m, at_m[q], slot_of(of_m, q), q, lds);
@@ -141,43 +141,38 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
   }
 
   const int64_t size = (int64_t)p.E * p.N * p.K;
-  drain(ring, wave / 4 * 32 * MT, wave % 4 * 32 * NT, wave, lane, acc, [&](int n, int k, const float (&v)[8]) {
-    if (m0 + n >= p.N || n0 + k >= p.K) return;
-    const int64_t at = ((int64_t)e * p.N + m0 + n) * p.K + n0 + k;
-    if (p.splits > 1) {
-      store(p.partial + (int64_t)blockIdx.y * size + at, v);
-      return;
-    }
-    O* dw = static_cast<O*>(p.dw) + at;
-    float sums[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sums[i] = v[i];
-    if (p.accumulate) {
-      const Eight<O> old = load8(dw);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sums[i] += (float)old.v[i];
-    }
-    store(dw, sums);
-  });
+  if (p.cut.splits > 1) {
+    float* partial = p.partial + (int64_t)blockIdx.y * size;
+    drain<float>(ring, wave / 4 * 32 * MT, wave % 4 * 32 * NT, wave, lane, acc, [&](int n, int k, float (&v)[4]) {
+      if (m0 + n < p.N && n0 + k < p.K) Line<float>::store(partial + ((int64_t)e * p.N + m0 + n) * p.K + n0 + k, v);
+    });
+  } else {
+    drain<O>(ring, wave / 4 * 32 * MT, wave % 4 * 32 * NT, wave, lane, acc, [&](int n, int k, float (&v)[Line<O>::kEach]) {
+      if (m0 + n >= p.N || n0 + k >= p.K) return;
+      O* dw = static_cast<O*>(p.dw) + ((int64_t)e * p.N + m0 + n) * p.K + n0 + k;
+      if (p.accumulate) Line<O>::add(dw, v);
+      Line<O>::store(dw, v);
+    });
+  }
 }
 
 // dW (+)= the shares, in their order.
 template <typename O>
 __global__ __launch_bounds__(256) void join_kernel(const float* partial, O* dw, int64_t size, int32_t splits,
                                                    int32_t accumulate) {
-  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < size; at += (int64_t)gridDim.x * 256 * 8) {
-    float sums[8] = {};
-    for (int s = 0; s < splits; ++s) {
-      const Eight<float> part = load8(partial + s * size + at);
+  constexpr int kEach = Line<O>::kEach;
+  const int64_t stride = (int64_t)gridDim.x * 256 * kEach;
+  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kEach; at < size; at += stride) {
+    float sums[kEach] = {};
+    for (int s = 0; s < splits; ++s)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sums[i] += part.v[i];
-    }
-    if (accumulate) {
-      const Eight<O> old = load8(dw + at);
+      for (int i = 0; i < kEach; i += 4) {
+        const floatx4 part = *reinterpret_cast<const floatx4*>(partial + s * size + at + i);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sums[i] += (float)old.v[i];
-    }
-    store(dw + at, sums);
+        for (int k = 0; k < 4; ++k) sums[i + k] += part[k];
+      }
+    if (accumulate) Line<O>::add(dw + at, sums);
+    Line<O>::store(dw + at, sums);
   }
 }
 
@@ -186,7 +181,7 @@ hipError_t launch_tile(const WgradParams& p, hipStream_t stream) {
   const int mtiles = (p.N + kTile - 1) / kTile, ntiles = (p.K + kTile - 1) / kTile;
   const int64_t chunk = ((int64_t)mtiles * ntiles + kXcds - 1) / kXcds;
   const int64_t grid = chunk * kXcds * p.E;
-  const dim3 g((unsigned)grid, (unsigned)p.splits), t(kThreads);
+  const dim3 g((unsigned)grid, (unsigned)p.cut.splits), t(kThreads);
   if (p.gather)
     hipLaunchKernelGGL((wgrad_kernel<T, O, kTile, true>), g, t, 0, stream, p, mtiles, ntiles);
   else
@@ -196,12 +191,12 @@ hipError_t launch_tile(const WgradParams& p, hipStream_t stream) {
 
 template <typename T, typename O>
 hipError_t launch(const WgradParams& p, hipStream_t stream) {
-  const hipError_t err = launch_tile<T, O, 256>(p, stream);
-  if (err != hipSuccess || p.splits == 1) return err;
+  const hipError_t err = p.cut.tile == 256 ? launch_tile<T, O, 256>(p, stream) : launch_tile<T, O, 128>(p, stream);
+  if (err != hipSuccess || p.cut.splits == 1) return err;
   const int64_t size = (int64_t)p.E * p.N * p.K;
-  const int64_t grid = std::min<int64_t>((size / 8 + 255) / 256, (int64_t)device_cu_count() * 32);
+  const int64_t grid = std::min<int64_t>((size / Line<O>::kEach + 255) / 256, (int64_t)device_cu_count() * 32);
   hipLaunchKernelGGL((join_kernel<O>), dim3((unsigned)grid), dim3(256), 0, stream, p.partial, static_cast<O*>(p.dw),
-                     size, p.splits, p.accumulate);
+                     size, p.cut.splits, p.accumulate);
   return hipGetLastError();
 }
 
@@ -212,10 +207,14 @@ int64_t wgrad_workgroups(int32_t E, int32_t N, int32_t K, int32_t splits) {
   return (tiles + kXcds - 1) / kXcds * kXcds * E * splits;
 }
 
-int32_t wgrad_splits(int32_t E, int32_t N, int32_t K, int32_t capacity) {
-  const int64_t tiles = (int64_t)E * ((N + 255) / 256) * ((K + 255) / 256);
+WgradCut wgrad_cut(int32_t E, int32_t N, int32_t K, int32_t capacity) {
+  const char* v = getenv("WG");
+  auto tiles = [&](int64_t t) { return E * ((N + t - 1) / t) * ((K + t - 1) / t); };
   const int64_t rows = capacity / E;
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, rows / 256, 16}));
+  WgradCut c;
+  c.tile = v ? atoi(v) / 100 : tiles(256) >= 256 ? 256 : 128;
+  c.splits = v ? atoi(v) % 100 : (int32_t)std::max<int64_t>(1, std::min<int64_t>({(c.tile == 256 ? 256 : 512) / tiles(c.tile), rows / 256, 16}));
+  return c;
 }
 
 hipError_t launch_grouped_wgrad(const WgradParams& p, int32_t dtype, int32_t dw_dtype, hipStream_t stream) {
