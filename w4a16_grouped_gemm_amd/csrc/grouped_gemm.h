@@ -37,6 +37,11 @@ struct GroupedParams {
 int64_t grouped_workgroups(int32_t N, int32_t capacity, int32_t block_m);
 hipError_t launch_grouped_gemm(const GroupedParams& p, int32_t dtype, int32_t out_dtype, hipStream_t stream);
 
+// How the weights' gradient is cut, a rule on sizes alone: tiles of tile x tile values, and how many workgroups share an
+// expert's rows.
+struct WgradCut {
+  int32_t tile, splits;
+};
 struct WgradParams {
   const void* dout;       // [capacity, N]
   const void* a;          // rows [a_rows, K]
@@ -52,11 +57,6 @@ struct WgradParams {
   int32_t log_block;      // of block_m, to base 2
   int32_t accumulate;
   WgradCut cut;
-};
-// How the weights' gradient is cut, a rule on sizes alone: tiles of tile x tile values, and how many workgroups share an
-// expert's rows.
-struct WgradCut {
-  int32_t tile, splits;
 };
 WgradCut wgrad_cut(int32_t E, int32_t N, int32_t K, int32_t capacity);
 int64_t wgrad_workgroups(int32_t E, int32_t N, int32_t K, int32_t splits);
