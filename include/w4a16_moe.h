@@ -604,8 +604,7 @@ int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q
  *                      weights as they are trained, no repacking
  *   out                device [capacity, N] of out_dtype (`dtype` or fp32)
  * a, w and out must be 16-byte aligned; out overlaps neither. No workspace; sums have a
- * fixed order, so runs on the same inputs give the same bits. capacity / block_m *
- * ceil(N / 128) must be under 2^23 - 8 (else W4A16_ERR_UNSUPPORTED). */
+ * fixed order, so runs on the same inputs give the same bits. */
 int moe_grouped_gemm(int32_t num_experts, int32_t N, int32_t K, const void* a, int32_t dtype, int32_t a_rows,
                      int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids, int32_t capacity,
                      const int32_t* expert_ids, const int32_t* num_tokens_post_padded, int32_t block_m, const void* w,
@@ -630,7 +629,7 @@ size_t moe_grouped_gemm_wgrad_workspace_bytes(int32_t num_experts, int32_t N, in
  *                      capacity) bytes (may be NULL when that is 0; else
  *                      W4A16_ERR_WORKSPACE); calls that overlap need one each
  * dout, a, dw and workspace must be 16-byte aligned; dw overlaps none of them. Sums have a
- * fixed order. Limits of sizes as above; num_experts * (ceil(N / 128) * ceil(K / 128) + 7)
+ * fixed order. Limits of sizes as above; num_experts * (ceil(N / 256) * ceil(K / 256) + 7)
  * must be under 2^23 (else W4A16_ERR_UNSUPPORTED). */
 int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void* dout, const void* a, int32_t dtype,
                            int32_t a_rows, int32_t gather, int32_t T, int32_t topk, const int32_t* sorted_token_ids,

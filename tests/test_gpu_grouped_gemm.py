@@ -44,6 +44,10 @@ SHAPES = [
     (200, 3, 4, 4, 264, 328, 128), (600, 1, 1, 1, 520, 192, 128), (700, 2, 3, 3, 136, 712, 128),
     (64, 8, 60, 64, 64, 512, 16), (520, 1, 2, 2, 1000, 88, 16), (260, 1, 1, 1, 96, 264, 32),
     (1000, 2, 6, 8, 384, 96, 64),
+    # large tiles, with full, half and nearly empty ones, and blocks larger and smaller than a tile
+    (300, 1, 1, 1, 28928, 72, 128), (500, 2, 3, 3, 10248, 136, 16), (900, 2, 8, 9, 4104, 64, 64), (700, 1, 3, 3, 2056, 136, 128),
+    (40, 2, 8, 8, 1032, 200, 128), (40, 2, 8, 8, 1032, 200, 16), (150, 2, 5, 5, 4104, 2056, 32), (130, 1, 2, 2, 1032, 1160, 128),
+    (1300, 1, 1, 1, 1032, 1160, 64), (5000, 1, 1, 1, 8, 24, 128), (6000, 2, 2, 2, 200, 136, 16),
 ]
 
 

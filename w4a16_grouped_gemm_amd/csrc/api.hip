@@ -896,7 +896,6 @@ int moe_grouped_gemm(int32_t num_experts, int32_t N, int32_t K, const void* a, i
   if (T == 0 || capacity == 0) return W4A16_OK;  // no slot, no row
   if (!a || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !w || !out) return W4A16_ERR_INVALID_ARG;
   if (!all_aligned16(a, w, out)) return W4A16_ERR_INVALID_ARG;
-  if (grouped_workgroups(N, capacity, block_m) >= kMaxWorkgroups) return W4A16_ERR_UNSUPPORTED;
   GroupedParams p{};
   p.a = a;
   p.w = w;
@@ -936,7 +935,7 @@ int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void
     return W4A16_ERR_INVALID_ARG;
   if (!all_aligned16(dout, a, dw, workspace)) return W4A16_ERR_INVALID_ARG;
   const WgradCut cut = wgrad_cut(num_experts, N, K, capacity);
-  if (wgrad_workgroups(num_experts, N, K, cut.splits) >= kMaxWorkgroups) return W4A16_ERR_UNSUPPORTED;
+  if (wgrad_workgroups(num_experts, N, K, cut) >= kMaxWorkgroups) return W4A16_ERR_UNSUPPORTED;
   const size_t need = moe_grouped_gemm_wgrad_workspace_bytes(num_experts, N, K, capacity);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
   WgradParams p{};

@@ -167,8 +167,22 @@ struct ColumnPanel {
 template <typename M, typename N, int kAhead>
 constexpr int kRingBytes = (kAhead + 1) * M::kBytes + kAhead * N::kBytes;
 
+// The first kAhead stages' copies. The slot of M after them stays as it is.
+template <typename M, typename N, int kAhead, int kBytesM, typename CopyM, typename CopyN>
+__device__ __forceinline__ void prologue(const uint8_t* ring, CopyM copy_m, CopyN copy_n) {
+  const uint32_t base_m = lds_address(ring), base_n = base_m + (kAhead + 1) * kBytesM;
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) {
+#pragma unroll
+    for (int q = 0; q < M::kMine; ++q) copy_m(q, base_m + s * kBytesM, s);
+#pragma unroll
+    for (int q = 0; q < N::kMine; ++q) copy_n(q, base_n + s * N::kBytes, s);
+  }
+}
+
 // All stages of a wave's 32 MT rows by 32 NT columns. copy_m(q, LDS address, stage) makes this wave's copy q of a
-// stage's panel M (M::kMine of them), copy_n of N. ring: kAhead + 1 stages of M, kAhead of N; free on return.
+// stage's panel M (M::kMine of them), copy_n of N. ring: kAhead + 1 stages of at most
+// kBytesM of M, kAhead of N; prologue has been called for them. All waves are past it on return.
 //
 // A stage is multiplied in four parts of 16 steps, a part's fragments being read from LDS while the part before
 // it is multiplied. Before the last part all waves meet: by then every wave has read all of stage s, and stage s + 1
@@ -178,14 +192,14 @@ constexpr int kRingBytes = (kAhead + 1) * M::kBytes + kAhead * N::kBytes;
 // parts after its issue. (32768 rows, 16 experts, 4096 x 7168, kAhead 2: 1618 us; both panels in two slots with
 // the copies in one part 1805, in two parts 1732, in all four 1904.) Copies past the last stage are of zeros.
 // settle() is where the wave has no LDS read on its way: scalar loads for the next copies are waited for there.
-template <typename T, typename M, typename N, int kAhead, int MT, int NT, typename CopyM, typename CopyN,
+template <typename T, typename M, typename N, int kAhead, int kBytesM, int MT, int NT, typename CopyM, typename CopyN,
           typename Settle>
 __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, int lane, floatx16 (&acc)[MT][NT],
                                      CopyM copy_m, CopyN copy_n, Settle settle) {
   static_assert(kAhead >= 2, "a stage is read while the next one lands");
   constexpr int kMfmas = MT * NT, kFragments = MT + NT;
-  uint8_t* const ring_n = ring + (kAhead + 1) * M::kBytes;
-  const uint32_t base_m = lds_address(ring), base_n = base_m + (kAhead + 1) * M::kBytes;
+  uint8_t* const ring_n = ring + (kAhead + 1) * kBytesM;
+  const uint32_t base_m = lds_address(ring), base_n = base_m + (kAhead + 1) * kBytesM;
   vec8<T> m[2][MT], n[2][NT];
   auto fetch = [&](int f, const uint8_t* slot_m, const uint8_t* slot_n, int k) {
     if (f < NT)
@@ -206,23 +220,16 @@ __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, 
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-#pragma unroll
-  for (int s = 0; s < kAhead; ++s) {
-#pragma unroll
-    for (int q = 0; q < M::kMine; ++q) copy_m(q, base_m + s * M::kBytes, s);
-#pragma unroll
-    for (int q = 0; q < N::kMine; ++q) copy_n(q, base_n + s * N::kBytes, s);
-  }
-  wait_copies<(kAhead - 1) * (M::kMine + N::kMine)>();
+  wait_copies<0>();  // and for the stores of a tile before, whose order among the copies is not known
   lds_barrier();
 #pragma unroll
   for (int f = 0; f < kFragments; ++f) fetch(f, ring, ring_n, 0);
   int at_m = 0, at_n = 0;  // the slots of stage s, in bytes
   for (int s = 0; s < stages; ++s) {
-    const int next_m = at_m == kAhead * M::kBytes ? 0 : at_m + M::kBytes;
+    const int next_m = at_m == kAhead * kBytesM ? 0 : at_m + kBytesM;
     const int next_n = at_n == (kAhead - 1) * N::kBytes ? 0 : at_n + N::kBytes;
     const uint8_t *slot_m = ring + at_m, *slot_n = ring_n + at_n;
-    const uint32_t free_m = base_m + (at_m == 0 ? kAhead * M::kBytes : at_m - M::kBytes);  // of stage s - 1
+    const uint32_t free_m = base_m + (at_m == 0 ? kAhead * kBytesM : at_m - kBytesM);  // of stage s - 1
     auto far = [&](int q) { copy_m(q, free_m, s + kAhead); };
     constexpr int kThird = (M::kMine + 2) / 3, kTwoThirds = 2 * M::kMine / 3 > kThird ? 2 * M::kMine / 3 : kThird;
     part(0, slot_m, slot_n, 1, 0, kThird, far);
@@ -240,11 +247,12 @@ __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, 
   lds_barrier();
 }
 
-// All stages of a tile of 32 rows by 32 NT columns that the eight waves share along r: of each stage of 128 steps
-// wave w multiplies 16. Few steps follow each other, so a tile of little work streams its operands with kAhead
-// stages on their way. Returns each wave's share of the sums. ring: kAhead slots.
-template <typename T, typename M, typename N, int kAhead, int NT, typename Copy>
-__device__ __forceinline__ void shared_loop(uint8_t* ring, int stages, int wave, int lane, floatx16 (&acc)[NT],
+// All stages of a tile of 32 MT rows by 32 NT columns that the eight waves share along r: of each stage of 128
+// steps wave w multiplies 16, so that a stage costs one barrier and one wait for LDS, where a wave's share of a
+// small tile would wait for LDS in every part. kAhead stages in LDS (copy makes both panels' copies of one).
+// acc: each wave's share of the sums.
+template <typename T, typename M, typename N, int kAhead, int MT, int NT, typename Copy>
+__device__ __forceinline__ void shared_loop(uint8_t* ring, int stages, int wave, int lane, floatx16 (&acc)[MT][NT],
                                             Copy copy) {
   constexpr int kBytes = M::kBytes + N::kBytes, kCopies = M::kMine + N::kMine;
   const uint32_t base = lds_address(ring);
@@ -254,11 +262,16 @@ __device__ __forceinline__ void shared_loop(uint8_t* ring, int stages, int wave,
   for (int s = 0; s < stages; ++s) {
     wait_copies<(kAhead - 2) * kCopies>();
     lds_barrier();  // stage s has landed, stage s - 1 has been read
-    copy(base + free, s + kAhead - 1);
-    const vec8<T> m = M::template fragment<T>(ring + slot, 0, wave, lane);
+    vec8<T> m[MT], n[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      acc[j] = mfma(N::template fragment<T>(ring + slot + M::kBytes, 32 * j, wave, lane), m, acc[j]);
+    for (int j = 0; j < NT; ++j) n[j] = N::template fragment<T>(ring + slot + M::kBytes, 32 * j, wave, lane);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) m[i] = M::template fragment<T>(ring + slot, 32 * i, wave, lane);
+    copy(base + free, s + kAhead - 1);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = mfma(n[j], m[i], acc[i][j]);
     free = slot;
     slot = slot == (kAhead - 1) * kBytes ? 0 : slot + kBytes;
   }
@@ -266,38 +279,86 @@ __device__ __forceinline__ void shared_loop(uint8_t* ring, int stages, int wave,
   lds_barrier();
 }
 
-// Sums leave through LDS, 32 rows of a wave's columns at a time, so that a store covers whole
-// lines; put(row, column, sums) stores those of the tile's row `row`, column `column` on: 16 bytes of O.
-template <typename O, int MT, int NT, typename Put>
-__device__ __forceinline__ void drain(uint8_t* ring, int m0, int n0, int wave, int lane, const floatx16 (&acc)[MT][NT],
-                                      Put put) {
-  constexpr int kPitch = 32 * NT * 4 + 16;  // 16 bytes between rows: rows begin on other banks
-  uint8_t* mine = ring + wave * 32 * kPitch;
-  constexpr int kEach = 16 / (int)sizeof(O);
-  constexpr int kLanes = 32 * NT / kEach;  // a row
-  constexpr int kRows = 64 / kLanes;
+// The waves' shares, added in wave order; put(row, column, sums) gets four columns. sums: 32 kWaves MT NT KB of LDS.
+template <int MT, int NT, typename Put>
+__device__ __forceinline__ void shared_drain(uint8_t* ring, int wave, int lane, const floatx16 (&acc)[MT][NT], Put put) {
+  constexpr int kRows = 32 * MT, kQuads = 8 * NT;
+  floatx4* sums = reinterpret_cast<floatx4*>(ring);  // [wave][row][quad], a quad's place swizzled by row
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<floatx4*>(mine + (lane & 31) * kPitch + (32 * j + 8 * g + 4 * (lane >> 5)) * 4) =
+      for (int g = 0; g < 4; ++g) {
+        const int row = 32 * i + (lane & 31), quad = 8 * j + 2 * g + (lane >> 5);
+        sums[(wave * kRows + row) * kQuads + (quad ^ (row & 7))] =
             floatx4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-#pragma unroll
-    for (int r = 0; r < 32 / kRows; ++r) {
-      const int row = r * kRows + lane / kLanes, column = kEach * (lane % kLanes);
-      const floatx4* at = reinterpret_cast<const floatx4*>(mine + row * kPitch + column * 4);
-      float v[kEach];
-#pragma unroll
-      for (int c = 0; c < kEach; c += 4) {
-        const floatx4 part = at[c / 4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[c + k] = part[k];
       }
-      put(m0 + 32 * i + row, n0 + column, v);
-    }
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < kRows * kQuads; i += kThreads) {
+    const int row = i / kQuads, quad = i % kQuads;
+    floatx4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) v += sums[(k * kRows + row) * kQuads + (quad ^ (row & 7))];
+    put(row, 4 * quad, v);
   }
+}
+
+// A wave's sums leave through kDrainBytes / kWaves of LDS of its own, so that a store covers whole lines (16 bytes a lane,
+// eight lanes a line; 32 bytes side by side straight from the registers took 1650 instead of 1577 us, streamed 1707):
+// put(row, column, line) gets 16 bytes of O, columns of one row. A lane holds four columns of a row and lane + 32 the
+// next four; 16-bit values of two such groups are exchanged between the two lanes, so that LDS is written by 16 bytes
+// too. The 16-byte chunk c of row i lies in place c ^ (i % 8).
+constexpr int kDrainBytes = kWaves * 32 * 128;
+template <typename O, int MT, int NT, typename Put>
+__device__ __forceinline__ void drain(uint8_t* scratch, int m0, int n0, int wave, int lane,
+                                      const floatx16 (&acc)[MT][NT], Put put) {
+  typedef O four __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  constexpr int kEach = 16 / (int)sizeof(O);
+  constexpr int kLine = 8 * kEach;                       // columns of a line
+  constexpr int kSide = kLine / 32 < NT ? kLine / 32 : NT;  // fragments side by side in a line (or as many as there are)
+  constexpr int kLanes = 32 * kSide / kEach;             // that store a row
+  uint8_t* const mine = scratch + wave * 32 * 128;
+  const int row = lane & 31, half = lane >> 5;
+  auto write = [&](int chunk, u32x4 v) {
+    *reinterpret_cast<u32x4*>(mine + row * 128 + ((chunk ^ (row & 7)) << 4)) = v;
+  };
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j0 = 0; j0 < NT; j0 += kSide) {
+#pragma unroll
+      for (int side = 0; side < kSide; ++side) {
+        const floatx16& sums = acc[i][j0 + side];
+        if constexpr (sizeof(O) == 4) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            write(2 * g + half, __builtin_bit_cast(u32x4, floatx4{sums[4 * g], sums[4 * g + 1], sums[4 * g + 2], sums[4 * g + 3]}));
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            four x, y;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = (O)sums[4 * g + k];
+              y[k] = (O)sums[4 * g + 4 + k];
+            }
+            const u32x2 a = __builtin_bit_cast(u32x2, x), b = __builtin_bit_cast(u32x2, y);
+            // lanes 32-63 of the first change places with lanes 0-31 of the second
+            const auto p = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+            const auto q = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+            write(4 * side + g + half, u32x4{p[0], q[0], p[1], q[1]});
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 32; r += 64 / kLanes) {
+        const int at = r + lane / kLanes, chunk = lane % kLanes;
+        put(m0 + 32 * i + at, n0 + 32 * j0 + kEach * chunk,
+            *reinterpret_cast<const u32x4*>(mine + at * 128 + ((chunk ^ (at & 7)) << 4)));
+      }
+    }
 }
 
 // 16 bytes of O, to and from an aligned place.
@@ -305,16 +366,24 @@ template <typename O>
 struct Line {
   static constexpr int kEach = 16 / (int)sizeof(O);
   typedef O vec __attribute__((ext_vector_type(kEach)));
-  static __device__ __forceinline__ void store(O* p, const float (&v)[kEach]) {
+  static __device__ __forceinline__ void store(O* p, u32x4 v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  }
+};
+
+// Four values to and from an aligned place.
+template <typename O>
+struct Four {
+  typedef O vec __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ void store(O* p, floatx4 v) {
     vec r;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) r[i] = (O)v[i];
-    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, r), reinterpret_cast<u32x4*>(p));
+    for (int i = 0; i < 4; ++i) r[i] = (O)v[i];
+    *reinterpret_cast<vec*>(p) = r;
   }
-  static __device__ __forceinline__ void add(const O* p, float (&v)[kEach]) {
+  static __device__ __forceinline__ floatx4 load(const O* p) {
     const vec r = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) v[i] += (float)r[i];
+    return floatx4{(float)r[0], (float)r[1], (float)r[2], (float)r[3]};
   }
 };
 

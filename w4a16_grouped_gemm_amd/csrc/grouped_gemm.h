@@ -33,8 +33,6 @@ struct GroupedParams {
   int32_t n_slots, capacity, block_m;
   int32_t transposed;
 };
-// Workgroups that a call launches at most, of 512 threads; a launch has less than 2^32 threads.
-int64_t grouped_workgroups(int32_t N, int32_t capacity, int32_t block_m);
 hipError_t launch_grouped_gemm(const GroupedParams& p, int32_t dtype, int32_t out_dtype, hipStream_t stream);
 
 // How the weights' gradient is cut, a rule on sizes alone: tiles of tile x tile values, and how many workgroups share an
@@ -59,7 +57,8 @@ struct WgradParams {
   WgradCut cut;
 };
 WgradCut wgrad_cut(int32_t E, int32_t N, int32_t K, int32_t capacity);
-int64_t wgrad_workgroups(int32_t E, int32_t N, int32_t K, int32_t splits);
+// Workgroups of 512 threads that the call launches; a launch has less than 2^32 threads.
+int64_t wgrad_workgroups(int32_t E, int32_t N, int32_t K, WgradCut cut);
 hipError_t launch_grouped_wgrad(const WgradParams& p, int32_t dtype, int32_t dw_dtype, hipStream_t stream);
 
 }  // namespace w4a16

@@ -157,21 +157,19 @@ __device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, i
   N n;
   set_weights<T, TRANSPOSED>(n, p, e, n0, wave, lane);
   const int at_m = wave / 4 * 32 * MT, at_n = wave % 4 * 32 * NT;
-  loop<T, M, N, W::kAhead>(
-      ring, (p.K + kStep - 1) / kStep, at_m, at_n, lane, acc,
-      [&](int q, uint32_t slot, int stage) { m.copy(q, slot, p.K - stage * kStep, wave); },
-      [&](int q, uint32_t slot, int stage) { n.copy(q, slot, p.K - stage * kStep, wave); }, [] {});
+  auto copy_m = [&](int q, uint32_t slot, int stage) { m.copy(q, slot, p.K - stage * kStep, wave); };
+  auto copy_n = [&](int q, uint32_t slot, int stage) { n.copy(q, slot, p.K - stage * kStep, wave); };
+  prologue<M, N, W::kAhead, M::kBytes>(ring, copy_m, copy_n);
+  loop<T, M, N, W::kAhead, M::kBytes>(ring, (p.K + kStep - 1) / kStep, at_m, at_n, lane, acc, copy_m, copy_n, [] {});
   uint32_t slotted[MT];  // which of 32 rows have a slot
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int row = at_m + 32 * i + (lane & 31);
     slotted[i] = (uint32_t)__ballot(row < rows && (uint32_t)p.sorted[first + min(row, rows - 1)] < (uint32_t)p.n_slots);
   }
-  drain<O>(ring, at_m, at_n, wave, lane, acc, [&](int row, int column, float (&v)[Line<O>::kEach]) {
+  drain<O>(ring, at_m, at_n, wave, lane, acc, [&](int row, int column, u32x4 v) {
     if (row >= rows || n0 + column >= p.N) return;
-    const bool real = slotted[(row - at_m) / 32] >> (row & 31) & 1;
-#pragma unroll
-    for (int i = 0; i < Line<O>::kEach; ++i) v[i] = real ? v[i] : 0.f;
+    if (!(slotted[(row - at_m) / 32] >> (row & 31) & 1)) v = u32x4{0, 0, 0, 0};
     Line<O>::store(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + n0 + column, v);
   });
 }
@@ -196,7 +194,7 @@ __global__ __launch_bounds__(kThreads, W::kRing > 80 * 1024 ? 2 : 4) void groupe
     const int rows = min(tile.blocks * p.block_m, kRows), n0 = nt * kTileN;
     if ((uint32_t)e >= (uint32_t)p.E) {  // no such expert
       constexpr int kEach = Line<O>::kEach, kLanes = kTileN / kEach;
-      const float zero[kEach] = {};
+      const u32x4 zero = {0, 0, 0, 0};
       for (int i = (int)threadIdx.x; i < rows * kLanes; i += kThreads) {
         const int row = i / kLanes, column = n0 + kEach * (i % kLanes);
         if (column < p.N) Line<O>::store(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + column, zero);
@@ -232,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, int n
     const int e = tile.expert;
     const int first = tile.block * p.block_m + (int)(target & ((1 << log_cut) - 1)) * kRows;
     const int rows = min(tile.blocks * p.block_m, kRows), n0 = nt * kTileN;
-    floatx16 acc[NT] = {};
+    floatx16 acc[1][NT] = {};
     const bool known = (uint32_t)e < (uint32_t)p.E;
     if (known) {
       M m;
@@ -247,31 +245,12 @@ __global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, int n
         for (int i = 0; i < N::kMine; ++i) n.copy(i, slot + M::kBytes, left, wave);
       });
     }
-    // the waves' shares, added in wave order; a thread's four columns
-    floatx4* sums = reinterpret_cast<floatx4*>(ring);  // [wave][32 rows][8 NT]
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int row = lane & 31, c = 8 * j + 2 * g + (lane >> 5);
-        sums[(wave * 32 + row) * (8 * NT) + (c ^ (row & 7))] =
-            floatx4{acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
-      }
-    __syncthreads();
-    for (int i = (int)threadIdx.x; i < 32 * 8 * NT; i += kThreads) {
-      const int row = i / (8 * NT), c = i % (8 * NT);
-      floatx4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) v += sums[(k * 32 + row) * (8 * NT) + (c ^ (row & 7))];
-      if (row < rows && n0 + 4 * c < p.N) {
-        const bool real = known && (uint32_t)p.sorted[first + row] < (uint32_t)p.n_slots;
-        typedef O vec __attribute__((ext_vector_type(4)));
-        vec out;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = (O)(real ? v[k] : 0.f);
-        *reinterpret_cast<vec*>(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + n0 + 4 * c) = out;
-      }
-    }
+    shared_drain(ring, wave, lane, acc, [&](int row, int column, floatx4 v) {
+      if (row >= rows || n0 + column >= p.N) return;
+      const bool real = known && (uint32_t)p.sorted[first + row] < (uint32_t)p.n_slots;
+      const floatx4 none = {0.f, 0.f, 0.f, 0.f};
+      Four<O>::store(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + n0 + column, real ? v : none);
+    });
     if (target + row_tiles >= tile.total << log_cut) return;
     __syncthreads();
   }
@@ -290,6 +269,8 @@ Cut cut(const GroupedParams& p, int rows, int columns) {
   c.row_tiles = (std::min(blocks, blocks / per + p.E) * pieces + kTileGroup - 1) / kTileGroup * kTileGroup;
   c.log_per = __builtin_ctz((unsigned)per);
   c.log_cut = __builtin_ctz((unsigned)pieces);
+  // a launch has less than 2^32 threads; a workgroup goes on with every row_tiles-th row tile
+  c.row_tiles = std::min(c.row_tiles, std::max(1, (1 << 20) / c.ntiles) * kTileGroup);
   const int64_t tiles = (int64_t)c.row_tiles * c.ntiles;
   c.grid = dim3((unsigned)((tiles + kXcds * kChunk - 1) / (kXcds * kChunk) * (kXcds * kChunk)));
   return c;
@@ -342,10 +323,6 @@ hipError_t launch(const GroupedParams& p, hipStream_t stream) {
 }
 
 }  // namespace
-
-int64_t grouped_workgroups(int32_t N, int32_t capacity, int32_t block_m) {
-  return ((int64_t)(capacity / block_m) + kTileGroup - 1) * ((N + 127) / 128) + kXcds * kChunk;
-}
 
 hipError_t launch_grouped_gemm(const GroupedParams& p, int32_t dtype, int32_t out_dtype, hipStream_t stream) {
   if (p.capacity < p.block_m) return hipSuccess;  // no whole block

@@ -12,7 +12,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <cstdlib>
 
 namespace w4a16 {
 namespace {
@@ -39,43 +38,116 @@ __device__ __forceinline__ bool tile_of(int mtiles, int ntiles, int& e, int& mt,
   return true;
 }
 
-// kTile x kTile values a workgroup, its waves 2 deep and 4 wide.
-template <typename T, typename O, int kTile, bool GATHER>
-__global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(WgradParams p, int mtiles, int ntiles) {
-  constexpr int MT = kTile / 64, NT = kTile / 128;
-  typedef ColumnPanel<kTile> Panel;
-  constexpr int kRows = 64 / Panel::kLanes;  // of a copy
-  constexpr int kMine = Panel::kMine;
-  static_assert(kMine * kRows == 8, "eight rows a wave");
-  __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes<Panel, Panel, 2>];
-  int* const run = reinterpret_cast<int*>(ring);
-  const int lane = (int)threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  int e, mt, nt;
-  if (!tile_of(mtiles, ntiles, e, mt, nt)) return;
-
-  // the expert's first and last block
+// The rows [begin, stop) of expert e that this workgroup (of blockIdx.y's share) goes through: from the expert's first
+// block to its last. scratch: two ints of LDS. All threads of the workgroup call it.
+struct Span {
+  int begin, stop;
+};
+__device__ __forceinline__ Span span_of(const WgradParams& p, int e, int* scratch) {
   const int used = p.capacity > 0 ? min(p.capacity, *p.ntpp) >> p.log_block : 0;
-  if (threadIdx.x == 0) run[0] = INT_MAX, run[1] = -1;
+  if (threadIdx.x == 0) scratch[0] = INT_MAX, scratch[1] = -1;
   __syncthreads();
   int lo = INT_MAX, hi = -1;
   for (int i = (int)threadIdx.x; i < used; i += kThreads)
     if (p.expert_ids[i] == e) lo = min(lo, i), hi = i;
   if (hi >= 0) {
-    atomicMin(&run[0], lo);
-    atomicMax(&run[1], hi);
+    atomicMin(&scratch[0], lo);
+    atomicMax(&scratch[1], hi);
   }
   __syncthreads();
-  const int last = __builtin_amdgcn_readfirstlane(run[1]);
-  const int begun = __builtin_amdgcn_readfirstlane(run[0]);
+  const int first = __builtin_amdgcn_readfirstlane(scratch[0]), last = __builtin_amdgcn_readfirstlane(scratch[1]);
   __syncthreads();  // the ring's copies go where the run is
-  const int first = last < 0 ? 0 : begun << p.log_block;
-  const int end = last < 0 ? 0 : (last + 1) << p.log_block;
-  const int share = (((end - first + kStep - 1) / kStep + p.cut.splits - 1) / p.cut.splits) * kStep;
-  const int begin = min((int64_t)first + (int64_t)share * blockIdx.y, (int64_t)end);
-  const int stop = min((int64_t)begin + share, (int64_t)end);
-  const int stages = (stop - begin + kStep - 1) / kStep;
+  if (last < 0) return {0, 0};
+  const int rows = (last + 1 - first) << p.log_block, begin = first << p.log_block;
+  const int share = ((rows + kStep - 1) / kStep + p.cut.splits - 1) / p.cut.splits * kStep;
+  const int at = (int)min((int64_t)share * blockIdx.y, (int64_t)rows);
+  return {begin + at, begin + min(at + share, rows)};
+}
 
+// Four sums of dW (one workgroup's share of them) to where they go.
+template <typename O>
+__device__ __forceinline__ void put4(const WgradParams& p, int e, int n, int k, floatx4 v) {
+  if (n >= p.N || k >= p.K) return;
+  const int64_t at = ((int64_t)e * p.N + n) * p.K + k;
+  if (p.cut.splits > 1) {
+    Four<float>::store(p.partial + (int64_t)blockIdx.y * p.E * p.N * p.K + at, v);
+    return;
+  }
+  O* dw = static_cast<O*>(p.dw) + at;
+  if (p.accumulate) v += Four<O>::load(dw);
+  Four<O>::store(dw, v);
+}
+
+// Few weights: 64 x 64 values a workgroup, shared by its waves along the rows, 128 of them a stage.
+template <typename T, typename O>
+__global__ __launch_bounds__(kThreads) void narrow_wgrad_kernel(WgradParams p, int mtiles, int ntiles) {
+  constexpr int kTile = 64, kSteps = 128, kAhead = 4, kTable = 4096;
+  typedef ColumnPanel<kTile, kSteps> Panel;
+  static_assert(Panel::kMine == 2, "two copies of eight rows a wave and panel");
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kAhead * 2 * Panel::kBytes];
+  __shared__ int32_t table[kTable];  // of kTable rows: the row of a, or -1 where the row adds nothing
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  int e, mt, nt;
+  if (!tile_of(mtiles, ntiles, e, mt, nt)) return;
+  const Span span = span_of(p, e, table);
+  const int m0 = mt * kTile, n0 = nt * kTile;
+  floatx16 acc[2][2] = {};
+  const int my_row = lane / Panel::kLanes;
+  const int64_t row_m = (int64_t)p.N * (int)sizeof(T), row_n = (int64_t)p.K * (int)sizeof(T);
+  for (int base = span.begin; base < span.stop; base += kTable) {
+    const int rows = min(span.stop - base, kTable), stages = (rows + kSteps - 1) / kSteps;
+    // the copies go up to kAhead - 1 stages past the last
+    const int filled = min((stages + kAhead) * kSteps, kTable);
+    for (int i = (int)threadIdx.x; i < filled; i += kThreads) {
+      const int row = base + min(i, rows - 1);
+      const uint32_t slot = (uint32_t)p.sorted[row];
+      const bool real = i < rows && slot < (uint32_t)p.n_slots && p.expert_ids[row >> p.log_block] == e;
+      table[i] = !real ? -1 : p.gather ? (int32_t)p.by_topk.of(slot) : row;
+    }
+    __syncthreads();
+    const uint8_t *at_m[2], *at_n[2];  // this lane's 16 bytes of the chunk's first row of dout, of row 0 of a
+    int32_t from[2];                   // its rows of a, of the stage to be copied next
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int row = 16 * wave + 8 * q + my_row;
+      const int column = 8 * (lane % Panel::kLanes ^ (Panel::swizzle(row) << 2));
+      at_m[q] = static_cast<const uint8_t*>(p.dout) + (int64_t)(base + row) * row_m + 2 * (m0 + (column < p.N - m0 ? column : 0));
+      at_n[q] = static_cast<const uint8_t*>(p.a) + 2 * (n0 + (column < p.K - n0 ? column : 0));
+      from[q] = table[row];
+    }
+    shared_loop<T, Panel, Panel, kAhead>(ring, stages, wave, lane, acc, [&](uint32_t lds, int stage) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bool real = from[q] >= 0;
+        const uint8_t* n = at_n[q] + (uint64_t)(uint32_t)from[q] * (uint32_t)row_n;
+        copy16(real ? (const void*)at_m[q] : (const void*)kZeros, lds + 1024 * (2 * wave + q));
+        copy16(real ? (const void*)n : (const void*)kZeros, lds + Panel::kBytes + 1024 * (2 * wave + q));
+        at_m[q] += kSteps * row_m;
+        const int next = (stage + 1) * kSteps + 16 * wave + 8 * q + my_row;
+        from[q] = next < filled ? table[next] : -1;
+      }
+    });
+  }
+  shared_drain(ring, wave, lane, acc, [&](int n, int k, floatx4 v) { put4<O>(p, e, m0 + n, n0 + k, v); });
+}
+
+// Many weights: kTile x kTile values a workgroup, its waves 2 deep and 4 wide.
+template <typename T, typename O, int kTile, bool GATHER>
+__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p, int mtiles, int ntiles) {
+  constexpr int MT = kTile / 64, NT = kTile / 128;
+  constexpr int kAhead = kTile == 256 ? 2 : 4;
+  typedef ColumnPanel<kTile> Panel;
+  constexpr int kRows = 64 / Panel::kLanes;  // of a copy
+  constexpr int kMine = Panel::kMine;
+  static_assert(kMine * kRows == 8, "eight rows a wave");
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes<Panel, Panel, kAhead>];
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  int e, mt, nt;
+  if (!tile_of(mtiles, ntiles, e, mt, nt)) return;
+  const Span span = span_of(p, e, reinterpret_cast<int*>(ring));
+  const int begin = span.begin, stop = span.stop, stages = (stop - begin + kStep - 1) / kStep;
   const int m0 = mt * kTile, n0 = nt * kTile;
   floatx16 acc[MT][NT] = {};
   if (stages > 0) {
@@ -110,27 +182,28 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
       copy16(real ? (const void*)at : (const void*)kZeros, lds + 1024 * (kMine * wave + q));
     };
     auto slot_of = [&](const Rows& r, int q) {  // of this lane's row
-      int32_t slot = r.slot[kRows * q];
-#pragma unroll
-      for (int i = 1; i < kRows; ++i) slot = my_row == i ? r.slot[kRows * q + i] : slot;
-      return (uint32_t)slot;
+      const int32_t* of = &r.slot[kRows * q];
+      if constexpr (kRows == 2) return (uint32_t)(my_row ? of[1] : of[0]);
+      // by the bits of my_row: a chain over its values becomes an array in memory
+      const int32_t low = my_row & 1 ? of[1] : of[0], high = my_row & 1 ? of[3] : of[2];
+      return (uint32_t)(my_row & 2 ? high : low);
     };
     look(of_m, 0);
     look(of_n, 0);
-    loop<T, Panel, Panel, 2>(
-        ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc,
-        [&](int q, uint32_t lds, int stage) {
-          copy(of_m, at_m[q], slot_of(of_m, q), q, lds);
-          at_m[q] += kStep * row_m;
-          if (q == kMine - 1) look(of_m, stage + 1);
-        },
-        [&](int q, uint32_t lds, int stage) {
-          const uint32_t slot = slot_of(of_n, q);
-          copy(of_n, GATHER ? at_n[q] + (uint64_t)p.by_topk.of(slot) * (uint32_t)row_n : at_n[q], slot, q, lds);
-          if (!GATHER) at_n[q] += kStep * row_n;
-          if (q == kMine - 1) look(of_n, stage + 1);
-        },
-        [&] {
+    auto copy_m = [&](int q, uint32_t lds, int stage) {
+      copy(of_m, at_m[q], slot_of(of_m, q), q, lds);
+      at_m[q] += kStep * row_m;
+      if (q == kMine - 1) look(of_m, stage + 1);
+    };
+    auto copy_n = [&](int q, uint32_t lds, int stage) {
+      const uint32_t slot = slot_of(of_n, q);
+      copy(of_n, GATHER ? at_n[q] + (uint64_t)p.by_topk.of(slot) * (uint32_t)row_n : at_n[q], slot, q, lds);
+      if (!GATHER) at_n[q] += kStep * row_n;
+      if (q == kMine - 1) look(of_n, stage + 1);
+    };
+    prologue<Panel, Panel, kAhead, Panel::kBytes>(ring, copy_m, copy_n);
+    loop<T, Panel, Panel, kAhead, Panel::kBytes>(
+        ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc, copy_m, copy_n, [&] {
           asm volatile(""
                        : "+s"(of_m.slot[0]), "+s"(of_m.slot[1]), "+s"(of_m.slot[2]), "+s"(of_m.slot[3]),
                          "+s"(of_m.slot[4]), "+s"(of_m.slot[5]), "+s"(of_m.slot[6]), "+s"(of_m.slot[7]), "+s"(of_m.owner));
@@ -140,39 +213,33 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 2 : 4) void wgrad_kernel(W
         });
   }
 
-  const int64_t size = (int64_t)p.E * p.N * p.K;
-  if (p.cut.splits > 1) {
-    float* partial = p.partial + (int64_t)blockIdx.y * size;
-    drain<float>(ring, wave / 4 * 32 * MT, wave % 4 * 32 * NT, wave, lane, acc, [&](int n, int k, float (&v)[4]) {
-      if (m0 + n < p.N && n0 + k < p.K) Line<float>::store(partial + ((int64_t)e * p.N + m0 + n) * p.K + n0 + k, v);
+  const int at_m = wave / 4 * 32 * MT, at_n = wave % 4 * 32 * NT;
+  if (p.cut.splits > 1 || (p.accumulate && sizeof(O) == 2)) {  // 32-bit sums to a share, or to be added to what is there
+    drain<float>(ring, at_m, at_n, wave, lane, acc, [&](int n, int k, u32x4 v) {
+      put4<O>(p, e, m0 + n, n0 + k, __builtin_bit_cast(floatx4, v));
     });
-  } else {
-    drain<O>(ring, wave / 4 * 32 * MT, wave % 4 * 32 * NT, wave, lane, acc, [&](int n, int k, float (&v)[Line<O>::kEach]) {
-      if (m0 + n >= p.N || n0 + k >= p.K) return;
-      O* dw = static_cast<O*>(p.dw) + ((int64_t)e * p.N + m0 + n) * p.K + n0 + k;
-      if (p.accumulate) Line<O>::add(dw, v);
-      Line<O>::store(dw, v);
-    });
+    return;
   }
+  drain<O>(ring, at_m, at_n, wave, lane, acc, [&](int n, int k, u32x4 v) {
+    if (m0 + n >= p.N || n0 + k >= p.K) return;
+    O* dw = static_cast<O*>(p.dw) + ((int64_t)e * p.N + m0 + n) * p.K + n0 + k;
+    if constexpr (sizeof(O) == 4) {
+      if (p.accumulate) v = __builtin_bit_cast(u32x4, __builtin_bit_cast(floatx4, v) + *reinterpret_cast<const floatx4*>(dw));
+    }
+    Line<O>::store(dw, v);
+  });
 }
 
 // dW (+)= the shares, in their order.
 template <typename O>
 __global__ __launch_bounds__(256) void join_kernel(const float* partial, O* dw, int64_t size, int32_t splits,
                                                    int32_t accumulate) {
-  constexpr int kEach = Line<O>::kEach;
-  const int64_t stride = (int64_t)gridDim.x * 256 * kEach;
-  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kEach; at < size; at += stride) {
-    float sums[kEach] = {};
-    for (int s = 0; s < splits; ++s)
-#pragma unroll
-      for (int i = 0; i < kEach; i += 4) {
-        const floatx4 part = *reinterpret_cast<const floatx4*>(partial + s * size + at + i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sums[i + k] += part[k];
-      }
-    if (accumulate) Line<O>::add(dw + at, sums);
-    Line<O>::store(dw + at, sums);
+  const int64_t stride = (int64_t)gridDim.x * 256 * 4;
+  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < size; at += stride) {
+    floatx4 sums = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s) sums += Four<float>::load(partial + s * size + at);
+    if (accumulate) sums += Four<O>::load(dw + at);
+    Four<O>::store(dw + at, sums);
   }
 }
 
@@ -182,7 +249,9 @@ hipError_t launch_tile(const WgradParams& p, hipStream_t stream) {
   const int64_t chunk = ((int64_t)mtiles * ntiles + kXcds - 1) / kXcds;
   const int64_t grid = chunk * kXcds * p.E;
   const dim3 g((unsigned)grid, (unsigned)p.cut.splits), t(kThreads);
-  if (p.gather)
+  if constexpr (kTile == 64)
+    hipLaunchKernelGGL((narrow_wgrad_kernel<T, O>), g, t, 0, stream, p, mtiles, ntiles);
+  else if (p.gather)
     hipLaunchKernelGGL((wgrad_kernel<T, O, kTile, true>), g, t, 0, stream, p, mtiles, ntiles);
   else
     hipLaunchKernelGGL((wgrad_kernel<T, O, kTile, false>), g, t, 0, stream, p, mtiles, ntiles);
@@ -191,10 +260,12 @@ hipError_t launch_tile(const WgradParams& p, hipStream_t stream) {
 
 template <typename T, typename O>
 hipError_t launch(const WgradParams& p, hipStream_t stream) {
-  const hipError_t err = p.cut.tile == 256 ? launch_tile<T, O, 256>(p, stream) : launch_tile<T, O, 128>(p, stream);
+  const hipError_t err = p.cut.tile == 256   ? launch_tile<T, O, 256>(p, stream)
+                         : p.cut.tile == 128 ? launch_tile<T, O, 128>(p, stream)
+                                             : launch_tile<T, O, 64>(p, stream);
   if (err != hipSuccess || p.cut.splits == 1) return err;
   const int64_t size = (int64_t)p.E * p.N * p.K;
-  const int64_t grid = std::min<int64_t>((size / Line<O>::kEach + 255) / 256, (int64_t)device_cu_count() * 32);
+  const int64_t grid = std::min<int64_t>((size / 4 + 255) / 256, (int64_t)device_cu_count() * 32);
   hipLaunchKernelGGL((join_kernel<O>), dim3((unsigned)grid), dim3(256), 0, stream, p.partial, static_cast<O*>(p.dw),
                      size, p.cut.splits, p.accumulate);
   return hipGetLastError();
@@ -202,18 +273,21 @@ hipError_t launch(const WgradParams& p, hipStream_t stream) {
 
 }  // namespace
 
-int64_t wgrad_workgroups(int32_t E, int32_t N, int32_t K, int32_t splits) {
-  const int64_t tiles = (int64_t)((N + 127) / 128) * ((K + 127) / 128);
-  return (tiles + kXcds - 1) / kXcds * kXcds * E * splits;
+int64_t wgrad_workgroups(int32_t E, int32_t N, int32_t K, WgradCut cut) {
+  const int64_t tiles = (int64_t)((N + cut.tile - 1) / cut.tile) * ((K + cut.tile - 1) / cut.tile);
+  return (tiles + kXcds - 1) / kXcds * kXcds * E * cut.splits;
 }
 
+// Measured, us by (256 x 256, 128 x 128, 64 x 64) tiles with the best number of shares, bf16, K last: 8 experts of 250 rows,
+// 1000 x 2000: 25, 36, 105; 8 of 4096, 512 x 512: 60 (4 shares), 45 (2), 59; 4 of 1388, 264 x 712: 25 (4), 22 (2), 17;
+// one of 4096, 512 x 1024: 31 (8), 26 (4), 21 (2), without shares 99, 57, 24; one of 4096, 256 x 256: 30 (8), 22 (8),
+// 15 (8), without 96, 52, 21; 64 of 64, 1024 x 1024: 43, 83, 350.
 WgradCut wgrad_cut(int32_t E, int32_t N, int32_t K, int32_t capacity) {
-  const char* v = getenv("WG");
   auto tiles = [&](int64_t t) { return E * ((N + t - 1) / t) * ((K + t - 1) / t); };
-  const int64_t rows = capacity / E;
   WgradCut c;
-  c.tile = v ? atoi(v) / 100 : tiles(256) >= 256 ? 256 : 128;
-  c.splits = v ? atoi(v) % 100 : (int32_t)std::max<int64_t>(1, std::min<int64_t>({(c.tile == 256 ? 256 : 512) / tiles(c.tile), rows / 256, 16}));
+  c.tile = tiles(256) >= 128 ? 256 : tiles(64) <= 256 ? 64 : 128;
+  // shares fill the card where tiles do not; each is of 512 rows at least
+  c.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({256 / tiles(c.tile), capacity / E / 512, 16}));
   return c;
 }
 
