@@ -115,7 +115,7 @@ struct Way {
   static constexpr int MT = MT_, NT = NT_, kAhead = kAhead_;
   static constexpr int kRows = 64 * MT, kTileN = 128 * NT;
   static constexpr int kRing = kRingBytes<RowPanel<kRows>, RowPanel<kTileN>, kAhead>;
-  typedef Way<(MT + 1) / 2, NT, kAhead> Half;
+  typedef Way<(MT + 1) / 2, NT, kAhead + (MT > 1)> Half;  // half the rows leave room for a stage more
 };
 
 // Where the wave's copies of rows come from: row i of the tile, or row 0 where it has no slot (zeroed at the store).
