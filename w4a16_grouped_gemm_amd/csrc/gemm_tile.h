@@ -94,10 +94,15 @@ struct RowPanel {
     first[i] = 8 * (lane % kLanes ^ swizzle(row_of(i, wave, lane)));
     at[i] = static_cast<const uint8_t*>(row) + 2 * first[i];
   }
-  // copy i of the next stage, of which `left` steps are in the operand
-  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave) {
+  // from the first stage to stage s
+  __device__ __forceinline__ void skip(int s) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) at[i] += (int64_t)s * kPitch;
+  }
+  // copy i of the next stage, of which `left` steps are in the operand; the copy after it is `on` stages on
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int on, int wave) {
     copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
-    at[i] += kPitch;
+    at[i] += (int64_t)on * kPitch;
   }
   // steps 16 k + 8 (lane / 32) + 0..7 of row outer0 + lane % 32; outer0 a multiple of 32
   template <typename T>
@@ -138,9 +143,13 @@ struct ColumnPanel {
       at[i] = reinterpret_cast<const uint8_t*>(base + first[i] * ld + (column < columns ? column : 0));
     }
   }
-  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave) {
+  __device__ __forceinline__ void skip(int s) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) at[i] += s * stride;
+  }
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int on, int wave) {
     copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
-    at[i] += stride;
+    at[i] += on * stride;
   }
   // As RowPanel's, by two transposing reads: sixteen lanes read four steps of sixteen columns,
   // lane i the columns 4 (i % 4) + 0..3 of step i / 4, and get column i's four steps.
