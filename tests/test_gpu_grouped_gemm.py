@@ -200,6 +200,30 @@ def test_blocks_in_any_order_and_of_no_expert(bm):
     assert torch.equal(dw.cpu().double(), ref)
 
 
+@pytest.mark.parametrize("bm", [16, 64])
+@pytest.mark.parametrize("shape", [(4096, 2, 2, 1024, 72), (2048, 2, 4, 384, 136), (256, 2, 8, 1024, 1024),
+                                   (500, 2, 4, 512, 768)], ids=str)
+def test_many_blocks_in_any_order(shape, bm):
+    """The same with more runs of blocks than experts, so that workgroups take tile after tile, at each tile's size."""
+    T, topk, E, N, K = shape
+    g = torch.Generator().manual_seed(22)
+    r = Routing(T, topk, E, E, bm, seed=23)
+    blocks = r.rows // bm
+    ids = r.expert_ids[:blocks].cpu()[torch.randperm(blocks, generator=g)]
+    ids[blocks // 2], ids[blocks // 3] = -1, E
+    r.expert_ids[:blocks] = ids.cuda()
+    r.expert = ids[r.live // bm].long()
+    a, weights, dout = whole(g, T, K), whole(g, E, N, K), whole(g, r.capacity, N)
+    a16, w16, d16 = a.bfloat16().cuda(), weights.bfloat16().cuda(), dout.bfloat16().cuda()
+    out = run(r, a16, w16, torch.float32, True, False).cpu()
+    assert torch.equal(out[: r.rows].double(), product(r, a, weights, True, False)[0])
+    assert bool((out[r.rows :] == POISON).all())
+    out = run(r, d16, w16, torch.float32, False, True).cpu()
+    assert torch.equal(out[: r.rows].double(), product(r, dout, weights, False, True)[0])
+    dw = run_wgrad(r, d16, a16, E, torch.float32, True)
+    assert torch.equal(dw.cpu().double(), weight_gradient(r, dout, a, E, True)[0])
+
+
 @pytest.mark.parametrize("T", [0, 4])
 def test_no_rows(T):
     """No tokens, and tokens without a resident expert: zeros, or what was there with accumulate; no row written."""
