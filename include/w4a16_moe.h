@@ -599,7 +599,8 @@ int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q
  *   T, topk            tokens and slots per token of the alignment
  *   sorted_token_ids, capacity, expert_ids, num_tokens_post_padded, block_m
  *                      moe_align's outputs and block size; rows of a block that does not
- *                      lie below capacity as a whole are not touched
+ *                      lie below capacity as a whole are not touched. capacity / block_m
+ *                      at most 2^17 (else W4A16_ERR_UNSUPPORTED): larger blocks for more rows
  *   w                  device [E, N, K], or [E, K, N] with transposed, of `dtype`: the
  *                      weights as they are trained, no repacking
  *   out                device [capacity, N] of out_dtype (`dtype` or fp32)

@@ -224,6 +224,31 @@ def test_many_blocks_in_any_order(shape, bm):
     assert torch.equal(dw.cpu().double(), weight_gradient(r, dout, a, E, True)[0])
 
 
+@pytest.mark.parametrize("blocks", [64, 65, 512, 513, 1025, 8192, 8193, 20000])
+@pytest.mark.parametrize("N", [8, 136])
+def test_many_blocks(N, blocks):
+    """Blocks of 16 rows on both sides of what is searched at once, runs of all lengths, experts without a block."""
+    E, K, bm = 40, 16, 16
+    g = torch.Generator().manual_seed(24)
+    r = Routing(blocks * bm, 1, E, E, bm, seed=25)
+    r.expert_ids[:blocks] = torch.randint(1, E - 1, (blocks,), generator=g).sort()[0].int().cuda()
+    slots = torch.randperm(blocks * bm, generator=g)
+    slots[torch.rand(blocks * bm, generator=g) < 0.1] = r.n  # padding anywhere
+    r.sorted[: blocks * bm] = slots.int().cuda()
+    r.ntpp.fill_(blocks * bm)
+    r.rows = blocks * bm
+    r.live = torch.nonzero(slots < r.n).flatten()
+    r.token = slots[r.live]
+    r.expert = r.expert_ids.cpu()[r.live // bm].long()
+    a, weights = whole(g, r.T, K), whole(g, E, N, K)
+    out = run(r, a.bfloat16().cuda(), weights.bfloat16().cuda(), torch.float32, True, False).cpu()
+    assert torch.equal(out[: r.rows].double(), product(r, a, weights, True, False)[0])
+    assert bool((out[r.rows :] == POISON).all())
+    dout = whole(g, r.capacity, N)
+    dw = run_wgrad(r, dout.bfloat16().cuda(), a.bfloat16().cuda(), E, torch.float32, True)
+    assert torch.equal(dw.cpu().double(), weight_gradient(r, dout, a, E, True)[0])
+
+
 @pytest.mark.parametrize("T", [0, 4])
 def test_no_rows(T):
     """No tokens, and tokens without a resident expert: zeros, or what was there with accumulate; no row written."""

@@ -44,7 +44,7 @@ SHARED = [
     (dict(topk=33), UNSUPPORTED), (dict(bm=48), UNSUPPORTED), (dict(bm=0), UNSUPPORTED), (dict(bm=256), UNSUPPORTED),
     (dict(T=1 << 29), UNSUPPORTED), (dict(cap=-1), INVALID), (dict(a_rows=63), INVALID), (dict(gather=1, a_rows=3), INVALID),
     (dict(a=None), INVALID), (dict(srt=None), INVALID), (dict(eid=None), INVALID), (dict(ntpp=None), INVALID),
-    (dict(a=ODD), INVALID),
+    (dict(a=ODD), INVALID), (dict(cap=(1 << 21) + 16, a_rows=1 << 22), UNSUPPORTED),
 ]
 
 

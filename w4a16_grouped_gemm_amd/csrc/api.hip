@@ -867,6 +867,9 @@ namespace {
 
 constexpr int64_t kMaxWorkgroups = 1 << 23;  // of 512 threads: a launch has less than 2^32 threads
 
+// Every workgroup of the products goes through the blocks' experts to find its rows, 8192 of them at a time.
+constexpr int32_t kMaxBlocks = 1 << 17;
+
 int check_products(int32_t E, int32_t N, int32_t K, int32_t dtype, int32_t out_dtype) {
   if (E < 1 || N < 1 || K < 1 || !dtype_ok(dtype) || !dtype_ok(out_dtype)) return W4A16_ERR_INVALID_ARG;
   if (E > W4A16_MAX_EXPERTS || N % 8 != 0 || K % 8 != 0 || N > kMaxRow || K > kMaxRow) return W4A16_ERR_UNSUPPORTED;
@@ -893,6 +896,7 @@ int moe_grouped_gemm(int32_t num_experts, int32_t N, int32_t K, const void* a, i
   st = check_tokens(T, topk, num_experts, block_m);
   if (st != W4A16_OK) return st;
   if (capacity < 0 || a_rows < (gather ? T : capacity)) return W4A16_ERR_INVALID_ARG;
+  if (capacity / block_m > kMaxBlocks) return W4A16_ERR_UNSUPPORTED;
   if (T == 0 || capacity == 0) return W4A16_OK;  // no slot, no row
   if (!a || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !w || !out) return W4A16_ERR_INVALID_ARG;
   if (!all_aligned16(a, w, out)) return W4A16_ERR_INVALID_ARG;
@@ -931,6 +935,7 @@ int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void
   st = check_tokens(T, topk, num_experts, block_m);
   if (st != W4A16_OK) return st;
   if (capacity < 0 || a_rows < (gather ? T : capacity) || !dw) return W4A16_ERR_INVALID_ARG;
+  if (capacity / block_m > kMaxBlocks) return W4A16_ERR_UNSUPPORTED;
   if (T > 0 && capacity > 0 && (!dout || !a || !sorted_token_ids || !expert_ids || !num_tokens_post_padded))
     return W4A16_ERR_INVALID_ARG;
   if (!all_aligned16(dout, a, dw, workspace)) return W4A16_ERR_INVALID_ARG;

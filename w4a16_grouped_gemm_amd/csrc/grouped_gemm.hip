@@ -40,7 +40,7 @@ __device__ __forceinline__ void tile_of(int ntiles, int64_t& row_tile, int& colu
 // block, of which those inside a tile end at once, costs more: they went to every other shader engine and left its
 // compute units idle, 2880 us instead of 1805 at 32768 rows, 16 experts, 4096 x 7168.)
 struct Scan {
-  int last[kWaves];   // last block of a wave's 64 where a run begins, or -1
+  int last[kWaves];   // last of a wave's blocks where a run begins, or -1
   int count[kWaves];  // tiles that begin in a wave's blocks
   int found;
 };
@@ -74,29 +74,58 @@ __device__ __forceinline__ RowTile find_tile(const GroupedParams& p, int log_per
   }
   if (target >= used) return t;
   if (threadIdx.x == 0) scan.found = -1;
+  // a wave takes `steps` times 64 blocks that follow each other, the workgroup 8192 at most
+  const int steps = min((used + kThreads - 1) / kThreads, 16);
   int begun = 0;  // where the run at the chunk's start begins
-  for (int chunk = 0; chunk < used; chunk += kThreads) {
-    const int b = chunk + (int)threadIdx.x;
-    const int e = expert_ids[min(b, used - 1)], previous = expert_ids[max(min(b, used) - 1, 0)];
-    const uint64_t begins = __ballot(b < used && (b == 0 || e != previous));
-    if (lane == 0) scan.last[wave] = begins ? b + 63 - __builtin_clzll(begins) : -1;
+  for (int chunk = 0; chunk < used; chunk += kThreads * steps) {
+    const int base = chunk + wave * 64 * steps;
+    int before = expert_ids[max(min(base, used) - 1, 0)], last = -1;
+    uint32_t mine = 0;  // which of this lane's blocks begin a run
+    for (int j = 0; j < steps; j += 4) {
+      int id[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) id[i] = expert_ids[min(base + 64 * (j + i) + lane, used - 1)];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = base + 64 * (j + i) + lane, below = __shfl_up(id[i], 1);
+        mine |= (uint32_t)((b < used) & ((b == 0) | (id[i] != (lane == 0 ? before : below)))) << (j + i);
+        before = __builtin_amdgcn_readlane(id[i], 63);
+      }
+    }
+    for (int j = 0; j < steps; ++j) {
+      const uint64_t begins = __ballot(mine >> j & 1);
+      if (begins) last = base + 64 * j + 63 - __builtin_clzll(begins);
+    }
+    if (lane == 0) scan.last[wave] = last;
     __syncthreads();
     int start = begun;
     for (int i = 0; i < kWaves; ++i) {
       if (i < wave) start = max(start, scan.last[i]);
       begun = max(begun, scan.last[i]);
     }
-    const uint64_t mine = begins & up_to;
-    if (mine) start = b - lane + 63 - __builtin_clzll(mine);
-    const uint64_t heads = __ballot(b < used && ((b - start) & (per - 1)) == 0);
-    if (lane == 0) scan.count[wave] = __builtin_popcountll(heads);
+    uint32_t heads = 0;
+    int count = 0;
+    for (int j = 0; j < steps; ++j) {
+      const int first = base + 64 * j, b = first + lane;
+      const uint64_t begins = __ballot(mine >> j & 1), at = begins & up_to;
+      const bool head = b < used && ((b - (at ? first + 63 - __builtin_clzll(at) : start)) & (per - 1)) == 0;
+      heads |= (uint32_t)head << j;
+      count += __builtin_popcountll(__ballot(head));
+      if (begins) start = first + 63 - __builtin_clzll(begins);
+    }
+    if (lane == 0) scan.count[wave] = count;
     __syncthreads();
-    int64_t index = t.total + __builtin_popcountll(heads & up_to) - 1;
+    int64_t ahead = t.total;  // tiles before this wave's
     for (int i = 0; i < kWaves; ++i) {
-      if (i < wave) index += scan.count[i];
+      if (i < wave) ahead += scan.count[i];
       t.total += scan.count[i];
     }
-    if (index == target && (heads >> lane & 1)) scan.found = b;
+    if (target < ahead || target >= ahead + count) continue;
+    for (int j = 0; j < steps; ++j) {
+      const uint64_t at = __ballot(heads >> j & 1);
+      if ((heads >> j & 1) && ahead + __builtin_popcountll(at & up_to) == target + 1) scan.found = base + 64 * j + lane;
+      ahead += __builtin_popcountll(at);
+    }
   }
   __syncthreads();
   t.block = __builtin_amdgcn_readfirstlane(scan.found);
@@ -295,7 +324,7 @@ Cut cut(const GroupedParams& p, int rows, int columns) {
   c.log_per = __builtin_ctz((unsigned)per);
   c.log_cut = __builtin_ctz((unsigned)pieces);
   // a launch has less than 2^32 threads; a workgroup goes on with every row_tiles-th row tile
-  c.row_tiles = std::min(c.row_tiles, std::max(1, (1 << 20) / c.ntiles) * kTileGroup);
+  c.row_tiles = std::min(c.row_tiles, ((1 << 20) - kXcds * kChunk) / c.ntiles * kTileGroup);
   const int64_t tiles = (int64_t)c.row_tiles * c.ntiles;
   c.grid = dim3((unsigned)((tiles + kXcds * kChunk - 1) / (kXcds * kChunk) * (kXcds * kChunk)));
   return c;

@@ -48,8 +48,14 @@ __device__ __forceinline__ Span span_of(const WgradParams& p, int e, int* scratc
   if (threadIdx.x == 0) scratch[0] = INT_MAX, scratch[1] = -1;
   __syncthreads();
   int lo = INT_MAX, hi = -1;
-  for (int i = (int)threadIdx.x; i < used; i += kThreads)
-    if (p.expert_ids[i] == e) lo = min(lo, i), hi = i;
+  for (int i = (int)threadIdx.x; i < used; i += 8 * kThreads) {
+    int id[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) id[j] = p.expert_ids[min(i + j * kThreads, used - 1)];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (id[j] == e) lo = min(lo, min(i + j * kThreads, used - 1)), hi = max(hi, min(i + j * kThreads, used - 1));
+  }
   if (hi >= 0) {
     atomicMin(&scratch[0], lo);
     atomicMax(&scratch[1], hi);
