@@ -213,8 +213,8 @@ __device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, i
   n.skip(turn.start);
   auto copy_m = [&](int q, uint32_t slot, int stage) { m.copy(q, slot, turn.left(stage), turn.on(stage), wave); };
   auto copy_n = [&](int q, uint32_t slot, int stage) { n.copy(q, slot, turn.left(stage), turn.on(stage), wave); };
-  prologue<M, N, W::kAhead, M::kBytes>(ring, copy_m, copy_n);
-  loop<T, M, N, W::kAhead, M::kBytes>(ring, turn.stages, at_m, at_n, lane, acc, copy_m, copy_n, [] {});
+  prologue<M, N, W::kAhead, M::kBytes>(ring, copy_m, copy_n, [](int) {});
+  loop<T, M, N, W::kAhead, M::kBytes>(ring, turn.stages, at_m, at_n, lane, acc, copy_m, copy_n, [](int) {}, [] {});
   uint32_t slotted[MT];  // which of 32 rows have a slot
 #pragma unroll
   for (int i = 0; i < MT; ++i) {

@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p, int m
       int32_t slot[8], owner;  // of a wave's rows of a stage, and their block's expert
       bool inside;
     };
-    Rows of_m, of_n;
+    Rows rows, next;  // of the stage that is being copied, and of the one after it
     auto look = [&](Rows& r, int stage) {
       const int row = begin + stage * kStep + 8 * wave, at = min(row, stop - 8);
 #pragma unroll
@@ -194,29 +194,20 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p, int m
       const int32_t low = my_row & 1 ? of[1] : of[0], high = my_row & 1 ? of[3] : of[2];
       return (uint32_t)(my_row & 2 ? high : low);
     };
-    look(of_m, 0);
-    look(of_n, 0);
-    auto copy_m = [&](int q, uint32_t lds, int stage) {
-      copy(of_m, at_m[q], slot_of(of_m, q), q, lds);
+    auto copy_m = [&](int q, uint32_t lds, int) {
+      copy(rows, at_m[q], slot_of(rows, q), q, lds);
       at_m[q] += kStep * row_m;
-      if (q == kMine - 1) look(of_m, stage + 1);
     };
-    auto copy_n = [&](int q, uint32_t lds, int stage) {
-      const uint32_t slot = slot_of(of_n, q);
-      copy(of_n, GATHER ? at_n[q] + (uint64_t)p.by_topk.of(slot) * (uint32_t)row_n : at_n[q], slot, q, lds);
+    auto copy_n = [&](int q, uint32_t lds, int) {
+      const uint32_t slot = slot_of(rows, q);
+      copy(rows, GATHER ? at_n[q] + (uint64_t)p.by_topk.of(slot) * (uint32_t)row_n : at_n[q], slot, q, lds);
       if (!GATHER) at_n[q] += kStep * row_n;
-      if (q == kMine - 1) look(of_n, stage + 1);
     };
-    prologue<Panel, Panel, kAhead, Panel::kBytes>(ring, copy_m, copy_n);
+    look(rows, 0);
+    prologue<Panel, Panel, kAhead, Panel::kBytes>(ring, copy_m, copy_n, [&](int stage) { look(rows, stage); });
     loop<T, Panel, Panel, kAhead, Panel::kBytes>(
-        ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc, copy_m, copy_n, [&] {
-          asm volatile(""
-                       : "+s"(of_m.slot[0]), "+s"(of_m.slot[1]), "+s"(of_m.slot[2]), "+s"(of_m.slot[3]),
-                         "+s"(of_m.slot[4]), "+s"(of_m.slot[5]), "+s"(of_m.slot[6]), "+s"(of_m.slot[7]), "+s"(of_m.owner));
-          asm volatile(""
-                       : "+s"(of_n.slot[0]), "+s"(of_n.slot[1]), "+s"(of_n.slot[2]), "+s"(of_n.slot[3]),
-                         "+s"(of_n.slot[4]), "+s"(of_n.slot[5]), "+s"(of_n.slot[6]), "+s"(of_n.slot[7]), "+s"(of_n.owner));
-        });
+        ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc, copy_m, copy_n,
+        [&](int stage) { look(next, stage); }, [&] { rows = next; });
   }
 
   const int at_m = wave / 4 * 32 * MT, at_n = wave % 4 * 32 * NT;
