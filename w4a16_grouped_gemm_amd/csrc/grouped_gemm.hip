@@ -4,9 +4,16 @@
 // with e(p) the expert of p's block and r(p) the row itself or its slot's token.
 //
 // Weights and rows go from memory straight to LDS (global_load_lds) and from there to the mfma
-// instructions (gemm_tile.h).
-// An expert's blocks lie side by side, so a tile takes as many of them as its rows hold, whatever
-// block_m is.
+// instructions (gemm_tile.h). An expert's blocks lie side by side, so a tile takes as many of them as its rows
+// hold, whatever block_m is. Tiles are 256 x 256 where that fills the card: 128 flops a byte copied from L2,
+// and at half of that (128 x 128) the copies alone would take the time of the products. Tiles with at most half
+// of their rows used multiply half.
+//
+// Measured (one MI355X, bf16): 32768 rows on 16 experts, 4096 x 7168: 1580..1720 us by card, 1.1..1.2 PFLOP/s, with
+// transposed weights 1670..1800. The clock is what gives: under this load it falls to 1.6 GHz of 2.4; at 2.4 (timing
+// builds without copies, on LDS that stays as it is) the same loop takes 1170. A tile of 256 x 256 x 64 takes 2500
+// cycles, of which the matrix cores work 2048, transposed 2700. 48 experts of 85 rows, 7168 x 2048: 320..340 us, 4.6
+// TB/s; of three rows, 4096 x 7168: 425..460 us, 6 TB/s (reads alone reach 6.9).
 #include "gemm_tile.h"
 #include "grouped_gemm.h"
 #include "row_ops.h"
@@ -21,19 +28,26 @@ using namespace tile;
 
 // Tile (row tile, column tile) of this workgroup: row tiles go in groups of kTileGroup with all their columns,
 // row tiles innermost. Workgroups go round-robin to the 8 XCDs, each with an L2 of its own, so XCD x
-// takes the x-th run of kChunk tiles of every 8 kChunk: about what its 32 compute units work on at once.
+// takes the x-th run of 1 << log_run tiles of every 8 runs: about what its 32 compute units work on at once.
 constexpr int kXcds = 8;
 constexpr int kTileGroup = 8;
-constexpr int kChunk = 32;
-__device__ __forceinline__ void tile_of(int ntiles, int64_t& row_tile, int& column_tile) {
+constexpr int kLogRun = 5;
+__device__ __forceinline__ void tile_of(int ntiles, int log_run, int64_t& row_tile, int& column_tile) {
   const int64_t at = (int64_t)blockIdx.x / kXcds;
-  const int64_t tile = (at / kChunk * kXcds + blockIdx.x % kXcds) * kChunk + at % kChunk;
+  const int64_t tile = (((at >> log_run) * kXcds + blockIdx.x % kXcds) << log_run) + (at & ((1 << log_run) - 1));
   const int64_t per_group = (int64_t)kTileGroup * ntiles;
   const int64_t group = tile / per_group;
   const int rest = (int)(tile - group * per_group);
   row_tile = group * kTileGroup + rest % kTileGroup;
   column_tile = rest / kTileGroup;
 }
+
+// How a call is cut into tiles.
+struct Cut {
+  int ntiles, row_tiles;  // of columns; of rows, as many as moe_align's order can have at most
+  int log_per, log_cut;   // blocks a tile, or tiles a block
+  int log_run;            // as in tile_of
+};
 
 // Row tile `target`: the tiles are the runs of blocks of one expert, cut into 1 << log_per
 // blocks. All threads of the workgroup call it. Counting here needs no launch or memory of its own. (A workgroup for every
@@ -230,21 +244,19 @@ __device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, i
 
 // A run's last tile takes half of the rows where it has no more.
 template <typename T, typename O, bool TRANSPOSED, typename W>
-__global__ __launch_bounds__(kThreads, W::kRing > 80 * 1024 ? 2 : 4) void grouped_kernel(GroupedParams p, int ntiles,
-                                                                                         int row_tiles, int log_per,
-                                                                                         int log_cut) {
+__global__ __launch_bounds__(kThreads, W::kRing > 80 * 1024 ? 2 : 4) void grouped_kernel(GroupedParams p, Cut c) {
   constexpr int kRows = W::kRows, kTileN = W::kTileN;
   __shared__ __attribute__((aligned(16))) uint8_t ring[W::kRing];
   int64_t target;
   int nt;
-  tile_of(ntiles, target, nt);
-  if (target >= row_tiles) return;
+  tile_of(c.ntiles, c.log_run, target, nt);
+  if (target >= c.row_tiles) return;
   // more tiles than moe_align's order can have: go round again
-  for (;; target += row_tiles) {
-    const RowTile tile = find_tile(p, log_per, target >> log_cut, *reinterpret_cast<Scan*>(ring));
+  for (;; target += c.row_tiles) {
+    const RowTile tile = find_tile(p, c.log_per, target >> c.log_cut, *reinterpret_cast<Scan*>(ring));
     if (tile.blocks == 0) return;
     const int e = tile.expert;
-    const int first = tile.block * p.block_m + (int)(target & ((1 << log_cut) - 1)) * kRows;
+    const int first = tile.block * p.block_m + (int)(target & ((1 << c.log_cut) - 1)) * kRows;
     const int rows = min(tile.blocks * p.block_m, kRows), n0 = nt * kTileN;
     if ((uint32_t)e >= (uint32_t)p.E) {  // no such expert
       constexpr int kEach = Line<O>::kEach, kLanes = kTileN / kEach;
@@ -258,15 +270,14 @@ __global__ __launch_bounds__(kThreads, W::kRing > 80 * 1024 ? 2 : 4) void groupe
     } else {
       product<T, O, TRANSPOSED, W>(p, ring, first, rows, e, n0);
     }
-    if (target + row_tiles >= tile.total << log_cut) return;
+    if (target + c.row_tiles >= tile.total << c.log_cut) return;
     __syncthreads();
   }
 }
 
 // Few rows an expert, or little work at all: a tile of 32 rows by 32 NT columns, shared by the waves along K.
 template <typename T, typename O, bool TRANSPOSED, int NT, int kAhead>
-__global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, int ntiles, int row_tiles, int log_per,
-                                                          int log_cut) {
+__global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, Cut c) {
   constexpr int kRows = 32, kTileN = 32 * NT, kSteps = 128;
   typedef RowPanel<kRows, kSteps> M;
   typedef std::conditional_t<TRANSPOSED, ColumnPanel<kTileN, kSteps>, RowPanel<kTileN, kSteps>> N;
@@ -276,13 +287,13 @@ __global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, int n
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   int64_t target;
   int nt;
-  tile_of(ntiles, target, nt);
-  if (target >= row_tiles) return;
-  for (;; target += row_tiles) {
-    const RowTile tile = find_tile(p, log_per, target >> log_cut, *reinterpret_cast<Scan*>(ring));
+  tile_of(c.ntiles, c.log_run, target, nt);
+  if (target >= c.row_tiles) return;
+  for (;; target += c.row_tiles) {
+    const RowTile tile = find_tile(p, c.log_per, target >> c.log_cut, *reinterpret_cast<Scan*>(ring));
     if (tile.blocks == 0) return;
     const int e = tile.expert;
-    const int first = tile.block * p.block_m + (int)(target & ((1 << log_cut) - 1)) * kRows;
+    const int first = tile.block * p.block_m + (int)(target & ((1 << c.log_cut) - 1)) * kRows;
     const int rows = min(tile.blocks * p.block_m, kRows), n0 = nt * kTileN;
     floatx16 acc[1][NT] = {};
     const bool known = (uint32_t)e < (uint32_t)p.E;
@@ -305,44 +316,44 @@ __global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, int n
       const floatx4 none = {0.f, 0.f, 0.f, 0.f};
       Four<O>::store(static_cast<O*>(p.out) + (int64_t)(first + row) * p.N + n0 + column, real ? v : none);
     });
-    if (target + row_tiles >= tile.total << log_cut) return;
+    if (target + c.row_tiles >= tile.total << c.log_cut) return;
     __syncthreads();
   }
 }
 
-// How the call is cut into tiles of `rows` rows by `columns` columns.
-struct Cut {
-  int ntiles, row_tiles, log_per, log_cut;
-  dim3 grid;
-};
 Cut cut(const GroupedParams& p, int rows, int columns) {
   const int per = std::max(1, rows / p.block_m), pieces = std::max(1, p.block_m / rows), blocks = p.capacity / p.block_m;
   Cut c;
   c.ntiles = (p.N + columns - 1) / columns;
-  // an expert's last tile may be of fewer blocks
-  c.row_tiles = (std::min(blocks, blocks / per + p.E) * pieces + kTileGroup - 1) / kTileGroup * kTileGroup;
+  // What moe_align's order can have at most: an expert's last tile may be of fewer rows. (By capacity alone, one token on
+  // 8 of 64 experts had 900 workgroups without a tile beside its 128: 18.6 us instead of 13.)
+  const int tiles = p.n_slots / std::max(rows, p.block_m) + std::min(p.E, p.n_slots);
+  c.row_tiles = (std::min(blocks, tiles) * pieces + kTileGroup - 1) / kTileGroup * kTileGroup;
   c.log_per = __builtin_ctz((unsigned)per);
   c.log_cut = __builtin_ctz((unsigned)pieces);
   // a launch has less than 2^32 threads; a workgroup goes on with every row_tiles-th row tile
-  c.row_tiles = std::min(c.row_tiles, ((1 << 20) - kXcds * kChunk) / c.ntiles * kTileGroup);
-  const int64_t tiles = (int64_t)c.row_tiles * c.ntiles;
-  c.grid = dim3((unsigned)((tiles + kXcds * kChunk - 1) / (kXcds * kChunk) * (kXcds * kChunk)));
+  c.row_tiles = std::min(c.row_tiles, ((1 << 20) - (kXcds << kLogRun)) / c.ntiles * kTileGroup);
+  const int64_t all = (int64_t)c.row_tiles * c.ntiles;
+  c.log_run = 0;  // few tiles go to all XCDs
+  while (c.log_run < kLogRun && (kXcds << (c.log_run + 1)) <= all) ++c.log_run;
   return c;
+}
+dim3 grid_of(const Cut& c) {
+  const int64_t all = (int64_t)c.row_tiles * c.ntiles, turn = kXcds << c.log_run;
+  return dim3((unsigned)((all + turn - 1) / turn * turn));
 }
 
 template <typename T, typename O, bool TRANSPOSED, typename W>
 hipError_t launch_tiles(const GroupedParams& p, hipStream_t stream) {
   const Cut c = cut(p, W::kRows, W::kTileN);
-  hipLaunchKernelGGL((grouped_kernel<T, O, TRANSPOSED, W>), c.grid, dim3(kThreads), 0, stream, p, c.ntiles, c.row_tiles,
-                     c.log_per, c.log_cut);
+  hipLaunchKernelGGL((grouped_kernel<T, O, TRANSPOSED, W>), grid_of(c), dim3(kThreads), 0, stream, p, c);
   return hipGetLastError();
 }
 
 template <typename T, typename O, bool TRANSPOSED, int NT, int kAhead>
 hipError_t launch_narrow(const GroupedParams& p, hipStream_t stream) {
   const Cut c = cut(p, 32, 32 * NT);
-  hipLaunchKernelGGL((narrow_kernel<T, O, TRANSPOSED, NT, kAhead>), c.grid, dim3(kThreads), 0, stream, p, c.ntiles,
-                     c.row_tiles, c.log_per, c.log_cut);
+  hipLaunchKernelGGL((narrow_kernel<T, O, TRANSPOSED, NT, kAhead>), grid_of(c), dim3(kThreads), 0, stream, p, c);
   return hipGetLastError();
 }
 
@@ -350,11 +361,11 @@ hipError_t launch_narrow(const GroupedParams& p, hipStream_t stream) {
 // as n_slots over E, their mean where every routed expert is resident; on a slice of the experts that counts
 // the others' slots too, and larger tiles may be taken than the slice's rows fill. Results do not
 // depend on the way but for the order of their sums. Measured, us by (256 x 256, 128 x 128, 64 x 128, 32 x 64) tiles,
-// bf16, K last: one expert of 4096 rows, 4096 x 4096: 118, 149, 192, 358; 8 experts of 256, 2048 x 2048: 55, 36,
-// 42, 64; 48 of 85, 7168 x 2048: 392, 397, 465, 879; one of 512 rows, 2048 x 2048: 45, 21, 18, 14; 10 of 77, 1384 x 1000
-// transposed: 23, 16, 18, 17; 384 of 11, 512 x 7168: 589, 548, 543, 528, and 7168 x 512 transposed: 721, 674, 628, 776;
-// 48 of 3 (384 routed), 4096 x 7168: 544, 497, 493, 481, transposed 579, 518, 504, 515; 8 experts of one row, 512 x
-// 7168: 82, 62, 50, 28, and by 32 x 32 tiles 21.
+// bf16, K last: one expert of 4096 rows, 4096 x 4096: 110, 141, 190, 351; 8 experts of 256, 2048 x 2048: 56, 35,
+// 40, 59; 48 of 85, 7168 x 2048: 325, 374, 435, 899; one of 512 rows, 2048 x 2048: 44, 21, 19, 14; 10 of 100, 1384 x 1000
+// transposed: 24, 17.5, 17.3, 22; 384 of 11, 512 x 7168: 489, 475, 475, 478, and 7168 x 512 transposed: 689, 634, 627, 821;
+// 48 of 3 (384 routed), 4096 x 7168: 464, 463, 464, 454, and 7168 x 4096 transposed 509, 483, 482, 498; 8 experts of one
+// row, 512 x 7168: 79, 42, 42, 19, and by 32 x 32 tiles 12.5 (of 512 rows above: 20).
 template <typename T, typename O, bool TRANSPOSED>
 hipError_t launch(const GroupedParams& p, hipStream_t stream) {
   const int64_t experts = std::min(p.E, p.n_slots), rows = (p.n_slots + experts - 1) / experts;
@@ -367,7 +378,8 @@ hipError_t launch(const GroupedParams& p, hipStream_t stream) {
     if (tiles(256, 256) >= 112 && p.N > 128) return launch_tiles<T, O, TRANSPOSED, Way<4, 2, 2>>(p, stream);
     if (tiles(128, 128) >= 96) return launch_tiles<T, O, TRANSPOSED, Way<2, 1, 2>>(p, stream);
   }
-  if (!TRANSPOSED && tiles(32, 64) < 128) return launch_narrow<T, O, TRANSPOSED, 1, 5>(p, stream);
+  // fewer workgroups than compute units: stages ahead for each instead (16 rows, 2048 x 8192: five 21.5 us, seven 17.3)
+  if (!TRANSPOSED && tiles(32, 64) < 128) return launch_narrow<T, O, TRANSPOSED, 1, 7>(p, stream);
   return launch_narrow<T, O, TRANSPOSED, 2, 3>(p, stream);
 }
 
