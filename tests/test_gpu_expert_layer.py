@@ -1,5 +1,8 @@
 """A training step of the experts' layer from its parts: rows to their experts, two products around the gated activation
 with its 8-bit checkpoint, rows back, and every gradient, against 64-bit autograd with bounds carried from part to part."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -230,3 +233,25 @@ def test_two_layers_at_once():
     for _, alone, beside, _ in cases:
         for k, v in beside.results().items():
             assert torch.equal(v, alone.results()[k]), k
+
+
+def test_readme_step():
+    """The README's training step on buffers of its names: the bits of Layer's calls."""
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
+        code, = [c for c in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "moe_grouped_gemm_wgrad" in c]
+    T, topk, E, G, bm, H, I = SHAPES[1]
+    t = torch.bfloat16
+    r = Routing(T, topk, E, G, bm, seed=51)
+    given = [v.cuda() for v in inputs(r, H, I, t, 52)]
+    layer, own = Layer(r, H, I, t, True), Layer(r, H, I, t, True)
+    layer.forward(*given[:4])
+    layer.backward(*given)
+    x, w1, w2, weights, dout = given
+    exec(code, {"w": w, "T": T, "topk": topk, "srt": r.sorted, "eid": r.expert_ids, "ntpp": r.ntpp, "bm": bm, "x": x,
+                "w1": w1, "w2": w2, "topk_weights": weights, "dout": dout, "xp": own.xp, "slot_rows": own.slot_rows,
+                "gu": own.gu, "h": own.h, "q": own.q, "s": own.s, "y": own.y, "out": own.out, "dy": own.dy, "dh": own.dh,
+                "dgu": own.dgu, "dw1": own.dw1, "dw2": own.dw2, "ws1": own.ws[0], "ws2": own.ws[1], "dxp": own.dxp,
+                "dx": own.dx, "dtopk_weights": own.dweights})
+    torch.cuda.synchronize()
+    for k, v in own.results().items():
+        assert torch.equal(v, layer.results()[k]), k
