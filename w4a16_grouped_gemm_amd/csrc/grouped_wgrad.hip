@@ -52,7 +52,9 @@ __device__ __forceinline__ Span span_of(const WgradParams& p, int e, int* scratc
   if (threadIdx.x == 0) scratch[0] = INT_MAX, scratch[1] = -1;
   __syncthreads();
   int lo = INT_MAX, hi = -1;
-  for (int i = (int)threadIdx.x; i < used; i += 8 * kThreads) {
+  int i = (int)threadIdx.x;
+  if (i < used && p.expert_ids[i] == e) lo = hi = i;
+  for (i += kThreads; i < used; i += 8 * kThreads) {  // many blocks: eight loads on their way together
     int id[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) id[j] = p.expert_ids[min(i + j * kThreads, used - 1)];
