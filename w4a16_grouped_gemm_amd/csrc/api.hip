@@ -916,6 +916,7 @@ int moe_grouped_gemm(int32_t num_experts, int32_t N, int32_t K, const void* a, i
   p.capacity = capacity;
   p.block_m = block_m;
   p.transposed = transposed != 0;
+  p.far = gather && (int64_t)T * K * 2 > (int64_t)UINT32_MAX;
   return hip_status(launch_grouped_gemm(p, dtype, out_dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -958,6 +959,7 @@ int moe_grouped_gemm_wgrad(int32_t num_experts, int32_t N, int32_t K, const void
   p.by_topk = Divisor::by((uint32_t)topk);
   p.n_slots = T * topk;
   p.capacity = T == 0 ? 0 : capacity;  // no slot: zeros, or dw as it was
+  p.far = gather && (int64_t)T * K * 2 > (int64_t)UINT32_MAX;
   p.log_block = __builtin_ctz((unsigned)block_m);
   p.accumulate = accumulate != 0;
   p.cut = cut;

@@ -21,6 +21,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace w4a16 {
 namespace tile {
 
@@ -56,6 +58,11 @@ static __device__ __attribute__((aligned(16))) const uint32_t kZeros[128] = {};
 __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
 }
+// The same from base + offset (bytes): no vector instruction but the copy.
+__device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
 // Until at most N of this wave's copies are on their way.
@@ -81,28 +88,32 @@ struct RowPanel {
   static constexpr int kUnits = kBytes / 1024;  // copies of a stage
   static constexpr int kMine = (kUnits + kWaves - 1) / kWaves;
   static constexpr int kLanes = kPitch / 16;  // that copy a row
-  const uint8_t* at[kMine];
-  int32_t first[kMine];  // this lane's first step of r in a stage
+  const uint8_t* base;     // of the stage to be copied next
+  uint32_t offset[kMine];  // this lane's 16 bytes from there, or `far` the row
+  int64_t far;             // bytes a row where 32 bits do not hold the offsets, else 0
 
   // where there are fewer copies than waves, two waves make the same one
   static __device__ __forceinline__ int unit_of(int i, int wave) { return (kMine * wave + i) % kUnits; }
   static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 64 / kLanes * unit_of(i, wave) + lane / kLanes; }
   static __device__ __forceinline__ int swizzle(int row) { return kSteps == 64 ? row >> 1 & 7 : row & 15; }
+  // this lane's first step of r in copy i
+  static __device__ __forceinline__ int first_of(int i, int wave, int lane) {
+    return 8 * (lane % kLanes ^ swizzle(row_of(i, wave, lane)));
+  }
 
-  // row: the start of row row_of(i, ...)
-  __device__ __forceinline__ void set(int i, const void* row, int wave, int lane) {
-    first[i] = 8 * (lane % kLanes ^ swizzle(row_of(i, wave, lane)));
-    at[i] = static_cast<const uint8_t*>(row) + 2 * first[i];
+  // row `row` of those from base on, of `pitch` bytes, is row_of(i, ...)
+  __device__ __forceinline__ void set(int i, uint32_t row, int64_t pitch, int wave, int lane) {
+    offset[i] = far ? row : row * (uint32_t)pitch + 2 * first_of(i, wave, lane);
   }
-  // from the first stage to stage s
-  __device__ __forceinline__ void skip(int s) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) at[i] += (int64_t)s * kPitch;
-  }
-  // copy i of the next stage, of which `left` steps are in the operand; the copy after it is `on` stages on
-  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int on, int wave) {
-    copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
-    at[i] += (int64_t)on * kPitch;
+  // to `on` stages on
+  __device__ __forceinline__ void go(int on) { base += (int64_t)on * kPitch; }
+  // copy i of a stage that lies in the operand as a whole, where nothing is far
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) const { copy16(base, offset[i], lds + 1024 * unit_of(i, wave)); }
+  // copy i of any stage, of which `left` steps are in the operand
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave, int lane) const {
+    const int first = first_of(i, wave, lane);
+    const uint8_t* at = base + (far ? (uint64_t)offset[i] * (uint64_t)far + 2 * first : offset[i]);
+    copy16(left > first ? (const void*)at : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
   }
   // steps 16 k + 8 (lane / 32) + 0..7 of row outer0 + lane % 32; outer0 a multiple of 32
   template <typename T>
@@ -123,33 +134,34 @@ struct ColumnPanel {
   static constexpr int kMine = (kUnits + kWaves - 1) / kWaves;
   static constexpr int kLanes = kOuter / 8;  // that copy a step
   static constexpr int kParts = kOuter / 32;
-  const uint8_t* at[kMine];
-  int32_t first[kMine];
-  int64_t stride;  // bytes a stage
+  const uint8_t* base;     // of the stage to be copied next
+  uint32_t offset[kMine];  // this lane's 16 bytes from there
+  int64_t stride;          // bytes a stage
 
   static __device__ __forceinline__ int unit_of(int i, int wave) { return (kMine * wave + i) % kUnits; }
   static __device__ __forceinline__ int swizzle(int step) {
     return kParts >= 4 ? step & 3 : kParts == 2 ? step >> 1 & 1 : 0;
   }
-  // base: step 0, column 0 of the panel; steps of ld columns, `columns` of them from `base` on. Columns past
+  // this lane's step of r in copy i
+  static __device__ __forceinline__ int first_of(int i, int wave, int lane) {
+    return (64 / kLanes) * unit_of(i, wave) + lane / kLanes;
+  }
+  // from: step 0, column 0 of the panel; steps of ld columns, `columns` of them from there on. Columns past
   // those are copies of column 0.
   template <typename T>
-  __device__ __forceinline__ void set(const T* base, int64_t ld, int32_t columns, int wave, int lane) {
-    stride = ld * kSteps * (int)sizeof(T);
+  __device__ __forceinline__ void set(const T* from, int32_t ld, int32_t columns, int wave, int lane) {
+    base = reinterpret_cast<const uint8_t*>(from);
+    stride = (int64_t)ld * kSteps * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      first[i] = (64 / kLanes) * unit_of(i, wave) + lane / kLanes;
-      const int column = 8 * ((lane % kLanes) ^ (swizzle(first[i]) << 2));
-      at[i] = reinterpret_cast<const uint8_t*>(base + first[i] * ld + (column < columns ? column : 0));
+      const int first = first_of(i, wave, lane), column = 8 * ((lane % kLanes) ^ (swizzle(first) << 2));
+      offset[i] = (uint32_t)sizeof(T) * ((uint32_t)first * (uint32_t)ld + (uint32_t)(column < columns ? column : 0));
     }
   }
-  __device__ __forceinline__ void skip(int s) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) at[i] += s * stride;
-  }
-  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int on, int wave) {
-    copy16(left > first[i] ? (const void*)at[i] : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
-    at[i] += on * stride;
+  __device__ __forceinline__ void go(int on) { base += on * stride; }
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) const { copy16(base, offset[i], lds + 1024 * unit_of(i, wave)); }
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave, int lane) const {
+    copy16(left > first_of(i, wave, lane) ? (const void*)(base + offset[i]) : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
   }
   // As RowPanel's, by two transposing reads: sixteen lanes read four steps of sixteen columns,
   // lane i the columns 4 (i % 4) + 0..3 of step i / 4, and get column i's four steps.
@@ -184,9 +196,9 @@ __device__ __forceinline__ void prologue(const uint8_t* ring, CopyM copy_m, Copy
 #pragma unroll
   for (int s = 0; s < kAhead; ++s) {
 #pragma unroll
-    for (int q = 0; q < M::kMine; ++q) copy_m(q, base_m + s * kBytesM, s);
+    for (int q = 0; q < M::kMine; ++q) copy_m(q, base_m + s * kBytesM, s, std::false_type());
 #pragma unroll
-    for (int q = 0; q < N::kMine; ++q) copy_n(q, base_n + s * N::kBytes, s);
+    for (int q = 0; q < N::kMine; ++q) copy_n(q, base_n + s * N::kBytes, s, std::false_type());
     next(s + 1);
   }
 }
@@ -207,9 +219,9 @@ __device__ __forceinline__ void prologue(const uint8_t* ring, CopyM copy_m, Copy
 // wait, a part after its issue (issued where the copies need them, twice a stage, the weights' gradient of
 // 32768 rows, 16 experts, 4096 x 7168 took 1894 instead of 1800 us).
 template <typename T, typename M, typename N, int kAhead, int kBytesM, int MT, int NT, typename CopyM, typename CopyN,
-          typename Ahead, typename Turn>
-__device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, int lane, floatx16 (&acc)[MT][NT],
-                                     CopyM copy_m, CopyN copy_n, Ahead ahead, Turn turn) {
+          typename Real, typename Ahead, typename Turn>
+__device__ __forceinline__ void loop(uint8_t* ring, int whole, int stages, int m0, int n0, int lane, floatx16 (&acc)[MT][NT],
+                                     CopyM copy_m, CopyN copy_n, Real real, Ahead ahead, Turn turn) {
   static_assert(kAhead >= 2, "a stage is read while the next one lands");
   constexpr int kMfmas = MT * NT, kFragments = MT + NT;
   uint8_t* const ring_n = ring + (kAhead + 1) * kBytesM;
@@ -238,13 +250,13 @@ __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, 
   lds_barrier();
 #pragma unroll
   for (int f = 0; f < kFragments; ++f) fetch(f, ring, ring_n, 0);
-  int at_m = 0, at_n = 0;  // the slots of stage s, in bytes
-  for (int s = 0; s < stages; ++s) {
+  int s = 0, at_m = 0, at_n = 0;  // the slots of stage s, in bytes
+  auto multiply = [&](auto kind) {
     const int next_m = at_m == kAhead * kBytesM ? 0 : at_m + kBytesM;
     const int next_n = at_n == (kAhead - 1) * N::kBytes ? 0 : at_n + N::kBytes;
     const uint8_t *slot_m = ring + at_m, *slot_n = ring_n + at_n;
     const uint32_t free_m = base_m + (at_m == 0 ? kAhead * kBytesM : at_m - kBytesM);  // of stage s - 1
-    auto far = [&](int q) { copy_m(q, free_m, s + kAhead); };
+    auto far = [&](int q) { copy_m(q, free_m, s + kAhead, kind); };
     constexpr int kThird = (M::kMine + 2) / 3, kTwoThirds = 2 * M::kMine / 3 > kThird ? 2 * M::kMine / 3 : kThird;
     ahead(s + kAhead + 1);
     part(0, slot_m, slot_n, 1, 0, kThird, far);
@@ -253,11 +265,14 @@ __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, 
     // a wave's copies land in order: younger than stage s + 1's are M's of kAhead - 1 stages and N's of kAhead - 2
     wait_copies<(kAhead - 1) * M::kMine + (kAhead - 2) * N::kMine>();
     lds_barrier();
-    part(3, ring + next_m, ring_n + next_n, 0, 0, N::kMine, [&](int q) { copy_n(q, base_n + at_n, s + kAhead); });
+    part(3, ring + next_m, ring_n + next_n, 0, 0, N::kMine, [&](int q) { copy_n(q, base_n + at_n, s + kAhead, kind); });
     turn();
     at_m = next_m;
     at_n = next_n;
-  }
+  };
+  // (a choice within one loop makes the compiler move all sums about)
+  for (; s < whole && real(); ++s) multiply(std::true_type());
+  for (; s < stages; ++s) multiply(std::false_type());
   wait_copies<0>();
   lds_barrier();
 }
@@ -266,30 +281,34 @@ __device__ __forceinline__ void loop(uint8_t* ring, int stages, int m0, int n0, 
 // steps wave w multiplies 16, so that a stage costs one barrier and one wait for LDS, where a wave's share of a
 // small tile would wait for LDS in every part. kAhead stages in LDS (copy makes both panels' copies of one).
 // acc: each wave's share of the sums.
-template <typename T, typename M, typename N, int kAhead, int MT, int NT, typename Copy>
-__device__ __forceinline__ void shared_loop(uint8_t* ring, int stages, int wave, int lane, floatx16 (&acc)[MT][NT],
-                                            Copy copy) {
+template <typename T, typename M, typename N, int kAhead, bool kSome, int MT, int NT, typename Copy>
+__device__ __forceinline__ void shared_loop(uint8_t* ring, int whole, int stages, int wave, int lane,
+                                            floatx16 (&acc)[MT][NT], Copy copy) {
   constexpr int kBytes = M::kBytes + N::kBytes, kCopies = M::kMine + N::kMine;
   const uint32_t base = lds_address(ring);
 #pragma unroll
-  for (int s = 0; s < kAhead - 1; ++s) copy(base + s * kBytes, s);
-  int slot = 0, free = (kAhead - 1) * kBytes;
-  for (int s = 0; s < stages; ++s) {
-    wait_copies<(kAhead - 2) * kCopies>();
-    lds_barrier();  // stage s has landed, stage s - 1 has been read
-    vec8<T> m[MT], n[NT];
+  for (int s = 0; s < kAhead - 1; ++s) copy(base + s * kBytes, s, std::false_type());
+  int s = 0, slot = 0, free = (kAhead - 1) * kBytes;
+  auto stretch = [&](int to, auto kind) {
+    for (; s < to; ++s) {
+      wait_copies<(kAhead - 2) * kCopies>();
+      lds_barrier();  // stage s has landed, stage s - 1 has been read
+      vec8<T> m[MT], n[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) n[j] = N::template fragment<T>(ring + slot + M::kBytes, 32 * j, wave, lane);
+      for (int j = 0; j < NT; ++j) n[j] = N::template fragment<T>(ring + slot + M::kBytes, 32 * j, wave, lane);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) m[i] = M::template fragment<T>(ring + slot, 32 * i, wave, lane);
-    copy(base + free, s + kAhead - 1);
+      for (int i = 0; i < MT; ++i) m[i] = M::template fragment<T>(ring + slot, 32 * i, wave, lane);
+      copy(base + free, s + kAhead - 1, kind);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma(n[j], m[i], acc[i][j]);
-    free = slot;
-    slot = slot == (kAhead - 1) * kBytes ? 0 : slot + kBytes;
-  }
+        for (int j = 0; j < NT; ++j) acc[i][j] = mfma(n[j], m[i], acc[i][j]);
+      free = slot;
+      slot = slot == (kAhead - 1) * kBytes ? 0 : slot + kBytes;
+    }
+  };
+  if constexpr (kSome) stretch(whole, std::true_type());
+  stretch(stages, std::false_type());
   wait_copies<0>();
   lds_barrier();
 }

@@ -32,6 +32,7 @@ struct GroupedParams {
   Divisor by_topk;
   int32_t n_slots, capacity, block_m;
   int32_t transposed;
+  int32_t far;            // token rows that 32 bits of bytes do not reach
 };
 hipError_t launch_grouped_gemm(const GroupedParams& p, int32_t dtype, int32_t out_dtype, hipStream_t stream);
 
@@ -52,6 +53,7 @@ struct WgradParams {
   int32_t gather;
   Divisor by_topk;
   int32_t n_slots, capacity;
+  int32_t far;            // token rows that 32 bits of bytes do not reach
   int32_t log_block;      // of block_m, to base 2
   int32_t accumulate;
   WgradCut cut;

@@ -161,7 +161,7 @@ template <bool ON>
 struct Turn {
   int K, stages, start;
   __device__ __forceinline__ Turn(int K_, int e)
-      : K(K_), stages((K_ + kStep - 1) / kStep), start(ON ? (int)(3u * (unsigned)e % (unsigned)stages) : 0) {}
+      : K(K_), stages((K_ + kStep - 1) / kStep), start(ON && K_ % kStep == 0 ? (int)(3u * (unsigned)e % (unsigned)stages) : 0) {}
   __device__ __forceinline__ int at(int stage) const {
     const int s = stage + start;
     return s < stages ? s : s - stages;
@@ -186,12 +186,14 @@ struct Way {
 // Where the wave's copies of rows come from: row i of the tile, or row 0 where it has no slot (zeroed at the store).
 template <typename T, typename M>
 __device__ __forceinline__ void set_rows(M& m, const GroupedParams& p, int first, int rows, int wave, int lane) {
+  const int64_t pitch = (int64_t)p.K * (int)sizeof(T);
+  m.base = static_cast<const uint8_t*>(p.a) + (p.gather ? 0 : first * pitch);
+  m.far = p.far ? pitch : 0;
 #pragma unroll
   for (int i = 0; i < M::kMine; ++i) {
     const int row = M::row_of(i, wave, lane);
     const uint32_t slot = row < rows ? (uint32_t)p.sorted[first + row] : ~0u;
-    const int64_t from = slot >= (uint32_t)p.n_slots ? 0 : p.gather ? (int64_t)p.by_topk.of(slot) : first + row;
-    m.set(i, static_cast<const T*>(p.a) + from * p.K, wave, lane);
+    m.set(i, slot >= (uint32_t)p.n_slots ? 0 : p.gather ? p.by_topk.of(slot) : (uint32_t)row, pitch, wave, lane);
   }
 }
 
@@ -200,11 +202,13 @@ template <typename T, bool TRANSPOSED, typename N>
 __device__ __forceinline__ void set_weights(N& n, const GroupedParams& p, int e, int n0, int wave, int lane) {
   const T* w = static_cast<const T*>(p.w) + (int64_t)e * p.N * p.K;
   if constexpr (TRANSPOSED) {
-    n.set(w + n0, (int64_t)p.N, p.N - n0, wave, lane);
+    n.set(w + n0, p.N, p.N - n0, wave, lane);
   } else {
+    n.base = reinterpret_cast<const uint8_t*>(w + (int64_t)n0 * p.K);
+    n.far = 0;
 #pragma unroll
     for (int i = 0; i < N::kMine; ++i)
-      n.set(i, w + (int64_t)min(n0 + N::row_of(i, wave, lane), p.N - 1) * p.K, wave, lane);
+      n.set(i, (uint32_t)min(N::row_of(i, wave, lane), p.N - 1 - n0), (int64_t)p.K * (int)sizeof(T), wave, lane);
   }
 }
 
@@ -223,12 +227,20 @@ __device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, i
   set_weights<T, TRANSPOSED>(n, p, e, n0, wave, lane);
   const int at_m = wave / 4 * 32 * MT, at_n = wave % 4 * 32 * NT;
   const Turn<(!TRANSPOSED && MT == 2 && NT == 2)> turn(p.K, e);
-  m.skip(turn.start);
-  n.skip(turn.start);
-  auto copy_m = [&](int q, uint32_t slot, int stage) { m.copy(q, slot, turn.left(stage), turn.on(stage), wave); };
-  auto copy_n = [&](int q, uint32_t slot, int stage) { n.copy(q, slot, turn.left(stage), turn.on(stage), wave); };
+  m.go(turn.start);
+  n.go(turn.start);
+  auto copy_of = [&](auto& panel, int q, uint32_t slot, int stage, auto whole) {
+    if constexpr (whole)
+      panel.copy(q, slot, wave);
+    else
+      panel.copy(q, slot, turn.left(stage), wave, lane);
+    if (q == std::remove_reference_t<decltype(panel)>::kMine - 1) panel.go(turn.on(stage));
+  };
+  auto copy_m = [&](int q, uint32_t slot, int stage, auto whole) { copy_of(m, q, slot, stage, whole); };
+  auto copy_n = [&](int q, uint32_t slot, int stage, auto whole) { copy_of(n, q, slot, stage, whole); };
   prologue<M, N, W::kAhead, M::kBytes>(ring, copy_m, copy_n, [](int) {});
-  loop<T, M, N, W::kAhead, M::kBytes>(ring, turn.stages, at_m, at_n, lane, acc, copy_m, copy_n, [](int) {}, [] {});
+  loop<T, M, N, W::kAhead, M::kBytes>(ring, p.far ? 0 : p.K / kStep - W::kAhead, turn.stages, at_m, at_n, lane, acc,
+                                      copy_m, copy_n, [] { return true; }, [](int) {}, [] {});
   uint32_t slotted[MT];  // which of 32 rows have a slot
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -302,12 +314,20 @@ __global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, Cut c
       set_rows<T>(m, p, first, rows, wave, lane);
       N n;
       set_weights<T, TRANSPOSED>(n, p, e, n0, wave, lane);
-      shared_loop<T, M, N, kAhead>(ring, (p.K + kSteps - 1) / kSteps, wave, lane, acc, [&](uint32_t slot, int stage) {
+      const int whole = p.far ? 0 : p.K / kSteps - (kAhead - 1);
+      shared_loop<T, M, N, kAhead, true>(ring, whole, (p.K + kSteps - 1) / kSteps, wave, lane, acc,
+                                         [&](uint32_t slot, int stage, auto kind) {
         const int left = p.K - stage * kSteps;
 #pragma unroll
-        for (int i = 0; i < M::kMine; ++i) m.copy(i, slot, left, 1, wave);
+        for (int i = 0; i < M::kMine; ++i)
+          if constexpr (kind) m.copy(i, slot, wave);
+          else m.copy(i, slot, left, wave, lane);
 #pragma unroll
-        for (int i = 0; i < N::kMine; ++i) n.copy(i, slot + M::kBytes, left, 1, wave);
+        for (int i = 0; i < N::kMine; ++i)
+          if constexpr (kind) n.copy(i, slot + M::kBytes, wave);
+          else n.copy(i, slot + M::kBytes, left, wave, lane);
+        m.go(1);
+        n.go(1);
       });
     }
     shared_drain(ring, wave, lane, acc, [&](int row, int column, floatx4 v) {

@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void narrow_wgrad_kernel(WgradParams p, i
       at_n[q] = static_cast<const uint8_t*>(p.a) + 2 * (n0 + (column < p.K - n0 ? column : 0));
       from[q] = table[row];
     }
-    shared_loop<T, Panel, Panel, kAhead>(ring, stages, wave, lane, acc, [&](uint32_t lds, int stage) {
+    shared_loop<T, Panel, Panel, kAhead, false>(ring, 0, stages, wave, lane, acc, [&](uint32_t lds, int stage, std::false_type) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const bool real = from[q] >= 0;
@@ -171,7 +171,10 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p, int m
       int32_t slot[8], owner;  // of a wave's rows of a stage, and their block's expert
       bool inside;
     };
-    Rows rows, next;  // of the stage that is being copied, and of the one after it
+    Rows rows, next;   // of the stage that is being copied, and of the one after it
+    uint32_t from[8];  // where the rows begin in a, in bytes (GATHER; not used where 32 bits do not hold them)
+    bool real;         // all eight have a slot
+    const int64_t row_m = (int64_t)p.N * (int)sizeof(T), row_n = (int64_t)p.K * (int)sizeof(T);
     auto look = [&](Rows& r, int stage) {
       const int row = begin + stage * kStep + 8 * wave, at = min(row, stop - 8);
 #pragma unroll
@@ -179,41 +182,64 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p, int m
       r.owner = expert_ids[at >> p.log_block];
       r.inside = row < stop;
     };
+    auto arrive = [&] {
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        most = max(most, (uint32_t)rows.slot[i]);
+        from[i] = GATHER ? p.by_topk.of((uint32_t)rows.slot[i]) * (uint32_t)row_n : 0;
+      }
+      real = (most < (uint32_t)p.n_slots) & (rows.owner == e) & rows.inside & !p.far;
+    };
     const int my_row = lane / Panel::kLanes;
-    const int64_t row_m = (int64_t)p.N * (int)sizeof(T), row_n = (int64_t)p.K * (int)sizeof(T);
-    const uint8_t *at_m[kMine], *at_n[kMine];  // this lane's 16 bytes in the copies of the next stage (GATHER: of token 0)
+    auto mine = [&](const auto* of) {  // of this lane's row
+      if constexpr (kRows == 2) return my_row ? of[1] : of[0];
+      // by the bits of my_row: a chain over its values becomes an array in memory
+      const auto low = my_row & 1 ? of[1] : of[0], high = my_row & 1 ? of[3] : of[2];
+      return my_row & 2 ? high : low;
+    };
+    // of the next stage's first row of the workgroup (GATHER: of token 0), and this lane's 16 bytes from there
+    const uint8_t* base_m = static_cast<const uint8_t*>(p.dout) + begin * row_m + 2 * m0;
+    const uint8_t* base_n = static_cast<const uint8_t*>(p.a) + (GATHER ? 0 : begin * row_n) + 2 * n0;
+    uint32_t offset_m[kMine], offset_n[kMine];
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
-      const int64_t row = begin + 8 * wave + kRows * q + my_row;
+      const int row = 8 * wave + kRows * q + my_row;
       const int column = 8 * (lane % Panel::kLanes ^ (Panel::swizzle(kRows * q + my_row) << 2));
-      at_m[q] = static_cast<const uint8_t*>(p.dout) + row * row_m + 2 * (m0 + (column < p.N - m0 ? column : 0));
-      at_n[q] = static_cast<const uint8_t*>(p.a) + (GATHER ? 0 : row * row_n) + 2 * (n0 + (column < p.K - n0 ? column : 0));
+      offset_m[q] = (uint32_t)row * (uint32_t)row_m + 2 * (m0 + column < p.N ? column : 0);
+      offset_n[q] = (GATHER ? 0 : (uint32_t)row * (uint32_t)row_n) + 2 * (n0 + column < p.K ? column : 0);
     }
-    auto copy = [&](const Rows& r, const uint8_t* at, uint32_t slot, int q, uint32_t lds) {
-      const bool real = (slot < (uint32_t)p.n_slots) & (r.owner == e) & r.inside;
-      copy16(real ? (const void*)at : (const void*)kZeros, lds + 1024 * (kMine * wave + q));
+    auto copy = [&](const uint8_t* at, uint32_t slot, int q, uint32_t lds) {
+      const bool some = (slot < (uint32_t)p.n_slots) & (rows.owner == e) & rows.inside;
+      copy16(some ? (const void*)at : (const void*)kZeros, lds + 1024 * (kMine * wave + q));
     };
-    auto slot_of = [&](const Rows& r, int q) {  // of this lane's row
-      const int32_t* of = &r.slot[kRows * q];
-      if constexpr (kRows == 2) return (uint32_t)(my_row ? of[1] : of[0]);
-      // by the bits of my_row: a chain over its values becomes an array in memory
-      const int32_t low = my_row & 1 ? of[1] : of[0], high = my_row & 1 ? of[3] : of[2];
-      return (uint32_t)(my_row & 2 ? high : low);
+    auto copy_m = [&](int q, uint32_t lds, int, auto whole) {
+      if constexpr (whole)
+        copy16(base_m, offset_m[q], lds + 1024 * (kMine * wave + q));
+      else
+        copy(base_m + offset_m[q], (uint32_t)mine(&rows.slot[kRows * q]), q, lds);
+      if (q == kMine - 1) base_m += kStep * row_m;
     };
-    auto copy_m = [&](int q, uint32_t lds, int) {
-      copy(rows, at_m[q], slot_of(rows, q), q, lds);
-      at_m[q] += kStep * row_m;
-    };
-    auto copy_n = [&](int q, uint32_t lds, int) {
-      const uint32_t slot = slot_of(rows, q);
-      copy(rows, GATHER ? at_n[q] + (uint64_t)p.by_topk.of(slot) * (uint32_t)row_n : at_n[q], slot, q, lds);
-      if (!GATHER) at_n[q] += kStep * row_n;
+    auto copy_n = [&](int q, uint32_t lds, int, auto whole) {
+      if constexpr (whole) {
+        copy16(base_n, GATHER ? offset_n[q] + mine(&from[kRows * q]) : offset_n[q], lds + 1024 * (kMine * wave + q));
+      } else {
+        const uint32_t slot = (uint32_t)mine(&rows.slot[kRows * q]);
+        const uint8_t* at = base_n + offset_n[q];
+        copy(GATHER ? at + (uint64_t)p.by_topk.of(slot) * (uint64_t)row_n : at, slot, q, lds);
+      }
+      if (!GATHER && q == kMine - 1) base_n += kStep * row_n;
     };
     look(rows, 0);
     prologue<Panel, Panel, kAhead, Panel::kBytes>(ring, copy_m, copy_n, [&](int stage) { look(rows, stage); });
+    arrive();
     loop<T, Panel, Panel, kAhead, Panel::kBytes>(
-        ring, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc, copy_m, copy_n,
-        [&](int stage) { look(next, stage); }, [&] { rows = next; });
+        ring, stages, stages, wave / 4 * 32 * MT, wave % 4 * 32 * NT, lane, acc, copy_m, copy_n, [&] { return real; },
+        [&](int stage) { look(next, stage); },
+        [&] {
+          rows = next;
+          arrive();
+        });
   }
 
   const int at_m = wave / 4 * 32 * MT, at_n = wave % 4 * 32 * NT;
