@@ -115,10 +115,11 @@ struct RowPanel {
     const uint8_t* at = base + (far ? (uint64_t)offset[i] * (uint64_t)far + 2 * first : offset[i]);
     copy16(left > first ? (const void*)at : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
   }
-  // steps 16 k + 8 (lane / 32) + 0..7 of row outer0 + lane % 32; outer0 a multiple of 32
+  // steps 16 k + 8 (lane / 32) + 0..7 of row outer0 + lane % 32; outer0 a multiple of 32, place that of it
+  static __device__ __forceinline__ int place(int outer0, int) { return outer0; }
   template <typename T>
-  static __device__ __forceinline__ vec8<T> fragment(const uint8_t* panel, int outer0, int k, int lane) {
-    const int row = outer0 + (lane & 31);
+  static __device__ __forceinline__ vec8<T> fragment(const uint8_t* panel, int place, int k, int lane) {
+    const int row = place + (lane & 31);
     return *reinterpret_cast<const vec8<T>*>(panel + row * kPitch + (((2 * k + (lane >> 5)) ^ swizzle(row)) << 4));
   }
 };
@@ -165,11 +166,16 @@ struct ColumnPanel {
   }
   // As RowPanel's, by two transposing reads: sixteen lanes read four steps of sixteen columns,
   // lane i the columns 4 (i % 4) + 0..3 of step i / 4, and get column i's four steps.
-  template <typename T>
-  static __device__ __forceinline__ vec8<T> fragment(const uint8_t* panel, int outer0, int k, int lane) {
+  static __device__ __forceinline__ int place(int outer0, int lane) {
     const int i = lane & 15;
     const int part = (outer0 >> 5) ^ swizzle(i >> 2);
-    const uint8_t* at = panel + (16 * k + 8 * (lane >> 5) + (i >> 2)) * kPitch + (part << 6) + 32 * (lane >> 4 & 1) + 8 * (i & 3);
+    int at = (8 * (lane >> 5) + (i >> 2)) * kPitch + (part << 6) + 32 * (lane >> 4 & 1) + 8 * (i & 3);
+    asm volatile("" : "+v"(at));  // as it is, not in its terms at every read
+    return at;
+  }
+  template <typename T>
+  static __device__ __forceinline__ vec8<T> fragment(const uint8_t* panel, int place, int k, int) {
+    const uint8_t* at = panel + place + 16 * k * kPitch;
     struct {
       shortx4 v[2];
     } r;
@@ -227,11 +233,16 @@ __device__ __forceinline__ void loop(uint8_t* ring, int whole, int stages, int m
   uint8_t* const ring_n = ring + (kAhead + 1) * kBytesM;
   const uint32_t base_m = lds_address(ring), base_n = base_m + (kAhead + 1) * kBytesM;
   vec8<T> m[2][MT], n[2][NT];
+  int place_m[MT], place_n[NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) place_m[i] = M::place(m0 + 32 * i, lane);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) place_n[j] = N::place(n0 + 32 * j, lane);
   auto fetch = [&](int f, const uint8_t* slot_m, const uint8_t* slot_n, int k) {
     if (f < NT)
-      n[k & 1][f] = N::template fragment<T>(slot_n, n0 + 32 * f, k, lane);
+      n[k & 1][f] = N::template fragment<T>(slot_n, place_n[f], k, lane);
     else
-      m[k & 1][f - NT] = M::template fragment<T>(slot_m, m0 + 32 * (f - NT), k, lane);
+      m[k & 1][f - NT] = M::template fragment<T>(slot_m, place_m[f - NT], k, lane);
   };
   // Part k. Behind its MFMAs, one by one, the next part's fragments and the copies first..last: the matrix
   // cores have work from the first instruction after the barrier on.
@@ -288,6 +299,11 @@ __device__ __forceinline__ void shared_loop(uint8_t* ring, int whole, int stages
   const uint32_t base = lds_address(ring);
 #pragma unroll
   for (int s = 0; s < kAhead - 1; ++s) copy(base + s * kBytes, s, std::false_type());
+  int place_m[MT], place_n[NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) place_m[i] = M::place(32 * i, lane);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) place_n[j] = N::place(32 * j, lane);
   int s = 0, slot = 0, free = (kAhead - 1) * kBytes;
   auto stretch = [&](int to, auto kind) {
     for (; s < to; ++s) {
@@ -295,9 +311,9 @@ __device__ __forceinline__ void shared_loop(uint8_t* ring, int whole, int stages
       lds_barrier();  // stage s has landed, stage s - 1 has been read
       vec8<T> m[MT], n[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) n[j] = N::template fragment<T>(ring + slot + M::kBytes, 32 * j, wave, lane);
+      for (int j = 0; j < NT; ++j) n[j] = N::template fragment<T>(ring + slot + M::kBytes, place_n[j], wave, lane);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) m[i] = M::template fragment<T>(ring + slot, 32 * i, wave, lane);
+      for (int i = 0; i < MT; ++i) m[i] = M::template fragment<T>(ring + slot, place_m[i], wave, lane);
       copy(base + free, s + kAhead - 1, kind);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
