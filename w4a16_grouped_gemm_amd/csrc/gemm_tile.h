@@ -65,6 +65,13 @@ __device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uin
 }
 #pragma clang diagnostic pop
 
+// An address that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const uint8_t* uniform(const void* p) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)at), high = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+  return reinterpret_cast<const uint8_t*>((uint64_t)high << 32 | low);
+}
+
 // Until at most N of this wave's copies are on their way.
 template <int N>
 __device__ __forceinline__ void wait_copies() {
@@ -151,7 +158,7 @@ struct ColumnPanel {
   // those are copies of column 0.
   template <typename T>
   __device__ __forceinline__ void set(const T* from, int32_t ld, int32_t columns, int wave, int lane) {
-    base = reinterpret_cast<const uint8_t*>(from);
+    base = uniform(from);
     stride = (int64_t)ld * kSteps * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {

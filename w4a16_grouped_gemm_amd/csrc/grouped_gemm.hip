@@ -187,7 +187,7 @@ struct Way {
 template <typename T, typename M>
 __device__ __forceinline__ void set_rows(M& m, const GroupedParams& p, int first, int rows, int wave, int lane) {
   const int64_t pitch = (int64_t)p.K * (int)sizeof(T);
-  m.base = static_cast<const uint8_t*>(p.a) + (p.gather ? 0 : first * pitch);
+  m.base = uniform(static_cast<const uint8_t*>(p.a) + (p.gather ? 0 : first * pitch));
   m.far = p.far ? pitch : 0;
 #pragma unroll
   for (int i = 0; i < M::kMine; ++i) {
@@ -204,7 +204,7 @@ __device__ __forceinline__ void set_weights(N& n, const GroupedParams& p, int e,
   if constexpr (TRANSPOSED) {
     n.set(w + n0, p.N, p.N - n0, wave, lane);
   } else {
-    n.base = reinterpret_cast<const uint8_t*>(w + (int64_t)n0 * p.K);
+    n.base = uniform(w + (int64_t)n0 * p.K);
     n.far = 0;
 #pragma unroll
     for (int i = 0; i < N::kMine; ++i)

@@ -199,8 +199,8 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p, int m
       return my_row & 2 ? high : low;
     };
     // of the next stage's first row of the workgroup (GATHER: of token 0), and this lane's 16 bytes from there
-    const uint8_t* base_m = static_cast<const uint8_t*>(p.dout) + begin * row_m + 2 * m0;
-    const uint8_t* base_n = static_cast<const uint8_t*>(p.a) + (GATHER ? 0 : begin * row_n) + 2 * n0;
+    const uint8_t* base_m = uniform(static_cast<const uint8_t*>(p.dout) + begin * row_m + 2 * m0);
+    const uint8_t* base_n = uniform(static_cast<const uint8_t*>(p.a) + (GATHER ? 0 : begin * row_n) + 2 * n0);
     uint32_t offset_m[kMine], offset_n[kMine];
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
