@@ -216,17 +216,20 @@ __device__ __forceinline__ void prologue(const uint8_t* ring, CopyM copy_m, Copy
   }
 }
 
-// All stages of a wave's 32 MT rows by 32 NT columns. copy_m(q, LDS address, stage) makes this wave's copy q of a
+// All stages of a wave's 32 MT rows by 32 NT columns. copy_m(q, LDS address, stage, kind) makes this wave's copy q of a
 // stage's panel M (M::kMine of them), copy_n of N. ring: kAhead + 1 stages of at most
 // kBytesM of M, kAhead of N; prologue has been called for them. All waves are past it on return.
+// kind is true in the first `whole` stages, as long as real() says so before each: copies that need no look at what
+// lies outside the operand, and no vector instruction beside them. (With two compares and a 64-bit address for
+// every copy: 1720 instead of 1670 us for the case below, transposed 1770 instead of 1650.)
 //
 // A stage is multiplied in four parts of 16 steps, a part's fragments being read from LDS while the part before
 // it is multiplied. Before the last part all waves meet: by then every wave has read all of stage s, and stage s + 1
 // has landed. N's slot then takes stage s + kAhead, copied at once so as to land in time; M's slot takes stage
 // s + kAhead + 1, copied in the parts that follow. So the copies, which at 64 bytes a cycle keep the vector cache busy
 // for more than half of a 256 x 256 tile's time, are spread over the stage, and none is waited for less than three
-// parts after its issue. (32768 rows, 16 experts, 4096 x 7168, kAhead 2: 1618 us; both panels in two slots with
-// the copies in one part 1805, in two parts 1732, in all four 1904.) Copies past the last stage are of zeros.
+// parts after its issue. (32768 rows, 16 experts, 4096 x 7168, kAhead 2, on one card: 1618 us; both panels in two slots
+// with the copies in one part 1805, in two parts 1732, in all four 1904.) Copies past the last stage are of zeros.
 // ahead(stage) comes before the first part and turn() after the last, for scalar loads that the copies of the
 // next stage need: while one is on its way every wait for LDS is for all reads and for it, and here that is one
 // wait, a part after its issue (issued where the copies need them, twice a stage, the weights' gradient of
@@ -288,7 +291,7 @@ __device__ __forceinline__ void loop(uint8_t* ring, int whole, int stages, int m
     at_m = next_m;
     at_n = next_n;
   };
-  // (a choice within one loop makes the compiler move all sums about)
+  // two loops: with the choice inside of one the compiler moves all the sums about
   for (; s < whole && real(); ++s) multiply(std::true_type());
   for (; s < stages; ++s) multiply(std::false_type());
   wait_copies<0>();
@@ -297,8 +300,8 @@ __device__ __forceinline__ void loop(uint8_t* ring, int whole, int stages, int m
 
 // All stages of a tile of 32 MT rows by 32 NT columns that the eight waves share along r: of each stage of 128
 // steps wave w multiplies 16, so that a stage costs one barrier and one wait for LDS, where a wave's share of a
-// small tile would wait for LDS in every part. kAhead stages in LDS (copy makes both panels' copies of one).
-// acc: each wave's share of the sums.
+// small tile would wait for LDS in every part. kAhead stages in LDS (copy makes both panels' copies of one, of the
+// whole kind as above in the first `whole` stages where kSome). acc: each wave's share of the sums.
 template <typename T, typename M, typename N, int kAhead, bool kSome, int MT, int NT, typename Copy>
 __device__ __forceinline__ void shared_loop(uint8_t* ring, int whole, int stages, int wave, int lane,
                                             floatx16 (&acc)[MT][NT], Copy copy) {

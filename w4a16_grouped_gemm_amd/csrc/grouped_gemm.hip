@@ -9,11 +9,11 @@
 // and at half of that (128 x 128) the copies alone would take the time of the products. Tiles with at most half
 // of their rows used multiply half.
 //
-// Measured (one MI355X, bf16): 32768 rows on 16 experts, 4096 x 7168: 1580..1720 us by card, 1.1..1.2 PFLOP/s, with
-// transposed weights 1670..1800. The clock is what gives: under this load it falls to 1.6 GHz of 2.4; at 2.4 (timing
-// builds without copies, on LDS that stays as it is) the same loop takes 1170. A tile of 256 x 256 x 64 takes 2500
-// cycles, of which the matrix cores work 2048, transposed 2700. 48 experts of 85 rows, 7168 x 2048: 320..340 us, 4.6
-// TB/s; of three rows, 4096 x 7168: 425..460 us, 6 TB/s (reads alone reach 6.9).
+// Measured (one MI355X, bf16): 32768 rows on 16 experts, 4096 x 7168: 1570..1670 us by card, 1.15..1.23 PFLOP/s, with
+// transposed weights 1560..1650; one expert of 8192 rows, 8192 x 8192: 804 us, 1.37. The clock is what gives: under
+// this load it falls to 1.6 GHz of 2.4 (a timing build without copies, on LDS that stays as it is, keeps 2.4). 48 experts
+// of 85 rows, 7168 x 2048: 320..340 us, 4.6 TB/s; of three rows, 4096 x 7168: 420..450 us, 6.1 TB/s (reads
+// alone reach 6.9); one token on 8 of 64 experts, 512 x 7168: 12.3 us, 4.8 TB/s.
 #include "gemm_tile.h"
 #include "grouped_gemm.h"
 #include "row_ops.h"
@@ -381,11 +381,11 @@ hipError_t launch_narrow(const GroupedParams& p, hipStream_t stream) {
 // as n_slots over E, their mean where every routed expert is resident; on a slice of the experts that counts
 // the others' slots too, and larger tiles may be taken than the slice's rows fill. Results do not
 // depend on the way but for the order of their sums. Measured, us by (256 x 256, 128 x 128, 64 x 128, 32 x 64) tiles,
-// bf16, K last: one expert of 4096 rows, 4096 x 4096: 110, 141, 190, 351; 8 experts of 256, 2048 x 2048: 56, 35,
-// 40, 59; 48 of 85, 7168 x 2048: 325, 374, 435, 899; one of 512 rows, 2048 x 2048: 44, 21, 19, 14; 10 of 100, 1384 x 1000
-// transposed: 24, 17.5, 17.3, 22; 384 of 11, 512 x 7168: 489, 475, 475, 478, and 7168 x 512 transposed: 689, 634, 627, 821;
-// 48 of 3 (384 routed), 4096 x 7168: 464, 463, 464, 454, and 7168 x 4096 transposed 509, 483, 482, 498; 8 experts of one
-// row, 512 x 7168: 79, 42, 42, 19, and by 32 x 32 tiles 12.5 (of 512 rows above: 20).
+// bf16, K last: one expert of 4096 rows, 4096 x 4096: 110, 141, 190, 351; 8 experts of 256, 2048 x 2048: 56, 33,
+// 40, 59; 48 of 85, 7168 x 2048: 320, 374, 435, 899; one of 512 rows, 2048 x 2048: 44, 21, 19, 12.5; 10 of 100, 1384 x 1000
+// transposed: 24, 15.7, 17.3, 22; 384 of 11, 512 x 7168: 489, 475, 475, 477, and 7168 x 512 transposed: 689, 634, 619, 821;
+// 48 of 3 (384 routed), 4096 x 7168: 464, 463, 464, 451, and 7168 x 4096 transposed 509, 483, 481, 498; 8 experts of one
+// row, 512 x 7168: 79, 42, 42, 19, and by 32 x 32 tiles 10.5 (of 512 rows above: 20).
 template <typename T, typename O, bool TRANSPOSED>
 hipError_t launch(const GroupedParams& p, hipStream_t stream) {
   const int64_t experts = std::min(p.E, p.n_slots), rows = (p.n_slots + experts - 1) / experts;

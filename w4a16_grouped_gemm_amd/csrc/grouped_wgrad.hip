@@ -7,9 +7,10 @@
 // are column panels: the rows are the steps of the sum. Rows without a slot, whatever they
 // hold, are replaced by zeros as they are copied to LDS (global_load_lds); the mfma loop is in gemm_tile.h.
 //
-// Measured (one MI355X): 32768 rows, 16 experts, 4096 x 7168: 1800 us, to fp32 1840, 1.05 PFLOP/s, as far as
-// the product itself bound by the clock that such a load leaves (1.66 GHz of 2.4); 131072 rows 6170 us, 1.25 PFLOP/s:
-// a tile's start and its store, 128 or 256 KB, take as long as five or six stages.
+// Measured (one MI355X): 32768 rows, 16 experts, 4096 x 7168: 1690..1770 us, to fp32 50 more, 1.1 PFLOP/s; 131072 rows
+// 6130..6290 us, 1.25. Bound as the product by the clock that the load leaves, and by a tile's start and its
+// store, 128 or 256 KB, which take as long as four or five of its 32 stages. 4 experts of 1388 rows, 264 x 712: 14.7
+// us, a chain of a dozen dependent steps.
 #include "gemm_tile.h"
 #include "grouped_gemm.h"
 #include "row_ops.h"
