@@ -58,7 +58,10 @@ static __device__ __attribute__((aligned(16))) const uint32_t kZeros[128] = {};
 __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory", "m0");
 }
-// The same from base + offset (bytes): no vector instruction but the copy.
+// The same from base + offset (bytes): no vector instruction but the copy. A vector instruction that writes a scalar
+// register (a readlane of one that was set aside in a vector register, for instance) must lie five wait states before a
+// memory instruction that reads it, and the compiler does not look into the asm. There is none near any copy (the tests
+// look); three more wait states here would cost 1% of a large product.
 __device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds)
                : "memory", "m0");
@@ -68,7 +71,8 @@ __device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uin
 // An address that is the same in all lanes, in scalar registers.
 __device__ __forceinline__ const uint8_t* uniform(const void* p) {
   const uint64_t at = reinterpret_cast<uint64_t>(p);
-  const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)at), high = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+  const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)at);
+  const uint32_t high = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
   return reinterpret_cast<const uint8_t*>((uint64_t)high << 32 | low);
 }
 
@@ -101,7 +105,9 @@ struct RowPanel {
 
   // where there are fewer copies than waves, two waves make the same one
   static __device__ __forceinline__ int unit_of(int i, int wave) { return (kMine * wave + i) % kUnits; }
-  static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 64 / kLanes * unit_of(i, wave) + lane / kLanes; }
+  static __device__ __forceinline__ int row_of(int i, int wave, int lane) {
+    return 64 / kLanes * unit_of(i, wave) + lane / kLanes;
+  }
   static __device__ __forceinline__ int swizzle(int row) { return kSteps == 64 ? row >> 1 & 7 : row & 15; }
   // this lane's first step of r in copy i
   static __device__ __forceinline__ int first_of(int i, int wave, int lane) {
@@ -115,7 +121,9 @@ struct RowPanel {
   // to `on` stages on
   __device__ __forceinline__ void go(int on) { base += (int64_t)on * kPitch; }
   // copy i of a stage that lies in the operand as a whole, where nothing is far
-  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) const { copy16(base, offset[i], lds + 1024 * unit_of(i, wave)); }
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) const {
+    copy16(base, offset[i], lds + 1024 * unit_of(i, wave));
+  }
   // copy i of any stage, of which `left` steps are in the operand
   __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave, int lane) const {
     const int first = first_of(i, wave, lane);
@@ -167,9 +175,12 @@ struct ColumnPanel {
     }
   }
   __device__ __forceinline__ void go(int on) { base += on * stride; }
-  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) const { copy16(base, offset[i], lds + 1024 * unit_of(i, wave)); }
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) const {
+    copy16(base, offset[i], lds + 1024 * unit_of(i, wave));
+  }
   __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave, int lane) const {
-    copy16(left > first_of(i, wave, lane) ? (const void*)(base + offset[i]) : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
+    const bool inside = left > first_of(i, wave, lane);
+    copy16(inside ? (const void*)(base + offset[i]) : (const void*)kZeros, lds + 1024 * unit_of(i, wave));
   }
   // As RowPanel's, by two transposing reads: sixteen lanes read four steps of sixteen columns,
   // lane i the columns 4 (i % 4) + 0..3 of step i / 4, and get column i's four steps.
@@ -236,8 +247,8 @@ __device__ __forceinline__ void prologue(const uint8_t* ring, CopyM copy_m, Copy
 // 32768 rows, 16 experts, 4096 x 7168 took 1894 instead of 1800 us).
 template <typename T, typename M, typename N, int kAhead, int kBytesM, int MT, int NT, typename CopyM, typename CopyN,
           typename Real, typename Ahead, typename Turn>
-__device__ __forceinline__ void loop(uint8_t* ring, int whole, int stages, int m0, int n0, int lane, floatx16 (&acc)[MT][NT],
-                                     CopyM copy_m, CopyN copy_n, Real real, Ahead ahead, Turn turn) {
+__device__ __forceinline__ void loop(uint8_t* ring, int whole, int stages, int m0, int n0, int lane,
+                                     floatx16 (&acc)[MT][NT], CopyM copy_m, CopyN copy_n, Real real, Ahead ahead, Turn turn) {
   static_assert(kAhead >= 2, "a stage is read while the next one lands");
   constexpr int kMfmas = MT * NT, kFragments = MT + NT;
   uint8_t* const ring_n = ring + (kAhead + 1) * kBytesM;
@@ -394,7 +405,8 @@ __device__ __forceinline__ void drain(uint8_t* scratch, int m0, int n0, int wave
         if constexpr (sizeof(O) == 4) {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            write(2 * g + half, __builtin_bit_cast(u32x4, floatx4{sums[4 * g], sums[4 * g + 1], sums[4 * g + 2], sums[4 * g + 3]}));
+            write(2 * g + half, __builtin_bit_cast(u32x4, floatx4{sums[4 * g], sums[4 * g + 1], sums[4 * g + 2],
+                                                                  sums[4 * g + 3]}));
         } else {
 #pragma unroll
           for (int g = 0; g < 4; g += 2) {

@@ -161,7 +161,9 @@ template <bool ON>
 struct Turn {
   int K, stages, start;
   __device__ __forceinline__ Turn(int K_, int e)
-      : K(K_), stages((K_ + kStep - 1) / kStep), start(ON && K_ % kStep == 0 ? (int)(3u * (unsigned)e % (unsigned)stages) : 0) {}
+      : K(K_),
+        stages((K_ + kStep - 1) / kStep),
+        start(ON && K_ % kStep == 0 ? (int)(3u * (unsigned)e % (unsigned)stages) : 0) {}
   __device__ __forceinline__ int at(int stage) const {
     const int s = stage + start;
     return s < stages ? s : s - stages;
@@ -320,12 +322,16 @@ __global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, Cut c
         const int left = p.K - stage * kSteps;
 #pragma unroll
         for (int i = 0; i < M::kMine; ++i)
-          if constexpr (kind) m.copy(i, slot, wave);
-          else m.copy(i, slot, left, wave, lane);
+          if constexpr (kind)
+            m.copy(i, slot, wave);
+          else
+            m.copy(i, slot, left, wave, lane);
 #pragma unroll
         for (int i = 0; i < N::kMine; ++i)
-          if constexpr (kind) n.copy(i, slot + M::kBytes, wave);
-          else n.copy(i, slot + M::kBytes, left, wave, lane);
+          if constexpr (kind)
+            n.copy(i, slot + M::kBytes, wave);
+          else
+            n.copy(i, slot + M::kBytes, left, wave, lane);
         m.go(1);
         n.go(1);
       });

@@ -125,11 +125,13 @@ __global__ __launch_bounds__(kThreads) void narrow_wgrad_kernel(WgradParams p, i
     for (int q = 0; q < 2; ++q) {
       const int row = 16 * wave + 8 * q + my_row;
       const int column = 8 * (lane % Panel::kLanes ^ (Panel::swizzle(row) << 2));
-      at_m[q] = static_cast<const uint8_t*>(p.dout) + (int64_t)(base + row) * row_m + 2 * (m0 + (column < p.N - m0 ? column : 0));
+      at_m[q] = static_cast<const uint8_t*>(p.dout) + (int64_t)(base + row) * row_m +
+                2 * (m0 + (column < p.N - m0 ? column : 0));
       at_n[q] = static_cast<const uint8_t*>(p.a) + 2 * (n0 + (column < p.K - n0 ? column : 0));
       from[q] = table[row];
     }
-    shared_loop<T, Panel, Panel, kAhead, false>(ring, 0, stages, wave, lane, acc, [&](uint32_t lds, int stage, std::false_type) {
+    shared_loop<T, Panel, Panel, kAhead, false>(ring, 0, stages, wave, lane, acc,
+                                                [&](uint32_t lds, int stage, std::false_type) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const bool real = from[q] >= 0;
@@ -254,7 +256,8 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p, int m
     if (m0 + n >= p.N || n0 + k >= p.K) return;
     O* dw = static_cast<O*>(p.dw) + ((int64_t)e * p.N + m0 + n) * p.K + n0 + k;
     if constexpr (sizeof(O) == 4) {
-      if (p.accumulate) v = __builtin_bit_cast(u32x4, __builtin_bit_cast(floatx4, v) + *reinterpret_cast<const floatx4*>(dw));
+      if (p.accumulate)
+        v = __builtin_bit_cast(u32x4, __builtin_bit_cast(floatx4, v) + *reinterpret_cast<const floatx4*>(dw));
     }
     Line<O>::store(dw, v);
   });

@@ -7,9 +7,10 @@
 // format's largest, or below, so no value saturates; dividing by it is exact,
 // and the conversion (nearest, ties to even) is the only rounding.
 //
-// All of it is bound by memory: each value is read and written once, in streams of 8 or 16 bytes a lane. Measured (one MI355X, bf16): 16384 rows of 7168 quantised in 56 us
-// and back in 57 (6.3 TB/s; reads alone reach 6.9, a copy 4.9); the activation of 32768 rows of 2 x 2048 88 us (6.1 TB/s),
-// its gradient 109 (6.2 TB/s); a few rows 3 us, a launch's own time.
+// All of it is bound by memory: each value is read and written once, in streams of 8 or 16 bytes a lane.
+// Measured (one MI355X, bf16): 16384 rows of 7168 quantised in 56 us and back in 57 (6.3 TB/s; reads alone reach
+// 6.9, a copy 4.9); the activation of 32768 rows of 2 x 2048 88 us (6.1 TB/s), its gradient 109 (6.2 TB/s); a few rows
+// 3 us, a launch's own time.
 #include "row_ops.h"
 #include "rows.h"
 
