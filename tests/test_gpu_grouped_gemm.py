@@ -249,6 +249,19 @@ def test_many_blocks(N, blocks):
     assert torch.equal(dw.cpu().double(), weight_gradient(r, dout, a, E, True)[0])
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("K", [8, 64, 128, 192, 256, 320, 328, 1024])
+def test_many_experts_of_few_rows(K, gather):
+    """Tiles that begin K at a stage of their expert's: numbers of stages below and above what is copied ahead."""
+    T, topk, E, N, bm = 1800, 2, 60, 304, 64
+    g = torch.Generator().manual_seed(28)
+    r = Routing(T, topk, E, E, bm, seed=29)
+    a, weights = whole(g, T if gather else r.capacity, K), whole(g, E, N, K)
+    out = run(r, a.bfloat16().cuda(), weights.bfloat16().cuda(), torch.float32, gather, False)
+    assert torch.equal(out[: r.rows].cpu().double(), product(r, a, weights, gather, False)[0])
+    assert bool((out[r.rows :] == POISON).all())
+
+
 @pytest.mark.parametrize("T", [0, 4])
 def test_no_rows(T):
     """No tokens, and tokens without a resident expert: zeros, or what was there with accumulate; no row written."""
@@ -323,6 +336,22 @@ def test_rows_past_32_bits(bm):
     ref, _ = weight_gradient(r, dout, part, E, True)
     dw = run_wgrad(r, dout.bfloat16().cuda(), a, E, torch.float32, True)
     assert torch.equal(dw[:, :, at.cuda()].cpu().double(), ref) and int((dw != 0).any(0).any(0).sum()) <= at.numel()
+
+
+@pytest.mark.parametrize("E, N", [(64, 8), (3, 904), (2, 4096)])
+def test_token_rows_past_32_bits_at_each_tile(E, N):
+    """The same gathered rows by the small tiles, the ones of 128 rows, and those of 256 with a shorter last one."""
+    K, T, bm = 1 << 20, 2100, 16
+    r = Routing(T, 1, E, E, bm, seed=26)
+    g = torch.Generator().manual_seed(27)
+    a = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")  # 4.4 GB
+    weights = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    at = torch.randint(0, K, (24,), generator=g).unique()
+    part, wpart = whole(g, T, at.numel()), whole(g, E, N, at.numel())
+    a[:, at.cuda()], weights[:, :, at.cuda()] = part.bfloat16().cuda(), wpart.bfloat16().cuda()
+    ref, _ = product(r, part, wpart, True, False)
+    out = run(r, a, weights, torch.float32, True, False)
+    assert torch.equal(out[: r.rows].cpu().double(), ref)
 
 
 def _case(T=300, topk=2, E=4, N=264, K=328, bm=64, seed=15):
