@@ -250,6 +250,37 @@ def test_many_blocks(N, blocks):
 
 
 @pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("shape", [(8, 1024, 1024), (4, 512, 768), (2, 136, 264)], ids=str)
+def test_padding_anywhere(shape, gather):
+    """Rows without a slot between real ones, NaN in them, at each tile size of the weights' gradient: a few blocks whole, then
+    one hole in a wave's eight rows, then many."""
+    E, N, K = shape
+    T, bm = 400 * E, 128
+    g = torch.Generator().manual_seed(30)
+    r = Routing(T, 1, E, E, bm, seed=31)
+    slots = r.sorted[: r.rows].cpu()
+    hole = (torch.rand(r.rows, generator=g) < 0.2) & (torch.arange(r.rows) % 384 >= 256)
+    hole[torch.arange(0, r.rows, 389)] = True
+    slots[hole] = r.n + 5
+    r.sorted[: r.rows] = slots.cuda()
+    r.live = torch.nonzero(slots < r.n).flatten()
+    r.token = slots[r.live].long()
+    r.expert = r.expert_ids.cpu()[r.live // bm].long()
+    a, dout = whole(g, T if gather else r.capacity, K), whole(g, r.capacity, N)
+    pad = torch.ones(r.capacity, dtype=torch.bool)
+    pad[r.live] = False
+    a16, d16 = a.bfloat16(), dout.bfloat16()
+    d16[pad] = float("nan")
+    if not gather:
+        a16[pad] = float("inf")
+    dw = run_wgrad(r, d16.cuda(), a16.cuda(), E, torch.float32, gather)
+    assert torch.equal(dw.cpu().double(), weight_gradient(r, dout, a, E, gather)[0])
+    weights = whole(g, E, N, K)
+    out = run(r, a16.cuda(), weights.bfloat16().cuda(), torch.float32, gather, False)
+    assert torch.equal(out[: r.rows].cpu().double(), product(r, a, weights, gather, False)[0])
+
+
+@pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("K", [8, 64, 128, 192, 256, 320, 328, 1024])
 def test_many_experts_of_few_rows(K, gather):
     """Tiles that begin K at a stage of their expert's: numbers of stages below and above what is copied ahead."""
