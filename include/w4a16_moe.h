@@ -676,8 +676,8 @@ int mxfp8_dequantize(const uint8_t* q, const uint8_t* s, int32_t rows, int32_t K
 /* The activation between the expert layer's two products, keeping its input in 8 bits:
  *   h[r, c] = silu(gu[r, c]) * gu[r, I + c]   in fp32, rounded once to `dtype`,
  * silu(g) = g / (1 + exp(-g)), and gu quantised as mxfp8_quantize does. h is of the
- * values as given, not of the quantised ones. Where exp(-|g|) is below 2^-126 it counts as
- * zero; g = -infinity gives NaN.
+ * values as given, not of the quantised ones. It holds to a few units of fp32's last place at any size of the factors
+ * (an fp32 gate below 2^-125 counts to 2^-150); g = -infinity gives NaN.
  *   gu                device [rows, 2 I] of `dtype`; I a multiple of 32
  *   h                 device [rows, I] of `dtype`
  *   q, s              device uint8 [rows, 2 I] and [rows, I / 16]: the checkpoint */
@@ -689,7 +689,8 @@ int mxfp8_silu_mul(const void* gu, int32_t dtype, int32_t rows, int32_t I, const
  *   dgu[r, c]     = dh[r, c] * u * y * (1 + g * (1 - y)),
  *   dgu[r, I + c] = dh[r, c] * g * y,
  *   h[r, c]       = g * y * u, the activation again (for the second product's weight gradient),
- * in fp32, each rounded once to `dtype`.
+ * in fp32, each rounded once to `dtype`, held as mxfp8_silu_mul's h is (dgu[r, c] relative to its terms' sizes: 1 and
+ * g * (1 - y) cancel near g = -1.28).
  *   dh                device [rows, I] of `dtype`
  *   dgu               device [rows, 2 I] of `dtype`
  *   h                 device [rows, I] of `dtype`, or NULL where it is not wanted

@@ -9,12 +9,14 @@
 //
 // All of it is bound by memory: each value is read and written once, in streams of 8 or 16 bytes a lane.
 // Measured (one MI355X, bf16): 16384 rows of 7168 quantised in 56 us and back in 57 (6.3 TB/s; reads alone reach
-// 6.9, a copy 4.9); the activation of 32768 rows of 2 x 2048 88 us (6.1 TB/s), its gradient 109 (6.2 TB/s); a few rows
-// 3 us, a launch's own time.
+// 6.9, a copy 4.9); the activation of 32768 rows of 2 x 2048 88 us (6.1 TB/s), its gradient 104 (6.5 TB/s), 98 and 119
+// where every wave has a gate so far out that the products go by mantissas and exponents; a few rows 3 us, a
+// launch's own time.
 #include "row_ops.h"
 #include "rows.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace w4a16 {
 namespace {
@@ -36,6 +38,7 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 struct Codes {
   uint32_t v[2];  // eight codes
   uint32_t scale;
+  uint32_t most;  // the block's largest magnitude, as bits
 };
 
 // Eight values of a lane's quarter block -> their codes and the block's scale byte. Magnitudes
@@ -61,6 +64,7 @@ __device__ __forceinline__ Codes encode8(const float (&x)[8]) {
     c.v[i] = (uint32_t)word;
   }
   c.scale = finite ? (uint32_t)byte : 255u;
+  c.most = most;
   return c;
 }
 
@@ -81,21 +85,70 @@ __device__ __forceinline__ void decode8(const uint32_t (&code)[2], float scale, 
   }
 }
 
-// 1 / (1 + exp(-g)) and 1 less that, neither by a difference: with t = exp(-|g|) they are
-// 1 / (1 + t) and t / (1 + t). exp(-|g|) = 2^(-|g| log2 e) with the product's rounding error
-// and the constant's put back, so that it holds to a few units in the last place at any g.
-__device__ __forceinline__ void sigmoid(float g, float& sig, float& rest) {
-  constexpr float kLog2E = 1.44269504f, kLow = 1.92596299e-8f;
-  const float x = fmaxf(-fabsf(g), -200.f);  // exp(-200) is 0; keeps an infinity out of the differences
-  const float hi = x * kLog2E;
-  const float lo = __builtin_fmaf(x, kLow, __builtin_fmaf(x, kLog2E, -hi));
-  const float t = __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, 0.693147181f, 1.f);
-  const float d = 1.f + t;
-  float inverse = __builtin_amdgcn_rcpf(d);
-  inverse = __builtin_fmaf(__builtin_fmaf(-d, inverse, 1.f), inverse, inverse);
+constexpr float kLog2E = 1.44269504f, kLog2ELow = 1.92596299e-8f;
+
+// 1 / d, with the instruction's error taken out by one step of Newton's.
+__device__ __forceinline__ float reciprocal(float d) {
+  const float r = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+}
+
+// 1 / (1 + exp(-g)), as sig * 2^power, and 1 less that, neither by a difference: with t = exp(-|g|) they are
+// 1 / (1 + t) and t / (1 + t). t = 2^(-|g| log2 e) is 2^whole times m = 2^part, the part with the product's rounding
+// error and the constant's put back, so that m holds to a few units in the last place at any g.
+// FAR: any g. t leaves fp32's numbers at |g| = 87, and products with it come back into them where the other factors are
+// large. From |g| = 400 on t is zero: below 2^-577, no product of a gate and two more fp32 values with it rounds to
+// anything else. Else |g| is up to 87, and power is 0.
+template <bool FAR>
+__device__ __forceinline__ void sigmoid(float g, float& sig, int& power, float& rest) {
+  const float x = FAR ? fmaxf(-fabsf(g), -400.f) : -fabsf(g);
+  const float whole = __builtin_rintf(x * kLog2E);
+  const float part = __builtin_fmaf(x, kLog2ELow, __builtin_fmaf(x, kLog2E, -whole));  // within 0.51: good to 2^-25
+  float m = __builtin_amdgcn_exp2f(part);
+  if (FAR) m = x > -400.f ? m : 0.f;
+  const float t = __builtin_amdgcn_ldexpf(m, (int)whole);
+  const float inverse = reciprocal(1.f + t);
   const float small = t * inverse;
-  sig = g < 0.f ? small : inverse;
+  sig = g < 0.f ? (FAR ? m * inverse : small) : inverse;
+  power = FAR && g < 0.f ? (int)whole : 0;
   rest = g < 0.f ? inverse : small;
+}
+
+// x = mantissa * 2^power. FAR: the mantissa in [0.5, 1), so that the only step that can leave fp32's numbers is the
+// product's last, and the bits are those of the plain product where that does not leave them.
+struct Parts {
+  float mantissa;
+  int power;
+};
+template <bool FAR>
+__device__ __forceinline__ Parts parts(float x) {
+  return FAR ? Parts{__builtin_amdgcn_frexp_mantf(x), __builtin_amdgcn_frexp_expf(x)} : Parts{x, 0};
+}
+template <bool FAR>
+__device__ __forceinline__ float times_power(float x, int power) {
+  return FAR ? __builtin_amdgcn_ldexpf(x, power) : x;
+}
+
+template <bool FAR>
+__device__ __forceinline__ float silu_mul(float gate, float up) {
+  float sig, rest;
+  int power;
+  sigmoid<FAR>(gate, sig, power, rest);
+  const Parts g = parts<FAR>(gate), u = parts<FAR>(up);
+  return times_power<FAR>(g.mantissa * sig * u.mantissa, g.power + u.power + power);
+}
+
+// dgate = dh up sig (1 + gate (1 - sig)), dup = dh gate sig, h = gate sig up
+template <bool FAR>
+__device__ __forceinline__ void gradient(float gate, float up, float dh, float& dgate, float& dup, float& h) {
+  float sig, rest;
+  int power;
+  sigmoid<FAR>(gate, sig, power, rest);
+  const Parts g = parts<FAR>(gate), u = parts<FAR>(up), d = parts<FAR>(dh);
+  const float silu = g.mantissa * sig, slope = sig * __builtin_fmaf(gate, rest, 1.f);
+  dgate = times_power<FAR>(d.mantissa * u.mantissa * slope, d.power + u.power + power);
+  dup = times_power<FAR>(d.mantissa * silu, d.power + g.power + power);
+  h = times_power<FAR>(silu * u.mantissa, g.power + u.power + power);
 }
 
 __device__ __forceinline__ int64_t live_rows(int32_t rows, const int32_t* num_rows) {
@@ -191,17 +244,21 @@ __global__ __launch_bounds__(kThreads) void silu_mul_kernel(const T* gu, int32_t
     const int64_t gate_at = 2 * at.row * I + at.column, up_at = gate_at + I;
     const Eight<T> a = load8<kStreamed>(gu + gate_at), b = load8<kStreamed>(gu + up_at);
     float gate[8], up[8];
-    Eight<T> r;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       gate[i] = (float)a.v[i];
       up[i] = (float)b.v[i];
-      float sig, rest;
-      sigmoid(gate[i], sig, rest);
-      r.v[i] = (T)(gate[i] * sig * up[i]);
+    }
+    const Codes cg = encode8(gate), cu = encode8(up);
+    Eight<T> r;
+    if (!__any(cg.most > __float_as_uint(87.f))) {  // by the wave: some lanes one way and some the other take both ways' time
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.v[i] = (T)silu_mul<false>(gate[i], up[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.v[i] = (T)silu_mul<true>(gate[i], up[i]);
     }
     store8<kStreamed>(h + at.row * I + at.column, r);
-    const Codes cg = encode8(gate), cu = encode8(up);
     store_codes(q, gate_at, cg);
     store_codes(q, up_at, cu);
     if ((g & 3) == 0) {
@@ -229,19 +286,31 @@ __global__ __launch_bounds__(kThreads) void silu_mul_backward_kernel(const uint8
     float gate[8], up[8];
     decode8(gate_code, scale_of(gate_scale), gate);
     decode8(up_code, scale_of(up_scale), up);
-    Eight<T> dg, du, again;
+    uint32_t most = 0;  // of dh, as bits
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float sig, rest;
-      sigmoid(gate[i], sig, rest);
-      const float silu = gate[i] * sig, grad = (float)d.v[i];
-      dg.v[i] = (T)(grad * up[i] * __builtin_fmaf(silu, rest, sig));
-      du.v[i] = (T)(grad * silu);
-      again.v[i] = (T)(silu * up[i]);
-    }
-    store8<kStreamed>(dgu + gate_at, dg);
-    store8<kStreamed>(dgu + up_at, du);
-    if (h) store8<kStreamed>(h + at.row * I + at.column, again);
+    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint((float)d.v[i]) & 0x7FFFFFFFu);
+    // |gate| up to 448 / 8, |up| and |dh| below 2^63: no product leaves fp32's numbers before the result does
+    const bool far = gate_scale > 127 - 3 || up_scale > 127 + 54 || most >= __float_as_uint(0x1p63f);
+    auto each = [&](auto kind) {
+      Eight<T> dg, du, again;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float dgate, dup, h_again;
+        gradient<kind>(gate[i], up[i], (float)d.v[i], dgate, dup, h_again);
+        dg.v[i] = (T)dgate;
+        du.v[i] = (T)dup;
+        again.v[i] = (T)h_again;
+      }
+      // a line's parts are stored together (32768 rows of 2 x 2048 far gates, fp32: 228 us instead of 368)
+      if (kind) __builtin_amdgcn_sched_barrier(0);
+      store8<kStreamed>(dgu + gate_at, dg);
+      store8<kStreamed>(dgu + up_at, du);
+      if (h) store8<kStreamed>(h + at.row * I + at.column, again);
+    };
+    if (!__any(far))
+      each(std::false_type());
+    else
+      each(std::true_type());
   }
 }
 
