@@ -1,0 +1,66 @@
+"""Inline-asm LDS copies from a scalar base, in the gfx950 assembly of every kernel source.
+
+A memory instruction needs five wait states after a vector instruction that wrote a scalar register it reads, and the
+compiler keeps no such distance to inline asm. So each of these copies has to read its base from registers that a scalar
+instruction of its own asm block wrote, whatever the compiler puts before the block. Runs on the CPU; skipped where
+hipcc is absent.
+"""
+import os
+import re
+
+from test_isa_hazards import _device_asm, needs_hipcc
+from w4a16_grouped_gemm_amd import build
+
+_COPY = re.compile(r"global_load_lds_\w+ v\d+, (s\[\d+:\d+\]|vcc)")
+
+
+def asm_blocks(asm: str):
+    """The instructions of each inline-asm block, a list a block."""
+    blocks, cur = [], None
+    for line in asm.splitlines():
+        if "#ASMSTART" in line:
+            cur = []
+        elif "#ASMEND" in line:
+            blocks.append(cur)
+            cur = None
+        elif cur is not None:
+            s = line.split(";")[0].strip()
+            if s:
+                cur.append(s)
+    return blocks
+
+
+def bases_from_outside(asm: str):
+    """The blocks with a copy whose scalar base no scalar instruction of the block wrote; and how many such copies there are."""
+    bad, copies = [], 0
+    for block in asm_blocks(asm):
+        for i, inst in enumerate(block):
+            m = _COPY.match(inst)
+            if m:
+                copies += 1
+                if not any(re.match(rf"s_\w+ {re.escape(m.group(1))}(,|$)", b) for b in block[:i]):
+                    bad.append(block)
+    return bad, copies
+
+
+def sources_asm(tmp_path):
+    return {os.path.basename(s): a for s, a in _device_asm(build.sources(), tmp_path).items()}
+
+
+def test_scanner_flags_a_base_from_outside():
+    block = "k:\n\tv_readlane_b32 s11, v40, 3\n\t;;#ASMSTART\n\ts_mov_b32 m0, s4\n\t{}\n\tglobal_load_lds_dwordx4 v2, s[10:11]\n\t;;#ASMEND\n"
+    assert len(bases_from_outside(block.format("s_nop 0"))[0]) == 1
+    assert len(bases_from_outside(block.format("s_mov_b64 s[12:13], s[6:7]"))[0]) == 1
+    assert len(bases_from_outside(block.format("v_readlane_b32 s[10:11], v3, 1"))[0]) == 1
+    assert bases_from_outside(block.format("s_mov_b64 s[10:11], s[6:7]")) == ([], 1)
+    assert bases_from_outside("k:\n\tglobal_load_lds_dwordx4 v2, s[10:11]\n") == ([], 0)  # the compiler's own
+
+
+@needs_hipcc
+def test_copies_read_bases_that_their_own_block_wrote(tmp_path):
+    bad, copies = [], {}
+    for src, asm in sources_asm(tmp_path).items():
+        found, copies[src] = bases_from_outside(asm)
+        bad += [(src, b) for b in found]
+    assert copies["grouped_gemm.hip"] > 0 and copies["grouped_wgrad.hip"] > 0
+    assert not bad, f"{len(bad)} copies, e.g. {bad[:3]}"

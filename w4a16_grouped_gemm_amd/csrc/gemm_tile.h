@@ -60,10 +60,13 @@ __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
 }
 // The same from base + offset (bytes): no vector instruction but the copy. A vector instruction that writes a scalar
 // register (a readlane of one that was set aside in a vector register, for instance) must lie five wait states before a
-// memory instruction that reads it, and the compiler does not look into the asm. There is none near any copy (the tests
-// look); three more wait states here would cost 1% of a large product.
-__device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds)
+// memory instruction that reads it, and the compiler does not look into the asm. So a scalar instruction of the block
+// writes the base anew, as it is: scalar instructions wait by themselves for what they read, and memory instructions for
+// what those write. It is M0's wait state too.
+__device__ __forceinline__ void copy16(const uint8_t*& base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_mov_b64 %0, %0\n\tglobal_load_lds_dwordx4 %1, %0"
+               : "+s"(base)
+               : "v"(offset), "s"(lds)
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
@@ -121,7 +124,7 @@ struct RowPanel {
   // to `on` stages on
   __device__ __forceinline__ void go(int on) { base += (int64_t)on * kPitch; }
   // copy i of a stage that lies in the operand as a whole, where nothing is far
-  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) const {
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) {
     copy16(base, offset[i], lds + 1024 * unit_of(i, wave));
   }
   // copy i of any stage, of which `left` steps are in the operand
@@ -175,7 +178,7 @@ struct ColumnPanel {
     }
   }
   __device__ __forceinline__ void go(int on) { base += on * stride; }
-  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) const {
+  __device__ __forceinline__ void copy(int i, uint32_t lds, int wave) {
     copy16(base, offset[i], lds + 1024 * unit_of(i, wave));
   }
   __device__ __forceinline__ void copy(int i, uint32_t lds, int left, int wave, int lane) const {
