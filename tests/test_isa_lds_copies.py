@@ -1,13 +1,15 @@
-"""Inline-asm LDS copies from a scalar base, in the gfx950 assembly of every kernel source.
+"""Inline-asm LDS copies from a scalar base, and the scans for wait states, in the gfx950 assembly of every kernel source.
 
 A memory instruction needs five wait states after a vector instruction that wrote a scalar register it reads, and the
 compiler keeps no such distance to inline asm. So each of these copies has to read its base from registers that a scalar
-instruction of its own asm block wrote, whatever the compiler puts before the block. Runs on the CPU; skipped where
-hipcc is absent.
+instruction of its own asm block wrote, whatever the compiler puts before the block. What a source includes holds copies and MFMAs too, so the scans look at
+every source's assembly, not at the words in its text. Runs on the CPU; skipped where hipcc is absent.
 """
 import os
 import re
 
+import test_isa_hazards as hazards
+import test_isa_scalar_bases as scalar_bases
 from test_isa_hazards import _device_asm, needs_hipcc
 from w4a16_grouped_gemm_amd import build
 
@@ -64,3 +66,27 @@ def test_copies_read_bases_that_their_own_block_wrote(tmp_path):
         bad += [(src, b) for b in found]
     assert copies["grouped_gemm.hip"] > 0 and copies["grouped_wgrad.hip"] > 0
     assert not bad, f"{len(bad)} copies, e.g. {bad[:3]}"
+
+
+PRODUCTS = {"grouped_gemm.hip", "grouped_wgrad.hip"}  # their copies and MFMAs are in a header that both include
+
+
+@needs_hipcc
+def test_wait_states_in_every_source(tmp_path):
+    """Scalar writes of M0 and vector writes of bases before copies, vector writes before MFMAs."""
+    with_copies, with_scalar_bases, with_mfma, bad = set(), set(), set(), []
+    for src, asm in sources_asm(tmp_path).items():
+        if "global_load_lds" in asm:
+            with_copies.add(src)
+            bad += [(src, "M0") + h for h in hazards.m0_too_close(asm)]
+        found, copies = scalar_bases.short_distances(asm)
+        if copies:
+            with_scalar_bases.add(src)
+            bad += [(src, "base") + h for h in found]
+        if "v_mfma" in asm:
+            with_mfma.add(src)
+            bad += [(src, "MFMA") + h for h in hazards.short_distances(asm)]
+    assert PRODUCTS <= with_copies and PRODUCTS <= with_scalar_bases and PRODUCTS <= with_mfma
+    assert {"moe_gemm_tiled.hip", "moe_gemm_stream.hip"} <= with_copies
+    assert {"moe_gemm.hip", "moe_gemm_stream.hip", "moe_gemm_tiled.hip", "mxfp4_gemm.hip"} <= with_mfma
+    assert not bad, f"{len(bad)}, e.g. {bad[:5]}"
