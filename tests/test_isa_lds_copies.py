@@ -90,3 +90,43 @@ def test_wait_states_in_every_source(tmp_path):
     assert {"moe_gemm_tiled.hip", "moe_gemm_stream.hip"} <= with_copies
     assert {"moe_gemm.hip", "moe_gemm_stream.hip", "moe_gemm_tiled.hip", "mxfp4_gemm.hip"} <= with_mfma
     assert not bad, f"{len(bad)}, e.g. {bad[:5]}"
+
+
+_FUNCTION = re.compile(r"^([\w$.]+):")
+
+
+def unordered_exchanges(asm: str):
+    """(function, first, second): LDS reads after writes, or writes after reads, of whole 16 bytes a lane with no barrier of the wave
+    or the workgroup between them in the assembly's order."""
+    found, name, last = [], None, None
+    for line in asm.splitlines():
+        m = _FUNCTION.match(line)
+        if m and not line.startswith("."):
+            name, last = m.group(1), None
+        s = line.strip()
+        if s.startswith("; wave barrier") or s.startswith("s_barrier"):
+            last = None
+        elif s.startswith(("ds_write_b128", "ds_read_b128")):
+            kind = s.split()[0]
+            if last is not None and last != kind:
+                found.append((name, last, kind))
+            last = kind
+    return found
+
+
+def test_scanner_flags_an_unordered_exchange():
+    write, read, barrier = "\tds_write_b128 v1, v[2:5]\n", "\tds_read_b128 v[2:5], v1\n", "\t; wave barrier\n"
+    assert len(unordered_exchanges("k:\n" + write + read)) == 1
+    assert len(unordered_exchanges("k:\n" + write + barrier + read + write)) == 1
+    assert unordered_exchanges("k:\n" + write + write + barrier + read + read + barrier + write) == []
+    assert unordered_exchanges("k:\n" + write + "\ts_barrier\n" + read) == []
+
+
+@needs_hipcc
+def test_lanes_that_exchange_values_meet(tmp_path):
+    """The sums of a tile leave through LDS of the wave's own: written by some lanes, read by others, overwritten by the next."""
+    for src, asm in sources_asm(tmp_path).items():
+        if src in PRODUCTS:
+            assert "ds_write_b128" in asm and "ds_read_b128" in asm
+            found = unordered_exchanges(asm)
+            assert not found, (src, len(found), found[0])

@@ -88,6 +88,14 @@ __device__ __forceinline__ void wait_copies() {
 // This wave's LDS reads have arrived, then all waves meet. Copies stay on their way.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Between LDS accesses of one wave by which its lanes exchange values. The hardware keeps their order; this keeps the
+// compiler to it, which may otherwise move a lane's access past those of the other lanes that its own address rules out.
+__device__ __forceinline__ void lanes_meet() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)(p);
 }
@@ -427,12 +435,14 @@ __device__ __forceinline__ void drain(uint8_t* scratch, int m0, int n0, int wave
           }
         }
       }
+      lanes_meet();
 #pragma unroll
       for (int r = 0; r < 32; r += 64 / kLanes) {
         const int at = r + lane / kLanes, chunk = lane % kLanes;
         put(m0 + 32 * i + at, n0 + 32 * j0 + kEach * chunk,
             *reinterpret_cast<const u32x4*>(mine + at * 128 + ((chunk ^ (at & 7)) << 4)));
       }
+      lanes_meet();  // before the next fragments overwrite what other lanes read
     }
 }
 
