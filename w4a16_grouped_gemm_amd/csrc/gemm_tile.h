@@ -7,10 +7,12 @@
 // (global_load_lds_dwordx4) while the stage before it is multiplied. A copy
 // writes 64 x 16 bytes side by side in lane order, so where a 16-byte chunk
 // lies in LDS is chosen by which lane fetches it: the places are swizzled by
-// row so that the fragments' reads hit the banks evenly. What lies outside an
-// operand (the end of r, rows without a slot, columns past the last) is copied
-// from sixteen zero bytes, in both operands, so that it adds exactly nothing
-// whatever the other holds.
+// row so that the fragments' reads hit the banks evenly. Steps of r that add
+// nothing (past the operand's end; in the weights' gradient, rows without a slot)
+// are copied from sixteen zero bytes, in both operands, so that they add exactly
+// nothing whatever either holds. A row or column of C that is not there (past the
+// last; in the product, a row without a slot) is computed from another one's values
+// and left out or zeroed where C is stored.
 //
 // The second operand (n) is the instruction's first, so a lane's four
 // neighbouring results are four neighbouring columns of one row of C.
@@ -29,6 +31,7 @@ namespace tile {
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 64;  // steps of r a stage
+constexpr int kXcds = 8;   // workgroups go round-robin to them, each has an L2 of its own
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
@@ -46,8 +49,8 @@ __device__ __forceinline__ floatx16 mfma(vec8<f16_t> a, vec8<f16_t> b, floatx16 
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// What copies from outside an operand read: as long as a row of a tile.
-static __device__ __attribute__((aligned(16))) const uint32_t kZeros[128] = {};
+// What copies of steps that add nothing read.
+static __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {};
 
 // 16 bytes a lane to LDS at `lds` + 16 * lane. Issued from an asm block: the compiler would
 // count a builtin's copy as an LDS access and make every later LDS read wait for it. It
@@ -361,7 +364,9 @@ __device__ __forceinline__ void shared_loop(uint8_t* ring, int whole, int stages
   lds_barrier();
 }
 
-// The waves' shares, added in wave order; put(row, column, sums) gets four columns. sums: 32 kWaves MT NT KB of LDS.
+// The waves' shares, added in wave order; put(row, column, sums) gets four columns. ring: kSumsBytes of LDS.
+template <int MT, int NT>
+constexpr int kSumsBytes = kWaves * 32 * MT * 32 * NT * (int)sizeof(float);
 template <int MT, int NT, typename Put>
 __device__ __forceinline__ void shared_drain(uint8_t* ring, int wave, int lane, const floatx16 (&acc)[MT][NT], Put put) {
   constexpr int kRows = 32 * MT, kQuads = 8 * NT;
@@ -450,7 +455,6 @@ __device__ __forceinline__ void drain(uint8_t* scratch, int m0, int n0, int wave
 template <typename O>
 struct Line {
   static constexpr int kEach = 16 / (int)sizeof(O);
-  typedef O vec __attribute__((ext_vector_type(kEach)));
   static __device__ __forceinline__ void store(O* p, u32x4 v) {
     __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
   }

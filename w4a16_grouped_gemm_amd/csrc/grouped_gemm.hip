@@ -6,8 +6,9 @@
 // Weights and rows go from memory straight to LDS (global_load_lds) and from there to the mfma
 // instructions (gemm_tile.h). An expert's blocks lie side by side, so a tile takes as many of them as its rows
 // hold, whatever block_m is. Tiles are 256 x 256 where that fills the card: 128 flops a byte copied from L2,
-// and at half of that (128 x 128) the copies alone would take the time of the products. Tiles with at most half
-// of their rows used multiply half.
+// and at half of that (128 x 128) the copies alone would take the time of the products. Tiles whose blocks fill at most
+// half of their rows multiply half. Rows count by blocks here: a block's padding is multiplied as its real rows are,
+// also in a tile that a large block of few rows leaves without any.
 //
 // Measured (one MI355X, bf16): 32768 rows on 16 experts, 4096 x 7168: 1570..1670 us by card, 1.15..1.23 PFLOP/s, with
 // transposed weights 1560..1650; one expert of 8192 rows, 8192 x 8192: 804 us, 1.37. The clock is what gives: under
@@ -27,9 +28,8 @@ namespace {
 using namespace tile;
 
 // Tile (row tile, column tile) of this workgroup: row tiles go in groups of kTileGroup with all their columns,
-// row tiles innermost. Workgroups go round-robin to the 8 XCDs, each with an L2 of its own, so XCD x
-// takes the x-th run of 1 << log_run tiles of every 8 runs: about what its 32 compute units work on at once.
-constexpr int kXcds = 8;
+// row tiles innermost. XCD x takes the x-th run of 1 << log_run tiles of every 8 runs: about what its 32 compute
+// units work on at once.
 constexpr int kTileGroup = 8;
 constexpr int kLogRun = 5;
 __device__ __forceinline__ void tile_of(int ntiles, int log_run, int64_t& row_tile, int& column_tile) {
@@ -183,6 +183,7 @@ struct Way {
   static constexpr int kRows = 64 * MT, kTileN = 128 * NT;
   static constexpr int kRing = kRingBytes<RowPanel<kRows>, RowPanel<kTileN>, kAhead>;
   typedef Way<(MT + 1) / 2, NT, kAhead + (MT > 1)> Half;  // half the rows leave room for a stage more
+  static_assert(kRing >= kDrainBytes && kRing >= (int)sizeof(Scan), "the sums leave through the ring's place");
 };
 
 // Where the wave's copies of rows come from: row i of the tile, or row 0 where it has no slot (zeroed at the store).
@@ -260,6 +261,7 @@ __device__ __forceinline__ void product(const GroupedParams& p, uint8_t* ring, i
 template <typename T, typename O, bool TRANSPOSED, typename W>
 __global__ __launch_bounds__(kThreads, W::kRing > 80 * 1024 ? 2 : 4) void grouped_kernel(GroupedParams p, Cut c) {
   constexpr int kRows = W::kRows, kTileN = W::kTileN;
+  static_assert(W::MT == 1 || W::Half::kRing <= W::kRing, "both ways are in one ring");
   __shared__ __attribute__((aligned(16))) uint8_t ring[W::kRing];
   int64_t target;
   int nt;
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(kThreads) void narrow_kernel(GroupedParams p, Cut c
   constexpr int kRows = 32, kTileN = 32 * NT, kSteps = 128;
   typedef RowPanel<kRows, kSteps> M;
   typedef std::conditional_t<TRANSPOSED, ColumnPanel<kTileN, kSteps>, RowPanel<kTileN, kSteps>> N;
-  constexpr int kRing = kAhead * (M::kBytes + N::kBytes), kSums = kWaves * kRows * kTileN * 4;
+  constexpr int kRing = kAhead * (M::kBytes + N::kBytes), kSums = kSumsBytes<1, NT>;
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRing > kSums ? kRing : kSums];
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -383,8 +385,8 @@ hipError_t launch_narrow(const GroupedParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Which way, by the tiles that the call is expected to have. The counts are on the device, so an expert's rows are taken
-// as n_slots over E, their mean where every routed expert is resident; on a slice of the experts that counts
+// Which way, by the tiles that the call is expected to have without padding. The counts are on the device, so an
+// expert's rows are taken as n_slots over E, their mean where every routed expert is resident; on a slice of the experts that counts
 // the others' slots too, and larger tiles may be taken than the slice's rows fill. Results do not
 // depend on the way but for the order of their sums. Measured, us by (256 x 256, 128 x 128, 64 x 128, 32 x 64) tiles,
 // bf16, K last: one expert of 4096 rows, 4096 x 4096: 110, 141, 190, 351; 8 experts of 256, 2048 x 2048: 56, 33,

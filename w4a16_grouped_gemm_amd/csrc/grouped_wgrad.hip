@@ -23,8 +23,6 @@ namespace {
 
 using namespace tile;
 
-constexpr int kXcds = 8;
-
 // The tile of expert e of this workgroup: XCD x takes a contiguous eighth of each expert's
 // tiles, in groups of 8 rows of tiles.
 __device__ __forceinline__ bool tile_of(int mtiles, int ntiles, int& e, int& mt, int& nt) {
@@ -98,6 +96,7 @@ __global__ __launch_bounds__(kThreads) void narrow_wgrad_kernel(WgradParams p, i
   typedef ColumnPanel<kTile, kSteps> Panel;
   static_assert(Panel::kMine == 2, "two copies of eight rows a wave and panel");
   __shared__ __attribute__((aligned(16))) uint8_t ring[kAhead * 2 * Panel::kBytes];
+  static_assert(sizeof(ring) >= kSumsBytes<2, 2>, "the waves' shares take the ring's place");
   __shared__ int32_t table[kTable];  // of kTable rows: the row of a, or -1 where the row adds nothing
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -157,6 +156,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p, int m
   constexpr int kMine = Panel::kMine;
   static_assert(kMine * kRows == 8, "eight rows a wave");
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes<Panel, Panel, kAhead>];
+  static_assert(sizeof(ring) >= kDrainBytes, "the sums leave through the ring's place");
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   int e, mt, nt;
