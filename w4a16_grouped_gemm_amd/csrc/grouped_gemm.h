@@ -34,6 +34,11 @@ struct GroupedParams {
   int32_t transposed;
   int32_t far;            // token rows that 32 bits of bytes do not reach
 };
+// The tile that a call goes by, a rule on sizes alone; n_slots at least 1.
+struct GroupedTile {
+  int32_t rows, columns;
+};
+GroupedTile grouped_tile(int32_t E, int32_t N, int32_t n_slots, bool transposed);
 hipError_t launch_grouped_gemm(const GroupedParams& p, int32_t dtype, int32_t out_dtype, hipStream_t stream);
 
 // How the weights' gradient is cut, a rule on sizes alone: tiles of tile x tile values, and how many workgroups share an

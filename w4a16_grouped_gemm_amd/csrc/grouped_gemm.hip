@@ -385,29 +385,16 @@ hipError_t launch_narrow(const GroupedParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Which way, by the tiles that the call is expected to have without padding. The counts are on the device, so an
-// expert's rows are taken as n_slots over E, their mean where every routed expert is resident; on a slice of the experts that counts
-// the others' slots too, and larger tiles may be taken than the slice's rows fill. Results do not
-// depend on the way but for the order of their sums. Measured, us by (256 x 256, 128 x 128, 64 x 128, 32 x 64) tiles,
-// bf16, K last: one expert of 4096 rows, 4096 x 4096: 110, 141, 190, 351; 8 experts of 256, 2048 x 2048: 56, 33,
-// 40, 59; 48 of 85, 7168 x 2048: 320, 374, 435, 899; one of 512 rows, 2048 x 2048: 44, 21, 19, 12.5; 10 of 100, 1384 x 1000
-// transposed: 24, 15.7, 17.3, 22; 384 of 11, 512 x 7168: 489, 475, 475, 477, and 7168 x 512 transposed: 689, 634, 619, 821;
-// 48 of 3 (384 routed), 4096 x 7168: 464, 463, 464, 451, and 7168 x 4096 transposed 509, 483, 481, 498; 8 experts of one
-// row, 512 x 7168: 79, 42, 42, 19, and by 32 x 32 tiles 10.5 (of 512 rows above: 20).
 template <typename T, typename O, bool TRANSPOSED>
 hipError_t launch(const GroupedParams& p, hipStream_t stream) {
-  const int64_t experts = std::min(p.E, p.n_slots), rows = (p.n_slots + experts - 1) / experts;
-  auto tiles = [&](int64_t r, int64_t columns) {
-    return experts * ((rows + r / 2 - 1) / r + (rows <= r / 2)) * ((p.N + columns - 1) / columns);
-  };
-  if (rows <= 48) {  // an expert's rows are one tile or two: what counts is the weights' stream
-    if (TRANSPOSED && tiles(64, 128) >= 64) return launch_tiles<T, O, TRANSPOSED, Way<1, 1, 3>>(p, stream);
+  const GroupedTile tile = grouped_tile(p.E, p.N, p.n_slots, TRANSPOSED);
+  if (tile.rows == 256) return launch_tiles<T, O, TRANSPOSED, Way<4, 2, 2>>(p, stream);
+  if (tile.rows == 128) return launch_tiles<T, O, TRANSPOSED, Way<2, 1, 2>>(p, stream);
+  if constexpr (TRANSPOSED) {
+    if (tile.rows == 64) return launch_tiles<T, O, true, Way<1, 1, 3>>(p, stream);
   } else {
-    if (tiles(256, 256) >= 112 && p.N > 128) return launch_tiles<T, O, TRANSPOSED, Way<4, 2, 2>>(p, stream);
-    if (tiles(128, 128) >= 96) return launch_tiles<T, O, TRANSPOSED, Way<2, 1, 2>>(p, stream);
+    if (tile.columns == 32) return launch_narrow<T, O, false, 1, 7>(p, stream);
   }
-  // fewer workgroups than compute units: stages ahead for each instead (16 rows, 2048 x 8192: five 21.5 us, seven 17.3)
-  if (!TRANSPOSED && tiles(32, 64) < 128) return launch_narrow<T, O, TRANSPOSED, 1, 7>(p, stream);
   return launch_narrow<T, O, TRANSPOSED, 2, 3>(p, stream);
 }
 
@@ -417,6 +404,31 @@ hipError_t launch(const GroupedParams& p, hipStream_t stream) {
 }
 
 }  // namespace
+
+// Which way, by the tiles that the call is expected to have without padding. The counts are on the device, so an
+// expert's rows are taken as n_slots over E, their mean where every routed expert is resident; on a slice of the experts that counts
+// the others' slots too, and larger tiles may be taken than the slice's rows fill. Results do not
+// depend on the way but for the order of their sums. Measured, us by (256 x 256, 128 x 128, 64 x 128, 32 x 64) tiles,
+// bf16, K last: one expert of 4096 rows, 4096 x 4096: 110, 141, 190, 351; 8 experts of 256, 2048 x 2048: 56, 33,
+// 40, 59; 48 of 85, 7168 x 2048: 320, 374, 435, 899; one of 512 rows, 2048 x 2048: 44, 21, 19, 12.5; 10 of 100, 1384 x 1000
+// transposed: 24, 15.7, 17.3, 22; 384 of 11, 512 x 7168: 489, 475, 475, 477, and 7168 x 512 transposed: 689, 634, 619, 821;
+// 48 of 3 (384 routed), 4096 x 7168: 464, 463, 464, 451, and 7168 x 4096 transposed 509, 483, 481, 498; 8 experts of one
+// row, 512 x 7168: 79, 42, 42, 19, and by 32 x 32 tiles 10.5 (of 512 rows above: 20).
+GroupedTile grouped_tile(int32_t E, int32_t N, int32_t n_slots, bool transposed) {
+  const int64_t experts = std::min(E, n_slots), rows = (n_slots + experts - 1) / experts;
+  auto tiles = [&](int64_t r, int64_t columns) {
+    return experts * ((rows + r / 2 - 1) / r + (rows <= r / 2)) * ((N + columns - 1) / columns);
+  };
+  if (rows <= 48) {  // an expert's rows are one tile or two: what counts is the weights' stream
+    if (transposed && tiles(64, 128) >= 64) return {64, 128};
+  } else {
+    if (tiles(256, 256) >= 112 && N > 128) return {256, 256};
+    if (tiles(128, 128) >= 96) return {128, 128};
+  }
+  // fewer workgroups than compute units: stages ahead for each instead (16 rows, 2048 x 8192: five 21.5 us, seven 17.3)
+  if (!transposed && tiles(32, 64) < 128) return {32, 32};
+  return {32, 64};
+}
 
 hipError_t launch_grouped_gemm(const GroupedParams& p, int32_t dtype, int32_t out_dtype, hipStream_t stream) {
   if (p.capacity < p.block_m) return hipSuccess;  // no whole block
