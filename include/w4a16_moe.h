@@ -586,8 +586,8 @@ int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q
  * or with `transposed` the same with w[e, k, n]: given the forward product's own weights
  * [E, N', K'] and the gradient of its outputs as a, that is the gradient of its rows
  * (N = K', K = N'; where the forward call gathered, moe_permute_backward then
- * sums the rows of a token). Products are exact, sums in fp32 (values below fp32's
- * normal numbers may count as zero), one rounding to out_dtype. Padding rows
+ * sums the rows of a token). Products are exact, sums in fp32 down to its smallest
+ * value, 2^-149, one rounding to out_dtype. Padding rows
  * p < num_tokens_post_padded, and rows of a block whose expert id lies outside
  * [0, num_experts), are written as zeros, whatever a holds there; later rows are left
  * as they were. Infinities and NaN enter the outputs whose sums they are in.
@@ -596,7 +596,8 @@ int mxfp4_moe_gemm(int32_t num_experts, int32_t N, int32_t K, const uint8_t* a_q
  *   a                  device [a_rows, K] of `dtype` (bf16 or fp16; fp32 is
  *                      W4A16_ERR_UNSUPPORTED); with gather a_rows >= T (token rows), without
  *                      a_rows >= capacity (aligned rows); else W4A16_ERR_INVALID_ARG
- *   T, topk            tokens and slots per token of the alignment
+ *   T, topk            tokens and slots per token of the alignment; with T = 0 nothing is read or
+ *                      written (the alignment of no token has no row)
  *   sorted_token_ids, capacity, expert_ids, num_tokens_post_padded, block_m
  *                      moe_align's outputs and block size; rows of a block that does not
  *                      lie below capacity as a whole are not touched. capacity / block_m

@@ -140,6 +140,27 @@ def test_values_below_the_types_normal_numbers(case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sizes", [(-70, -60), (-133, 10), (10, -133), (-133, -10)], ids=str)
+@pytest.mark.parametrize("case", [PRODUCTS[0], PRODUCTS[2], PRODUCTS[5], PRODUCTS[6]], ids=str)
+def test_sums_below_fp32s_normal_numbers(case, sizes):
+    """bf16 values of which either or the products lie below 2^-126, the products multiples of 2^-143 and their sums below 2^24
+    of those: fp32 values, so the outputs are exact."""
+    (T, topk, E, N, K, bm), *_ = case
+    rows, columns = 2.0 ** sizes[0], 2.0 ** sizes[1]
+    g = torch.Generator().manual_seed(82)
+    r = Routing(T, topk, E, E, bm, seed=83)
+    a, dout = whole(g, T, K).double() * rows, whole(g, r.capacity, N).double() * rows
+    weights, dout2 = whole(g, E, N, K).double() * columns, whole(g, r.capacity, N).double() * columns
+    a16, w16, d16 = (x.bfloat16().cuda() for x in (a, weights, dout))
+    out = run(r, a16, w16, torch.float32, True, False)
+    assert torch.equal(out[: r.rows].cpu().double(), product(r, a, weights, True, False)[0])
+    out = run(r, d16, w16, torch.float32, False, True)
+    assert torch.equal(out[: r.rows].cpu().double(), product(r, dout, weights, False, True)[0])
+    dw = run_wgrad(r, dout2.bfloat16().cuda(), a16, E, torch.float32, True)
+    assert torch.equal(dw.cpu().double(), weight_gradient(r, dout2, a, E, True)[0])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("case", PRODUCTS[:4], ids=str)
 def test_infinities_stay_in_their_sums(case):
     (T, topk, E, N, K, bm), *_ = case

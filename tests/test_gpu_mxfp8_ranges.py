@@ -105,3 +105,23 @@ def test_not_finite_beside_far_gates(dtype):
     assert bool(dgu[1:4, :32].isnan().all()) and bool(again[1:5].isnan().all()) and bool(dgu[4, :32].isnan().all())
     assert dgu[5, 31] == -inf and dgu[5, 63] == -inf
     assert bool(torch.isfinite(dgu[0]).all()) and bool(torch.isfinite(dgu[5, :31]).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_far_neighbours_change_no_bits(dtype):
+    """A wave goes by mantissas and exponents where one of its factors is far: rows of ordinary values have the same bits beside
+    far rows as without them. 32 columns: a wave holds sixteen rows."""
+    g = torch.Generator().manual_seed(62)
+    t = TYPES[dtype]
+    rows, I = 512, 32
+    gu = (torch.randn(rows, 2 * I, generator=g) * torch.exp2(torch.randn(rows, 1, generator=g))).clamp(-30, 30).to(t)
+    dh = torch.randn(rows, I, generator=g).to(t)
+    alone = run(gu, dh)
+    mixed_gu, mixed_dh = gu.clone(), dh.clone()
+    mixed_gu[::7, 3], mixed_gu[::7, 5] = -200.0, 300.0
+    if dtype != "fp16":
+        mixed_dh[::11, 9] = 2.0**90
+    mixed = run(mixed_gu, mixed_dh)
+    same = (torch.arange(rows) % 7 != 0) & (torch.arange(rows) % 11 != 0)
+    for a, b in zip(alone, mixed):
+        assert torch.equal(a[same], b[same])
