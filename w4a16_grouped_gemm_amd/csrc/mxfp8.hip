@@ -93,25 +93,24 @@ __device__ __forceinline__ float reciprocal(float d) {
   return __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
 }
 
-// 1 / (1 + exp(-g)), as sig * 2^power, and 1 less that, neither by a difference: with t = exp(-|g|) they are
-// 1 / (1 + t) and t / (1 + t). t = 2^(-|g| log2 e) is 2^whole times m = 2^part, the part with the product's rounding
-// error and the constant's put back, so that m holds to a few units in the last place at any g.
-// FAR: any g. t leaves fp32's numbers at |g| = 87, and products with it come back into them where the other factors are
-// large. From |g| = 400 on t is zero: below 2^-577, no product of a gate and two more fp32 values with it rounds to
+// 1 / (1 + exp(-g)), as sig * 2^power, and 1 less that, neither by a difference. exp(-g) is 2^whole times m = 2^part, the
+// part with the product's rounding error and the constant's put back, so that m holds to a few units in the last place
+// at any g; where whole is positive, both terms of the sum are taken 2^-whole times.
+// FAR: any g. exp(g) leaves fp32's numbers at g = -87, and products with it come back into them where the other factors
+// are large. Below -400 it counts as zero: under 2^-577, no product of a gate and two more fp32 values with it rounds to
 // anything else. Else |g| is up to 87, and power is 0.
 template <bool FAR>
 __device__ __forceinline__ void sigmoid(float g, float& sig, int& power, float& rest) {
-  const float x = FAR ? fmaxf(-fabsf(g), -400.f) : -fabsf(g);
+  const float x = FAR ? __builtin_amdgcn_fmed3f(-g, -400.f, 400.f) : -g;
   const float whole = __builtin_rintf(x * kLog2E);
   const float part = __builtin_fmaf(x, kLog2ELow, __builtin_fmaf(x, kLog2E, -whole));  // within 0.51: good to 2^-25
-  float m = __builtin_amdgcn_exp2f(part);
-  if (FAR) m = x > -400.f ? m : 0.f;
-  const float t = __builtin_amdgcn_ldexpf(m, (int)whole);
-  const float inverse = reciprocal(1.f + t);
-  const float small = t * inverse;
-  sig = g < 0.f ? (FAR ? m * inverse : small) : inverse;
-  power = FAR && g < 0.f ? (int)whole : 0;
-  rest = g < 0.f ? inverse : small;
+  const float m = __builtin_amdgcn_exp2f(part);
+  const int down = max((int)whole, 0);
+  const float over = __builtin_amdgcn_ldexpf(m, (int)whole - down);
+  const float inverse = reciprocal(__builtin_amdgcn_ldexpf(1.f, -down) + over);
+  sig = !FAR ? __builtin_amdgcn_ldexpf(inverse, -down) : x < 400.f ? inverse : 0.f;
+  power = FAR ? -down : 0;
+  rest = over * inverse;
 }
 
 // x = mantissa * 2^power. FAR: the mantissa in [0.5, 1), so that the only step that can leave fp32's numbers is the
@@ -145,7 +144,7 @@ __device__ __forceinline__ void gradient(float gate, float up, float dh, float& 
   int power;
   sigmoid<FAR>(gate, sig, power, rest);
   const Parts g = parts<FAR>(gate), u = parts<FAR>(up), d = parts<FAR>(dh);
-  const float silu = g.mantissa * sig, slope = sig * __builtin_fmaf(gate, rest, 1.f);
+  const float silu = g.mantissa * sig, slope = __builtin_fmaf(gate * sig, rest, sig);
   dgate = times_power<FAR>(d.mantissa * u.mantissa * slope, d.power + u.power + power);
   dup = times_power<FAR>(d.mantissa * silu, d.power + g.power + power);
   h = times_power<FAR>(silu * u.mantissa, g.power + u.power + power);
