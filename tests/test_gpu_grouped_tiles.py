@@ -3,6 +3,7 @@
 Which tile a call goes by is a rule on its sizes; each test says which it is there for, and the rule is asked. Inputs of
 small whole numbers make every sum an fp32 value, so an output is the 64-bit result rounded once, bit for bit."""
 import ctypes
+import os
 
 import pytest
 import torch
@@ -11,6 +12,14 @@ import w4a16_grouped_gemm_amd as w
 from _gpu import say
 from _grouped import TYPES, Routing, product, weight_gradient
 from test_gpu_grouped_gemm import POISON, run, run_wgrad, whole
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    if not os.path.exists(w.LIB_PATH):
+        from w4a16_grouped_gemm_amd import build
+
+        build.build()
 
 
 class Pair(ctypes.Structure):

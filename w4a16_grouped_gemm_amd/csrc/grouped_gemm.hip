@@ -10,8 +10,8 @@
 // half of their rows multiply half. Rows count by blocks here: a block's padding is multiplied as its real rows are,
 // also in a tile that a large block of few rows leaves without any.
 //
-// Measured (one MI355X, bf16): 32768 rows on 16 experts, 4096 x 7168: 1570..1670 us by card, 1.15..1.23 PFLOP/s, with
-// transposed weights 1560..1650; one expert of 8192 rows, 8192 x 8192: 804 us, 1.37. The clock is what gives: under
+// Measured (one MI355X, bf16): 32768 rows on 16 experts, 4096 x 7168: 1560..1670 us by card, 1.15..1.23 PFLOP/s, with
+// transposed weights 1550..1680; one expert of 8192 rows, 8192 x 8192: 804 us, 1.37. The clock is what gives: under
 // this load it falls to 1.6 GHz of 2.4 (a timing build without copies, on LDS that stays as it is, keeps 2.4). 48 experts
 // of 85 rows, 7168 x 2048: 320..340 us, 4.6 TB/s; of three rows, 4096 x 7168: 420..450 us, 6.1 TB/s (reads
 // alone reach 6.9); one token on 8 of 64 experts, 512 x 7168: 12.3 us, 4.8 TB/s.

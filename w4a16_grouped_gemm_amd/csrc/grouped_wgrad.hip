@@ -7,7 +7,8 @@
 // are column panels: the rows are the steps of the sum. Rows without a slot, whatever they
 // hold, are replaced by zeros as they are copied to LDS (global_load_lds); the mfma loop is in gemm_tile.h.
 //
-// Measured (one MI355X): 32768 rows, 16 experts, 4096 x 7168: 1690..1770 us, to fp32 50 more, 1.1 PFLOP/s; 131072 rows
+// Measured (one MI355X): 32768 rows, 16 experts, 4096 x 7168: aligned rows to bf16 1620..1770 us by card, gathered ones to
+// fp32 1740..1880, 1.02..1.18 PFLOP/s; 131072 rows
 // 6130..6290 us, 1.25. Bound as the product by the clock that the load leaves, and by a tile's start and its
 // store, 128 or 256 KB, which take as long as four or five of its 32 stages. 4 experts of 1388 rows, 264 x 712: 14.7
 // us, a chain of a dozen dependent steps.

@@ -9,7 +9,7 @@
 //
 // All of it is bound by memory: each value is read and written once, in streams of 8 or 16 bytes a lane.
 // Measured (one MI355X, bf16): 16384 rows of 7168 quantised in 56 us and back in 57 (6.3 TB/s; reads alone reach
-// 6.9, a copy 4.9); the activation of 32768 rows of 2 x 2048 88 us (6.1 TB/s), its gradient 104 (6.5 TB/s), 98 and 119
+// 6.9, a copy 4.9); the activation of 32768 rows of 2 x 2048 89 us (6.1 TB/s), its gradient 106 (6.3 TB/s), 98 and 120
 // where every wave has a gate so far out that the products go by mantissas and exponents; a few rows 3 us, a
 // launch's own time.
 #include "row_ops.h"
